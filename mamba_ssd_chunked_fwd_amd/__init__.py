@@ -1,6 +1,7 @@
 """Mamba-2 SSD chunked forward on AMD Instinct MI355X (gfx950).
 
-A thin Python binding over libssd's C ABI (``include/ssd.h``).  Every step of
+A thin Python binding over libssd's C ABI (``include/ssd.h`` and
+``include/ssd_block.h``).  Every step of
 the computation runs in the library's HIP kernels; this module only checks
 tensor shapes/dtypes, builds the dims struct and passes device pointers and
 the current HIP stream.  PyTorch supplies device memory and streams.
@@ -8,8 +9,12 @@ the current HIP stream.  PyTorch supplies device memory and streams.
 Entry points (same names as the C ABI):
   ssd_chunk_cumsum, ssd_fwd_pass_state, ssd_chunk_state, ssd_state_passing,
   ssd_compute_out, ssd_state_and_out, ssd_forward, ssd_forward_noalloc,
-  ssd_decode_step, ssd_causal_conv1d, ssd_gdn_chunk_fwd_h, ssd_gdn_chunk_fwd_o
-and the allocating convenience wrapper ``forward``.
+  ssd_decode_step, ssd_causal_conv1d, ssd_gdn_chunk_fwd_h, ssd_gdn_chunk_fwd_o,
+  ssd_linattn_fwd, ssd_linattn_bwd, ssd_linattn_step, ssd_add_norm_fwd,
+  ssd_add_norm_bwd, ssd_gated_norm_fwd, ssd_gated_norm_bwd
+and the allocating convenience wrappers ``forward``, ``linattn``,
+``linattn_backward``, ``add_norm``, ``add_norm_backward``, ``gated_norm`` and
+``gated_norm_backward``.
 
 Importing fails loudly (ImportError) when libssd.so has not been built:
 there is no fallback implementation.
@@ -26,6 +31,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssd.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ssd.h")
+BLOCK_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ssd_block.h")
 
 SSD_OK = 0
 SSD_ERR_INVALID_ARGUMENT = 1
@@ -34,6 +40,7 @@ SSD_ERR_WORKSPACE = 3
 SSD_ERR_HIP = 4
 SSD_F32 = 0
 SSD_BF16 = 1
+SSD_GATES = {"silu": 0, "sigmoid": 1}
 
 
 class SsdDims(ctypes.Structure):
@@ -47,6 +54,17 @@ class GdnDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("nheads", ctypes.c_int64), ("dk", ctypes.c_int64),
                 ("dv", ctypes.c_int64), ("chunk_size", ctypes.c_int64)]
+
+
+class LinattnDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("nseq", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64)]
+
+
+class GatedNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("group", ctypes.c_int64), ("weight_dim", ctypes.c_int64)]
 
 
 class SsdError(RuntimeError):
@@ -93,6 +111,30 @@ def _load() -> ctypes.CDLL:
     lib.ssd_gdn_chunk_fwd_o.restype = i
     lib.ssd_causal_conv1d.argtypes = [vp] * 4 + [i64] * 4 + [i, i, vp]
     lib.ssd_causal_conv1d.restype = i
+    f = ctypes.c_float
+    ldims = ctypes.POINTER(LinattnDims)
+    for name in ("ssd_linattn_fwd_workspace_bytes", "ssd_linattn_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [ldims, i]
+        getattr(lib, name).restype = sz
+    lib.ssd_linattn_fwd.argtypes = [vp] * 9 + [sz, f, i, ldims, vp]
+    lib.ssd_linattn_fwd.restype = i
+    lib.ssd_linattn_bwd.argtypes = [vp] * 13 + [sz, f, i, ldims, vp]
+    lib.ssd_linattn_bwd.restype = i
+    lib.ssd_linattn_step.argtypes = [vp] * 6 + [f, i, ldims, vp]
+    lib.ssd_linattn_step.restype = i
+    lib.ssd_add_norm_fwd.argtypes = [vp] * 6 + [i64, i64, f, i, i, vp]
+    lib.ssd_add_norm_fwd.restype = i
+    lib.ssd_add_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+    lib.ssd_add_norm_bwd_workspace_bytes.restype = sz
+    lib.ssd_add_norm_bwd.argtypes = [vp] * 11 + [sz, i64, i64, f, i, i, vp]
+    lib.ssd_add_norm_bwd.restype = i
+    ndims = ctypes.POINTER(GatedNormDims)
+    lib.ssd_gated_norm_fwd.argtypes = [vp] * 4 + [f, i, i, i, i, ndims, vp]
+    lib.ssd_gated_norm_fwd.restype = i
+    lib.ssd_gated_norm_bwd_workspace_bytes.argtypes = [ndims]
+    lib.ssd_gated_norm_bwd_workspace_bytes.restype = sz
+    lib.ssd_gated_norm_bwd.argtypes = [vp] * 8 + [sz, f, i, i, i, i, ndims, vp]
+    lib.ssd_gated_norm_bwd.restype = i
     return lib
 
 
@@ -104,9 +146,9 @@ def library() -> ctypes.CDLL:
     return _lib
 
 
-def header_functions() -> list:
-    """Names of the functions include/ssd.h declares."""
-    text = open(HEADER_PATH).read()
+def header_functions(path: str = HEADER_PATH) -> list:
+    """Names of the functions a header (by default include/ssd.h) declares."""
+    text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"^\s*(?:const\s+)?[A-Za-z_][A-Za-z0-9_]*\s*\*?\s*"
                       r"(ssd_[a-z0-9_]+)\s*\(", text, flags=re.M)
@@ -500,6 +542,270 @@ def ssd_causal_conv1d(x: torch.Tensor, weight: torch.Tensor,
         "ssd_causal_conv1d")
 
 
+# --------------------------------------------------------- block operators
+_FLOATS = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
+
+
+def _call(where: str, dev: torch.device, *args) -> None:
+    """The entry point on the current stream of ``dev``, which need not be the
+    current device."""
+    f = getattr(_lib, where)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(dev))
+    _raise(st, where)
+
+
+def _linattn_check(q, k, v, log_decay, init_state, cu_seqlens) -> LinattnDims:
+    """The dims of a linear attention call, its inputs checked."""
+    for t, name in ((q, "q"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a tensor [batch, seqlen, heads, size]")
+    b, L, G, K = q.shape
+    H, V = v.shape[2:]
+    dev = q.device
+    _check(q, "q", None, _FLOATS)
+    _check(k, "k", (b, L, G, K), (q.dtype,), dev)
+    _check(v, "v", (b, L, H, V), (q.dtype,), dev)
+    _check(log_decay, "log_decay", (H,), _F32, dev)
+    nseq = b
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 \
+                or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a tensor [sequences + 1]")
+        if b != 1:
+            raise ValueError(f"packed sequences need a batch of 1, not {b}")
+        _check(cu_seqlens, "cu_seqlens", None, (torch.int32,), dev)
+        nseq = cu_seqlens.numel() - 1
+    _check(init_state, "init_state", (nseq, H, K, V), _F32, dev, optional=True)
+    return LinattnDims(b * L, nseq, H, G, K, V)
+
+
+def linattn_workspace_bytes(d: LinattnDims, dtype: torch.dtype, backward: bool = False) -> int:
+    f = (_lib.ssd_linattn_bwd_workspace_bytes if backward
+         else _lib.ssd_linattn_fwd_workspace_bytes)
+    return int(f(ctypes.byref(d), _dtype_code(dtype)))
+
+
+def _scale(scale: Optional[float], K: int):
+    return ctypes.c_float(K ** -0.5 if scale is None else scale)
+
+
+def ssd_linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    log_decay: torch.Tensor, init_state: Optional[torch.Tensor],
+                    cu_seqlens: Optional[torch.Tensor], o: torch.Tensor,
+                    final_state: Optional[torch.Tensor], workspace: torch.Tensor,
+                    scale: Optional[float] = None) -> None:
+    """Linear attention with a decay for each head: S_t = exp(log_decay) S_{t-1}
+    + k_t v_t^T, o_t = scale q_t^T S_t.  q, k [b, L, G, K], v and o
+    [b, L, H, V] (fp32 or bf16; H a multiple of G), log_decay [H] fp32; states
+    [sequences, H, K, V] fp32 or None.  With cu_seqlens [sequences + 1] int32
+    the sequences are packed in a batch of 1; else each batch row is one.
+    ``workspace`` has linattn_workspace_bytes(dims, dtype) bytes.  scale None:
+    K^-0.5."""
+    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
+    dev = q.device
+    _check(o, "o", tuple(v.shape), (q.dtype,), dev)
+    _check(final_state, "final_state", (d.nseq, d.nheads, d.dk, d.dv), _F32, dev, optional=True)
+    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
+    nbytes = workspace.numel() * workspace.element_size()
+    _call("ssd_linattn_fwd", dev,
+          _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(init_state), _ptr(cu_seqlens),
+          _ptr(o), _ptr(final_state), _ptr(workspace), nbytes, _scale(scale, d.dk),
+          _dtype_code(q.dtype), ctypes.byref(d))
+
+
+def ssd_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    log_decay: torch.Tensor, init_state: Optional[torch.Tensor],
+                    cu_seqlens: Optional[torch.Tensor], dout: torch.Tensor,
+                    dfinal: Optional[torch.Tensor], dq: torch.Tensor, dk: torch.Tensor,
+                    dv: torch.Tensor, dinit: Optional[torch.Tensor],
+                    workspace: torch.Tensor, scale: Optional[float] = None) -> None:
+    """Gradients of ``ssd_linattn_fwd`` for dout [b, L, H, V] and dfinal (or
+    None) into dq, dk, dv and dinit (or None).  log_decay has none."""
+    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
+    dev = q.device
+    own = (q.dtype,)
+    state = (d.nseq, d.nheads, d.dk, d.dv)
+    _check(dout, "dout", tuple(v.shape), own, dev)
+    _check(dfinal, "dfinal", state, _F32, dev, optional=True)
+    _check(dq, "dq", tuple(q.shape), own, dev)
+    _check(dk, "dk", tuple(q.shape), own, dev)
+    _check(dv, "dv", tuple(v.shape), own, dev)
+    _check(dinit, "dinit", state, _F32, dev, optional=True)
+    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
+    nbytes = workspace.numel() * workspace.element_size()
+    _call("ssd_linattn_bwd", dev,
+          _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(init_state), _ptr(cu_seqlens),
+          _ptr(dout), _ptr(dfinal), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dinit), _ptr(workspace),
+          nbytes, _scale(scale, d.dk), _dtype_code(q.dtype), ctypes.byref(d))
+
+
+def ssd_linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: torch.Tensor, state: torch.Tensor, o: torch.Tensor,
+                     scale: Optional[float] = None) -> None:
+    """One token of linear attention for every sequence: ``state`` [b, H, K, V]
+    fp32 is updated in place and ``o`` [b, H, V] written.  q, k [b, G, K],
+    v [b, H, V]."""
+    for t, name in ((q, "q"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be a tensor [batch, heads, size]")
+    b, G, K = q.shape
+    H, V = v.shape[1:]
+    dev = q.device
+    _check(q, "q", None, _FLOATS)
+    _check(k, "k", (b, G, K), (q.dtype,), dev)
+    _check(v, "v", (b, H, V), (q.dtype,), dev)
+    _check(log_decay, "log_decay", (H,), _F32, dev)
+    _check(state, "state", (b, H, K, V), _F32, dev)
+    _check(o, "o", (b, H, V), (q.dtype,), dev)
+    d = LinattnDims(b, b, H, G, K, V)
+    _call("ssd_linattn_step", dev,
+          _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o), _scale(scale, K),
+          _dtype_code(q.dtype), ctypes.byref(d))
+
+
+def _rows(x: torch.Tensor, name: str) -> Tuple[int, int]:
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError(f"{name} must be a tensor [..., dim]")
+    D = x.shape[-1]
+    return (x.numel() // D if D else 0), D
+
+
+def ssd_add_norm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor],
+                     res_scale: Optional[torch.Tensor], weight: Optional[torch.Tensor],
+                     y: torch.Tensor, residual_out: Optional[torch.Tensor],
+                     eps: float = 1e-5) -> None:
+    """h = residual + res_scale o x; residual_out = h; y = RMS norm of h, times
+    weight.  x and y [..., dim] in one type, residual and residual_out in
+    one (fp32 or bf16 each); res_scale and weight [dim] fp32.  residual,
+    res_scale, weight and residual_out may be None."""
+    rows, D = _rows(x, "x")
+    dev = x.device
+    shape = tuple(x.shape)
+    _check(x, "x", None, _FLOATS)
+    _check(residual, "residual", shape, _FLOATS, dev, optional=True)
+    _check(res_scale, "res_scale", (D,), _F32, dev, optional=True)
+    _check(weight, "weight", (D,), _F32, dev, optional=True)
+    _check(y, "y", shape, (x.dtype,), dev)
+    rdt = residual.dtype if residual is not None else None
+    _check(residual_out, "residual_out", shape, _FLOATS if rdt is None else (rdt,), dev,
+           optional=True)
+    if rdt is None:
+        rdt = x.dtype if residual_out is None else residual_out.dtype
+    _call("ssd_add_norm_fwd", dev,
+          _ptr(x), _ptr(residual), _ptr(res_scale), _ptr(weight), _ptr(y), _ptr(residual_out),
+          rows, D, eps, _dtype_code(x.dtype), _dtype_code(rdt))
+
+
+def ssd_add_norm_bwd(x: torch.Tensor, residual: Optional[torch.Tensor],
+                     res_scale: Optional[torch.Tensor], weight: Optional[torch.Tensor],
+                     dy: torch.Tensor, dresidual_out: Optional[torch.Tensor],
+                     dx: torch.Tensor, dresidual: Optional[torch.Tensor],
+                     dres_scale: Optional[torch.Tensor], dweight: Optional[torch.Tensor],
+                     workspace: torch.Tensor, eps: float = 1e-5) -> None:
+    """Gradients of ``ssd_add_norm_fwd`` from its inputs.  ``workspace`` has
+    add_norm_workspace_bytes(rows, dim) bytes."""
+    rows, D = _rows(x, "x")
+    dev = x.device
+    shape = tuple(x.shape)
+    _check(x, "x", None, _FLOATS)
+    _check(residual, "residual", shape, _FLOATS, dev, optional=True)
+    _check(res_scale, "res_scale", (D,), _F32, dev, optional=True)
+    _check(weight, "weight", (D,), _F32, dev, optional=True)
+    _check(dy, "dy", shape, (x.dtype,), dev)
+    rdts = _FLOATS if residual is None else (residual.dtype,)
+    _check(dresidual_out, "dresidual_out", shape, rdts, dev, optional=True)
+    _check(dx, "dx", shape, (x.dtype,), dev)
+    _check(dresidual, "dresidual", shape, rdts, dev, optional=True)
+    _check(dres_scale, "dres_scale", (D,), _F32, dev, optional=True)
+    _check(dweight, "dweight", (D,), _F32, dev, optional=True)
+    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
+    rdt = next((t.dtype for t in (residual, dresidual_out) if t is not None), x.dtype)
+    nbytes = workspace.numel() * workspace.element_size()
+    _call("ssd_add_norm_bwd", dev,
+          _ptr(x), _ptr(residual), _ptr(res_scale), _ptr(weight), _ptr(dy), _ptr(dresidual_out),
+          _ptr(dx), _ptr(dresidual), _ptr(dres_scale), _ptr(dweight), _ptr(workspace), nbytes,
+          rows, D, eps, _dtype_code(x.dtype), _dtype_code(rdt))
+
+
+def add_norm_workspace_bytes(rows: int, dim: int) -> int:
+    return int(_lib.ssd_add_norm_bwd_workspace_bytes(rows, dim))
+
+
+def _gate(gate: str) -> int:
+    if gate not in SSD_GATES:
+        raise ValueError(f"gate must be one of {sorted(SSD_GATES)}, not {gate!r}")
+    return SSD_GATES[gate]
+
+
+def _gated_check(x, z, weight, group) -> GatedNormDims:
+    rows, D = _rows(x, "x")
+    dev = x.device
+    group = D if group is None else int(group)
+    _check(x, "x", None, _FLOATS)
+    _check(z, "z", tuple(x.shape), _FLOATS, dev, optional=True)
+    wdim = D
+    if weight is not None:
+        if not isinstance(weight, torch.Tensor) or weight.dim() != 1 \
+                or weight.numel() not in (D, group):
+            raise ValueError(f"weight must be a tensor [{D}] or [{group}]")
+        _check(weight, "weight", None, _F32, dev)
+        wdim = weight.numel()
+    return GatedNormDims(rows, D, group, wdim)
+
+
+def ssd_gated_norm_fwd(x: torch.Tensor, z: Optional[torch.Tensor],
+                       weight: Optional[torch.Tensor], y: torch.Tensor, eps: float = 1e-5,
+                       group: Optional[int] = None, gate: str = "silu",
+                       gate_first: bool = False) -> None:
+    """RMS norm of x [..., dim] over groups of channels (None: the whole row)
+    with a gate act(z): y = norm(x o act(z)) o weight with gate_first, else
+    y = norm(x) o weight o act(z).  z (or None: no gate) and y share a type,
+    which x need not have; weight [dim] or [group] fp32 or None; gate "silu"
+    or "sigmoid"."""
+    d = _gated_check(x, z, weight, group)
+    dev = x.device
+    _check(y, "y", tuple(x.shape), _FLOATS if z is None else (z.dtype,), dev)
+    _call("ssd_gated_norm_fwd", dev,
+          _ptr(x), _ptr(z), _ptr(weight), _ptr(y), eps, _gate(gate), int(gate_first),
+          _dtype_code(x.dtype), _dtype_code(y.dtype), ctypes.byref(d))
+
+
+def gated_norm_workspace_bytes(d: GatedNormDims) -> int:
+    return int(_lib.ssd_gated_norm_bwd_workspace_bytes(ctypes.byref(d)))
+
+
+def ssd_gated_norm_bwd(x: torch.Tensor, z: Optional[torch.Tensor],
+                       weight: Optional[torch.Tensor], dy: torch.Tensor, dx: torch.Tensor,
+                       dz: Optional[torch.Tensor], dweight: Optional[torch.Tensor],
+                       workspace: torch.Tensor, eps: float = 1e-5,
+                       group: Optional[int] = None, gate: str = "silu",
+                       gate_first: bool = False) -> None:
+    """Gradients of ``ssd_gated_norm_fwd`` from its inputs.  ``workspace`` has
+    gated_norm_workspace_bytes(dims) bytes."""
+    d = _gated_check(x, z, weight, group)
+    dev = x.device
+    shape = tuple(x.shape)
+    _check(dy, "dy", shape, _FLOATS if z is None else (z.dtype,), dev)
+    _check(dx, "dx", shape, (x.dtype,), dev)
+    if (z is None) != (dz is None):
+        raise ValueError("dz is given exactly when z is")
+    _check(dz, "dz", shape, (dy.dtype,), dev, optional=True)
+    if dweight is not None and dweight.dim() == 1 and weight is None:
+        d.weight_dim = dweight.numel()
+    _check(dweight, "dweight", (d.weight_dim,), _F32, dev, optional=True)
+    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
+    nbytes = workspace.numel() * workspace.element_size()
+    _call("ssd_gated_norm_bwd", dev,
+          _ptr(x), _ptr(z), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dweight),
+          _ptr(workspace), nbytes, eps, _gate(gate), int(gate_first), _dtype_code(x.dtype),
+          _dtype_code(dy.dtype), ctypes.byref(d))
+
+
 # ------------------------------------------------------------ convenience
 def forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
             B: torch.Tensor, C: torch.Tensor, D: torch.Tensor,
@@ -525,3 +831,92 @@ def forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
     ssd_forward(x, dt, A, B, C, D, init_state, y, states, final, ws,
                 chunk_size)
     return y, states, final
+
+
+def _bytes(n: int, dev: torch.device) -> torch.Tensor:
+    # invalid or unsupported dims report 0 bytes; the call itself then returns
+    # the precise status before touching the (minimal) workspace
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+
+def linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+            init_state: Optional[torch.Tensor] = None,
+            cu_seqlens: Optional[torch.Tensor] = None,
+            scale: Optional[float] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Allocate and run ``ssd_linattn_fwd``: (o, final_state).  Rows of o outside
+    every packed sequence are not written."""
+    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
+    o = torch.empty_like(v)
+    final = torch.empty((d.nseq, d.nheads, d.dk, d.dv), dtype=torch.float32, device=q.device)
+    ws = _bytes(linattn_workspace_bytes(d, q.dtype), q.device)
+    ssd_linattn_fwd(q, k, v, log_decay, init_state, cu_seqlens, o, final, ws, scale)
+    return o, final
+
+
+def linattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: torch.Tensor, dout: torch.Tensor,
+                     dfinal: Optional[torch.Tensor] = None,
+                     init_state: Optional[torch.Tensor] = None,
+                     cu_seqlens: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Allocate and run ``ssd_linattn_bwd``: (dq, dk, dv, dinit)."""
+    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dinit = torch.empty((d.nseq, d.nheads, d.dk, d.dv), dtype=torch.float32, device=q.device)
+    ws = _bytes(linattn_workspace_bytes(d, q.dtype, backward=True), q.device)
+    ssd_linattn_bwd(q, k, v, log_decay, init_state, cu_seqlens, dout, dfinal, dq, dk, dv, dinit,
+                    ws, scale)
+    return dq, dk, dv, dinit
+
+
+def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+             res_scale: Optional[torch.Tensor] = None,
+             weight: Optional[torch.Tensor] = None,
+             eps: float = 1e-5) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Allocate and run ``ssd_add_norm_fwd``: (y, residual_out)."""
+    y = torch.empty_like(x)
+    out = torch.empty_like(x if residual is None else residual)
+    ssd_add_norm_fwd(x, residual, res_scale, weight, y, out, eps)
+    return y, out
+
+
+def add_norm_backward(x: torch.Tensor, residual: Optional[torch.Tensor],
+                      res_scale: Optional[torch.Tensor], weight: Optional[torch.Tensor],
+                      dy: torch.Tensor, dresidual_out: Optional[torch.Tensor] = None,
+                      eps: float = 1e-5) -> Tuple[Optional[torch.Tensor], ...]:
+    """Allocate and run ``ssd_add_norm_bwd``: (dx, dresidual, dres_scale,
+    dweight), None for each of the last three whose input is None."""
+    rows, D = _rows(x, "x")
+    dx = torch.empty_like(x)
+    dres, dscale, dw = (None if t is None else torch.empty_like(t)
+                        for t in (residual, res_scale, weight))
+    ws = _bytes(add_norm_workspace_bytes(rows, D), x.device)
+    ssd_add_norm_bwd(x, residual, res_scale, weight, dy, dresidual_out, dx, dres, dscale, dw, ws,
+                     eps)
+    return dx, dres, dscale, dw
+
+
+def gated_norm(x: torch.Tensor, z: Optional[torch.Tensor] = None,
+               weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               group: Optional[int] = None, gate: str = "silu",
+               gate_first: bool = False) -> torch.Tensor:
+    """Allocate and run ``ssd_gated_norm_fwd``: y, in z's type (x's without a
+    gate)."""
+    y = torch.empty_like(x if z is None else z)
+    ssd_gated_norm_fwd(x, z, weight, y, eps, group, gate, gate_first)
+    return y
+
+
+def gated_norm_backward(x: torch.Tensor, z: Optional[torch.Tensor],
+                        weight: Optional[torch.Tensor], dy: torch.Tensor, eps: float = 1e-5,
+                        group: Optional[int] = None, gate: str = "silu",
+                        gate_first: bool = False) -> Tuple[Optional[torch.Tensor], ...]:
+    """Allocate and run ``ssd_gated_norm_bwd``: (dx, dz, dweight), None for each
+    of the last two whose input is None."""
+    d = _gated_check(x, z, weight, group)
+    dx = torch.empty_like(x)
+    dz, dw = (None if t is None else torch.empty_like(t) for t in (z, weight))
+    ws = _bytes(gated_norm_workspace_bytes(d), x.device)
+    ssd_gated_norm_bwd(x, z, weight, dy, dx, dz, dw, ws, eps, group, gate, gate_first)
+    return dx, dz, dw
