@@ -32,10 +32,11 @@
 //     operand of the sum over j as they sit; Z comes from the LDS transpose read;
 //   - the output comes out transposed too, one token and 8 (fp32: 4)
 //     consecutive columns per lane: 16-byte stores.
-// bf16 tensors: 16x16x32 bf16 products, chunks of 64.  M and the scores are
-// rounded to bf16 as operands (each adds as much error to `out` as its own
-// rounding does); in M's update the decayed Z is split into two bf16 terms, so
-// that the fp32 state keeps 16 bits of each product.  fp32 tensors: 16x16x4 fp32
+// bf16 tensors: 16x16x32 bf16 products, chunks of 64.  M is rounded to bf16 as the
+// operand of X^T M: that part of the output gets an error as large as the
+// output's own rounding.  The scores are split into two bf16 terms, and so is the
+// decayed Z in M's update (three where M goes on to an fp32 state in memory: the
+// product is then as exact as an fp32 one).  fp32 tensors: 16x16x4 fp32
 // products, chunks of 32 (the scores' share grows with the chunk, and these
 // calls are bound by the matrix pipe).
 //
@@ -125,12 +126,6 @@ __device__ __forceinline__ Run find_run(const Seqs& s, int item) {
   return out;
 }
 
-// Consecutive logical items on one XCD (blocks are dealt round-robin).
-__device__ __forceinline__ int xcd_map(int bid, int total) {
-  if (total % 8) return bid;
-  return (bid % 8) * (total / 8) + bid / 8;
-}
-
 // log2 of lam.  The clamp keeps a head without memory (log_decay -inf) from
 // giving 0 * inf: 2^(-1e30) is 0 and 2^0 is 1.
 __device__ __forceinline__ float log2_decay(const float* ld, int h) {
@@ -158,10 +153,15 @@ struct Shape2 {
   static constexpr int NZ = ZD / (16 * kWaves);      // column blocks of a wave
   // LDS row strides, in elements: with these the 16 rows of an operand read and
   // the 4 rows of a transpose read fall on different banks.
-  static constexpr int YS = BF16 ? (YD == 128 ? 152 : 72) : YD + 4;
-  static constexpr int ZS = BF16 ? (ZD == 128 ? 152 : 72) : ZD + 4;
+  static constexpr int YS = BF16 ? YD + 16 : YD + 4;
+  static constexpr int ZS = BF16 ? (ZD == 128 ? 144 : 72) : ZD + 4;
+  static constexpr int PS = BF16 ? C + 8 : C + 4;
   static constexpr int XBYTES = C * YS * ES;
   static constexpr int ZBYTES = C * ZS * ES;
+  static constexpr int PBYTES = (BF16 ? 2 : 1) * C * PS * ES;   // the scores, bf16 as two terms
+  static constexpr int WBYTES = C * 4;                          // the weights of Z
+  static constexpr int BYTES = 2 * XBYTES + ZBYTES + PBYTES + WBYTES;
+  static constexpr int STATE_BYTES = XBYTES + ZBYTES + WBYTES;
   static constexpr int YU = C * YD * ES / 16 / kThreads;   // 16-byte units per thread
   static constexpr int ZU = C * ZD * ES / 16 / kThreads;
   // Column of M that row (or lane) rho of a wave's column block nz stands for.
@@ -170,6 +170,15 @@ struct Shape2 {
     return 16 * NZ * wave + 16 * nz + rho;
   }
 };
+
+// Place of column c of a bf16 row that is read along the k slots of a product:
+// within 32 columns, the slots of one lane group (columns 4 g + 0..3 and 16 on)
+// side by side, so that a lane reads its eight with one 16-byte load (two 8-byte
+// loads of a row take twice the LDS cycles, 16 against 8 of a wave). Four
+// columns stay together.
+__device__ __forceinline__ int slot_of(int c) {
+  return (c & ~31) + 8 * ((c >> 2) & 3) + 4 * ((c >> 4) & 1) + (c & 3);
+}
 
 // A tile of `n` token rows in the walk's order: its descriptor and each
 // thread's units.
@@ -189,29 +198,101 @@ struct Tile {
       v[j] = load_b128(r, i < n ? off : kPastRange);
     }
   }
+  template <bool SLOTS>
   __device__ __forceinline__ void commit(char* lds, int stride) const {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int u = (int)threadIdx.x + kThreads * j;
       const int i = u / (D * ES / 16), c = u % (D * ES / 16);
-      *(u32x4*)(lds + i * stride * ES + c * 16) = v[j];
+      char* row = lds + i * stride * ES;
+      if constexpr (SLOTS) {
+        *(u32x2*)(row + slot_of(8 * c) * 2) = (u32x2){v[j][0], v[j][1]};
+        *(u32x2*)(row + slot_of(8 * c + 4) * 2) = (u32x2){v[j][2], v[j][3]};
+      } else {
+        *(u32x4*)(row + c * 16) = v[j];
+      }
     }
   }
 };
+
+// The output rows of a chunk: block (tb, nz) holds token 16 tb + lr of the
+// chunk and four columns of the wave's block nz.
+template <int YD, int ZD, bool BF16, int NB, int NZ>
+__device__ __forceinline__ void store_rows(const Walk& w, const f32x4 (&o)[NB][NZ],
+                                           int64_t lowest, int n, int h, int H, int wave) {
+  using S = Shape2<YD, ZD, BF16>;
+  const int lane = threadIdx.x % kWave, lr = lane & 15, lq = lane >> 4;
+  const int64_t oheads = H / w.oshare;
+  const bool f32o = !BF16 || w.f32out;
+  const int oes = f32o ? 4 : 2;
+  const uint32_t orow = (uint32_t)(oheads * ZD * oes);
+  const rsrc_t orr = make_rsrc((char*)w.out + (lowest * oheads + h / w.oshare) * (ZD * oes),
+                               (uint32_t)(n - 1) * orow + ZD * oes);
+#pragma unroll
+  for (int tb = 0; tb < NB; ++tb) {
+    const int i = 16 * tb + lr;
+    const uint32_t at = i < n ? (uint32_t)(w.down ? n - 1 - i : i) * orow : kPastRange;
+    if (f32o) {
+#pragma unroll
+      for (int nz = 0; nz < NZ; ++nz)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[tb][nz]), orr,
+                                               (int)(at + S::zcol(wave, nz, 4 * lq) * 4), 0, 0);
+    } else {
+      const int off = (int)(at + S::zcol(wave, 0, 4 * lq) * 2);
+      const u32x2 a = {pack_bf16(o[tb][0][0], o[tb][0][1]), pack_bf16(o[tb][0][2], o[tb][0][3])};
+      if constexpr (NZ == 2) {
+        const u32x2 b = {pack_bf16(o[tb][1][0], o[tb][1][1]),
+                         pack_bf16(o[tb][1][2], o[tb][1][3])};
+        __builtin_amdgcn_raw_buffer_store_b128((u32x4){a[0], a[1], b[0], b[1]}, orr, off, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_buffer_store_b64(a, orr, off, 0, 0);
+      }
+    }
+  }
+}
+
+// lam^C from chunk to chunk: the factor that brings the product of all factors
+// so far nearest to the exact power, so the roundings do not add up.
+struct Factor {
+  Power p;
+  float off;              // relative error of the product
+  __device__ __forceinline__ float next() {
+    const float t = __builtin_fmaf(-p.hi, off, p.lo);
+    const float f = p.hi + t;
+    off = p.hi > 0.0f ? ((f - p.hi) - t) * __builtin_amdgcn_rcpf(p.hi) : 0.0f;
+    return f;
+  }
+};
+
+// Four fp32 values as bf16, and what the rounding left, as bf16 again.
+__device__ __forceinline__ void split4(const f32x4& v, u32x2& hi, u32x2& lo) {
+  uint32_t h0, h1, l0, l1;
+  split_bf16(v[0], v[1], h0, l0);
+  split_bf16(v[2], v[3], h1, l1);
+  hi = (u32x2){h0, h1};
+  lo = (u32x2){l0, l1};
+}
+__device__ __forceinline__ u32x4 join(u32x2 a, u32x2 b) { return (u32x4){a[0], a[1], b[0], b[1]}; }
 
 // One run of one walk; with OUT the outputs too, else only M from zero.
 template <int YD, int ZD, bool BF16, bool OUT>
 __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Run& run,
                                          const float* log_decay, int h, int H, char* lds) {
   using S = Shape2<YD, ZD, BF16>;
-  constexpr int C = S::C, NB = S::NB, NY = S::NY, NZ = S::NZ, YS = S::YS, ZS = S::ZS;
+  constexpr int C = S::C, NB = S::NB, NY = S::NY, NZ = S::NZ, YS = S::YS, ZS = S::ZS, PS = S::PS;
   constexpr int ES = S::ES;
-  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int lr = lane & 15, lq = lane >> 4;
-  char* xs = lds;
-  char* ys = lds + (OUT ? S::XBYTES : 0);
+  float* wtab = (float*)lds;
+  char* ys = lds + S::WBYTES;
   char* zs = ys + S::XBYTES;
+  char* xs = zs + S::ZBYTES;
+  char* ps = xs + S::XBYTES;
 
+  // Whether M goes on to a state in memory, where fp32 is asked for, or only
+  // into outputs of the tensors' type.
+  const bool exact = w.end != nullptr && (!OUT || run.r == run.nruns - 1);
   const float l2 = log2_decay(log_decay, h);
   const int a = w.down ? 0 : 1;
   const int64_t p0 = (int64_t)run.r * sq.run;
@@ -241,27 +322,33 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     }
   }
 
-  // Decays: of the scores by block distance, of X^T M by token, of Z by token.
-  float dec[NB][4], ex[NB], wz[NB][4];
+  // Decays of the scores, on the diagonal block and one block below it (each
+  // further block: lam^16 more), and of X^T M by token.
+  float dec0[4], dec1[4], ex[NB];
   const float cs = w.cx * w.cz;
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = 16 * b + lr - 4 * lq - r;
-      dec[b][r] = d >= 0 ? cs * exp2_hw(l2 * (float)d) : 0.0f;
-      wz[b][r] = w.cz * exp2_hw(l2 * (float)(C - a - (16 * b + 4 * lq + r)));
-    }
-    ex[b] = w.cx * exp2_hw(l2 * (float)(16 * b + lr + a));
+  for (int r = 0; r < 4; ++r) {
+    const int d = lr - 4 * lq - r;
+    dec0[r] = d >= 0 ? cs * exp2_hw(l2 * (float)d) : 0.0f;
+    dec1[r] = cs * exp2_hw(l2 * (float)(16 + d));
   }
-  Power lam_n = power(log_decay, h, C);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) ex[b] = w.cx * exp2_hw(l2 * (float)(16 * b + lr + a));
+  Factor lam{power(log_decay, h, C), 0.0f};
+
+  if constexpr (OUT && BF16) {
+    // score blocks (0, 1) and (2, 3) lie above the diagonal and are read
+    for (int u = tid; u < C * PS / 4; u += kThreads) *(u32x4*)(ps + 16 * u) = (u32x4){0, 0, 0, 0};
+  }
 
   Tile<YD, C, ES, S::YU> tx, ty;
   Tile<ZD, C, ES, S::ZU> tz;
+  auto lowest_of = [&](int p, int n) {
+    return w.down ? run.t0 + run.len - p0 - p - n : run.t0 + p0 + p;
+  };
   auto issue = [&](int p) {
     const int n = len - p < C ? len - p : C;
-    const int64_t lowest =
-        w.down ? run.t0 + run.len - p0 - p - n : run.t0 + p0 + p;
+    const int64_t lowest = lowest_of(p, n);
     if constexpr (OUT) tx.issue(w.x, H / w.xshare, h / w.xshare, lowest, n, w.down);
     ty.issue(w.y, H / w.yshare, h / w.yshare, lowest, n, w.down);
     tz.issue(w.z, H / w.zshare, h / w.zshare, lowest, n, w.down);
@@ -270,155 +357,154 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   for (int p = 0; p < len; p += C) {
     const int n = len - p < C ? len - p : C;
     __syncthreads();
-    if constexpr (OUT) tx.commit(xs, YS);
-    ty.commit(ys, YS);
-    tz.commit(zs, ZS);
+    if constexpr (OUT) tx.template commit<BF16>(xs, YS);
+    ty.template commit<BF16>(ys, YS);
+    tz.template commit<false>(zs, ZS);
+    if (tid < C) wtab[tid] = tid < n ? w.cz * exp2_hw(l2 * (float)(n - a - tid)) : 0.0f;
     __syncthreads();
-    if (p + C < len) issue(p + C);
-    if (n < C) {
-      lam_n = power(log_decay, h, n);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * b + 4 * lq + r;
-          wz[b][r] = j < n ? w.cz * exp2_hw(l2 * (float)(n - a - j)) : 0.0f;
-        }
-      }
+    if constexpr (!BF16) {
+      if (p + C < len) issue(p + C);
     }
-
-    // The output rows' descriptor.
-    const int64_t lowest = w.down ? run.t0 + run.len - p0 - p - n : run.t0 + p0 + p;
-    const int64_t oheads = H / w.oshare;
-    const bool f32o = !BF16 || w.f32out;
-    const int oes = f32o ? 4 : 2;
-    const uint32_t orow = (uint32_t)(oheads * ZD * oes);
-    const rsrc_t orr = make_rsrc((char*)w.out + (lowest * oheads + h / w.oshare) * (ZD * oes),
-                                 (uint32_t)(n - 1) * orow + ZD * oes);
-    auto store_out = [&](int tb, const f32x4 (&o)[NZ]) {
-      const int i = 16 * tb + lr;
-      const uint32_t at = i < n ? (uint32_t)(w.down ? n - 1 - i : i) * orow : kPastRange;
-#pragma unroll
-      for (int nz = 0; nz < NZ; ++nz) {
-        const uint32_t off = at + S::zcol(wave, nz, 4 * lq) * oes;
-        if (f32o) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[nz]), orr, (int)off,
-                                                 0, 0);
-        } else if constexpr (NZ == 2) {
-          if (nz == 0)
-            __builtin_amdgcn_raw_buffer_store_b128(
-                (u32x4){pack_bf16(o[0][0], o[0][1]), pack_bf16(o[0][2], o[0][3]),
-                        pack_bf16(o[1][0], o[1][1]), pack_bf16(o[1][2], o[1][3])},
-                orr, (int)off, 0, 0);
-        } else {
-          __builtin_amdgcn_raw_buffer_store_b64(
-              (u32x2){pack_bf16(o[0][0], o[0][1]), pack_bf16(o[0][2], o[0][3])}, orr, (int)off, 0,
-              0);
-        }
-      }
-    };
 
     if constexpr (BF16) {
       const uint16_t* xl = (const uint16_t*)xs;
       const uint16_t* yl = (const uint16_t*)ys;
       const uint16_t* zl = (const uint16_t*)zs;
-      // Z with tokens along the k slots: 32 kk + 4 lq + 0..3 and + 16
-      u32x4 zf[NB / 2][NZ];
-#pragma unroll
-      for (int kk = 0; kk < NB / 2; ++kk) {
-#pragma unroll
-        for (int nz = 0; nz < NZ; ++nz) {
-          const uint16_t* zp = zl + (32 * kk + 4 * lq + (lr >> 2)) * ZS +
-                               S::zcol(wave, nz, 4 * (lr & 3));
-          const u32x2 z0 = lds_read_tr16(zp), z1 = lds_read_tr16(zp + 16 * ZS);
-          zf[kk][nz] = (u32x4){z0[0], z0[1], z1[0], z1[1]};
-        }
-      }
-      auto row_frag = [&](const uint16_t* base, int i, int kk) {
-        const uint16_t* q = base + i * YS + 32 * kk + 4 * lq;
-        const u32x2 q0 = *(const u32x2*)q, q1 = *(const u32x2*)(q + 16);
-        return (u32x4){q0[0], q0[1], q1[0], q1[1]};
+      uint16_t* ph = (uint16_t*)ps;
+      uint16_t* pl = ph + C * PS;
+      // eight k slots of row i: columns 32 kk + 4 lq + 0..3 and 16 on
+      auto row_frag = [&](const uint16_t* base, int stride, int i, int kk) {
+        return *(const u32x4*)(base + i * stride + 32 * kk + 8 * lq);
       };
+      f32x4 o[NB][NZ] = {};
       if constexpr (OUT) {
-        u32x4 mb[NY / 2][NZ];
+        // (1) the ten score blocks on and below the diagonal, transposed (Y X^T),
+        // two or three per wave
+        auto score = [&](int id) {
+          const int tb = id > 5 ? 3 : id > 2 ? 2 : id > 0 ? 1 : 0, sb = id - tb * (tb + 1) / 2;
+          f32x4 d = {};
+#pragma unroll
+          for (int kk = 0; kk < NY / 2; ++kk)
+            d = mfma_bf16(row_frag(yl, YS, 16 * sb + lr, kk), row_frag(xl, YS, 16 * tb + lr, kk),
+                          d);
+          if (tb > sb) {
+            d *= exp2_hw(l2 * (float)(16 * (tb - sb - 1)));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[r] *= dec1[r];
+          } else {
+            // where j > i the score is selected away, never multiplied by 0
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[r] = lr >= 4 * lq + r ? d[r] * dec0[r] : 0.0f;
+          }
+          u32x2 hi, lo;
+          split4(d, hi, lo);
+          const int at = (16 * tb + lr) * PS + slot_of(16 * sb + 4 * lq);
+          *(u32x2*)(ph + at) = hi;
+          *(u32x2*)(pl + at) = lo;
+        };
+        score(wave);
+        score(wave + 4);
+        if (wave < 2) score(wave + 8);
+        __builtin_amdgcn_sched_barrier(0);
+        // (2) X^T M, transposed, for all tokens
 #pragma unroll
         for (int kk = 0; kk < NY / 2; ++kk) {
+          u32x4 mb[NZ], xf[NB];
 #pragma unroll
           for (int nz = 0; nz < NZ; ++nz) {
             const f32x4 m0 = m[2 * kk][nz], m1 = m[2 * kk + 1][nz];
-            mb[kk][nz] = (u32x4){pack_bf16(m0[0], m0[1]), pack_bf16(m0[2], m0[3]),
-                                 pack_bf16(m1[0], m1[1]), pack_bf16(m1[2], m1[3])};
+            mb[nz] = (u32x4){pack_bf16(m0[0], m0[1]), pack_bf16(m0[2], m0[3]),
+                             pack_bf16(m1[0], m1[1]), pack_bf16(m1[2], m1[3])};
+          }
+#pragma unroll
+          for (int tb = 0; tb < NB; ++tb) xf[tb] = row_frag(xl, YS, 16 * tb + lr, kk);
+#pragma unroll
+          for (int tb = 0; tb < NB; ++tb) {
+#pragma unroll
+            for (int nz = 0; nz < NZ; ++nz) o[tb][nz] = mfma_bf16(mb[nz], xf[tb], o[tb][nz]);
           }
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
-          u32x4 xf[NY / 2];
-          f32x4 o[NZ] = {};
 #pragma unroll
-          for (int kk = 0; kk < NY / 2; ++kk) {
-            xf[kk] = row_frag(xl, 16 * tb + lr, kk);
+          for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex[tb];
+        }
+        __syncthreads();
+      }
+      // Z with tokens along the k slots: 32 kk + 4 lq + 0..3 and 16 on
+      auto z_frag = [&](int kk, int nz) {
+        const uint16_t* zp = zl + (32 * kk + 4 * lq + (lr >> 2)) * ZS +
+                             S::zcol(wave, nz, 4 * (lr & 3));
+        return join(lds_read_tr16(zp), lds_read_tr16(zp + 16 * ZS));
+      };
+      // (3) the scores' part of the output
+      if constexpr (OUT) {
 #pragma unroll
-            for (int nz = 0; nz < NZ; ++nz) o[nz] = mfma_bf16(mb[kk][nz], xf[kk], o[nz]);
-          }
+        for (int kk = 0; kk < NB / 2; ++kk) {
+          u32x4 zf[NZ];
 #pragma unroll
-          for (int nz = 0; nz < NZ; ++nz) o[nz] *= ex[tb];
+          for (int nz = 0; nz < NZ; ++nz) zf[nz] = z_frag(kk, nz);
 #pragma unroll
-          for (int sp = 0; sp <= tb / 2; ++sp) {
-            f32x4 d[2] = {};
+          for (int term = 0; term < 2; ++term) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int sb = 2 * sp + e;
-              if (sb <= tb) {
+            for (int tb = 2 * kk; tb < NB; ++tb) {
+              const u32x4 pf = row_frag(term ? pl : ph, PS, 16 * tb + lr, kk);
 #pragma unroll
-                for (int kk = 0; kk < NY / 2; ++kk)
-                  d[e] = mfma_bf16(row_frag(yl, 16 * sb + lr, kk), xf[kk], d[e]);
-                // where j > i the score is selected away, never multiplied by 0
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  d[e][r] = (sb < tb || lr >= 4 * lq + r) ? d[e][r] * dec[tb - sb][r] : 0.0f;
-              }
+              for (int nz = 0; nz < NZ; ++nz) o[tb][nz] = mfma_bf16(zf[nz], pf, o[tb][nz]);
             }
-            const u32x4 pf = {pack_bf16(d[0][0], d[0][1]), pack_bf16(d[0][2], d[0][3]),
-                              pack_bf16(d[1][0], d[1][1]), pack_bf16(d[1][2], d[1][3])};
-#pragma unroll
-            for (int nz = 0; nz < NZ; ++nz) o[nz] = mfma_bf16(zf[sp][nz], pf, o[nz]);
           }
-          store_out(tb, o);
         }
+        store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave);
+        __builtin_amdgcn_sched_barrier(0);   // o's registers are free from here on
       }
-      // M = lam^n M + Y^T (wz o Z), the decayed Z as two bf16 terms
-      u32x4 zh[NB / 2][NZ], zlo[NB / 2][NZ];
-#pragma unroll
-      for (int kk = 0; kk < NB / 2; ++kk) {
-#pragma unroll
-        for (int nz = 0; nz < NZ; ++nz) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t u = zf[kk][nz][e];
-            const float* f = wz[2 * kk + e / 2] + 2 * (e % 2);
-            split_bf16(bf16_lo(u) * f[0], bf16_hi(u) * f[1], hi[e], lo[e]);
-          }
-          zh[kk][nz] = make_u32x4(hi);
-          zlo[kk][nz] = make_u32x4(lo);
-        }
-      }
+      if (p + C < len) issue(p + C);
+      // (4) M = lam^n M + Y^T (wz o Z), the decayed Z as three bf16 terms where
+      // `exact`, else as two
+      const float f = n == C ? lam.next() : power(log_decay, h, n).hi;
 #pragma unroll
       for (int yb = 0; yb < NY; ++yb) {
 #pragma unroll
+        for (int nz = 0; nz < NZ; ++nz) m[yb][nz] *= f;
+      }
+#pragma unroll
+      for (int kk = 0; kk < NB / 2; ++kk) {
+        u32x4 zh[NZ], zm[NZ], zl3[NZ];
+        const f32x4 w0 = *(const f32x4*)(wtab + 32 * kk + 4 * lq);
+        const f32x4 w1 = *(const f32x4*)(wtab + 32 * kk + 16 + 4 * lq);
+#pragma unroll
         for (int nz = 0; nz < NZ; ++nz) {
+          const u32x4 zf = z_frag(kk, nz);
+          uint32_t t[3][4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) m[yb][nz][r] = times(lam_n, m[yb][nz][r]);
+          for (int e = 0; e < 4; ++e) {
+            const float a0 = e < 2 ? w0[2 * e] : w1[2 * e - 4];
+            const float a1 = e < 2 ? w0[2 * e + 1] : w1[2 * e - 3];
+            split3_bf16(bf16_lo(zf[e]) * a0, bf16_hi(zf[e]) * a1, t[0][e], t[1][e], t[2][e]);
+          }
+          zh[nz] = make_u32x4(t[0]);
+          zm[nz] = make_u32x4(t[1]);
+          zl3[nz] = make_u32x4(t[2]);
         }
+constexpr int YG = 4;                  // row blocks at a time: independent products
 #pragma unroll
-        for (int kk = 0; kk < NB / 2; ++kk) {
-          const uint16_t* yp = yl + (32 * kk + 4 * lq + (lr >> 2)) * YS + 16 * yb + 4 * (lr & 3);
-          const u32x2 y0 = lds_read_tr16(yp), y1 = lds_read_tr16(yp + 16 * YS);
-          const u32x4 yf = {y0[0], y0[1], y1[0], y1[1]};
+        for (int y0 = 0; y0 < NY; y0 += YG) {
+          u32x4 yf[YG];
 #pragma unroll
-          for (int nz = 0; nz < NZ; ++nz) {
-            m[yb][nz] = mfma_bf16(yf, zh[kk][nz], m[yb][nz]);
-            m[yb][nz] = mfma_bf16(yf, zlo[kk][nz], m[yb][nz]);
+          for (int y = 0; y < YG; ++y) {
+            const uint16_t* yp = yl + (32 * kk + 4 * lq + (lr >> 2)) * YS +
+                                 slot_of(16 * (y0 + y) + 4 * (lr & 3));
+            yf[y] = join(lds_read_tr16(yp), lds_read_tr16(yp + 16 * YS));
+          }
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            if (term == 2 && !exact) break;
+#pragma unroll
+            for (int y = 0; y < YG; ++y) {
+#pragma unroll
+              for (int nz = 0; nz < NZ; ++nz)
+                m[y0 + y][nz] = mfma_bf16(yf[y], term == 0 ? zh[nz] : term == 1 ? zm[nz] : zl3[nz],
+                                          m[y0 + y][nz]);
+            }
           }
         }
       }
@@ -426,6 +512,46 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
       const float* xl = (const float*)xs;
       const float* yl = (const float*)ys;
       const float* zl = (const float*)zs;
+      float* pl = (float*)ps;
+      f32x4 o[NB][NZ] = {};
+      if constexpr (OUT) {
+        // (1) the three score blocks of a chunk, one per wave
+        if (wave < 3) {
+          const int tb = (wave + 1) / 2, sb = wave / 2;
+          f32x4 d = {};
+#pragma unroll
+          for (int yb = 0; yb < NY; ++yb) {
+            const f32x4 xf = *(const f32x4*)(xl + (16 * tb + lr) * YS + 16 * yb + 4 * lq);
+            const f32x4 yf = *(const f32x4*)(yl + (16 * sb + lr) * YS + 16 * yb + 4 * lq);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d = mfma_f32(yf[r], xf[r], d);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            d[r] = sb < tb ? d[r] * dec1[r] : lr >= 4 * lq + r ? d[r] * dec0[r] : 0.0f;
+          *(f32x4*)(pl + (16 * tb + lr) * PS + 16 * sb + 4 * lq) = d;
+        }
+        // (2) X^T M
+#pragma unroll
+        for (int yb = 0; yb < NY; ++yb) {
+#pragma unroll
+          for (int tb = 0; tb < NB; ++tb) {
+            const f32x4 xf = *(const f32x4*)(xl + (16 * tb + lr) * YS + 16 * yb + 4 * lq);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+#pragma unroll
+              for (int nz = 0; nz < NZ; ++nz) o[tb][nz] = mfma_f32(m[yb][nz][r], xf[r], o[tb][nz]);
+            }
+          }
+        }
+#pragma unroll
+        for (int tb = 0; tb < NB; ++tb) {
+#pragma unroll
+          for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex[tb];
+        }
+        __syncthreads();
+      }
+      // (3)
       f32x4 zf[NB][NZ];
 #pragma unroll
       for (int sb = 0; sb < NB; ++sb) {
@@ -435,56 +561,26 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           for (int r = 0; r < 4; ++r)
             zf[sb][nz][r] = zl[(16 * sb + 4 * lq + r) * ZS + S::zcol(wave, nz, lr)];
         }
-      }
-      if constexpr (OUT) {
+        if constexpr (OUT) {
 #pragma unroll
-        for (int tb = 0; tb < NB; ++tb) {
-          f32x4 xf[NY], o[NZ] = {};
-#pragma unroll
-          for (int yb = 0; yb < NY; ++yb) {
-            xf[yb] = *(const f32x4*)(xl + (16 * tb + lr) * YS + 16 * yb + 4 * lq);
+          for (int tb = sb; tb < NB; ++tb) {
+            const f32x4 pf = *(const f32x4*)(pl + (16 * tb + lr) * PS + 16 * sb + 4 * lq);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
 #pragma unroll
-              for (int nz = 0; nz < NZ; ++nz) o[nz] = mfma_f32(m[yb][nz][r], xf[yb][r], o[nz]);
+              for (int nz = 0; nz < NZ; ++nz) o[tb][nz] = mfma_f32(zf[sb][nz][r], pf[r], o[tb][nz]);
             }
           }
-#pragma unroll
-          for (int nz = 0; nz < NZ; ++nz) o[nz] *= ex[tb];
-#pragma unroll
-          for (int sb = 0; sb <= tb; ++sb) {
-            f32x4 d = {};
-#pragma unroll
-            for (int yb = 0; yb < NY; ++yb) {
-              const f32x4 yf = *(const f32x4*)(yl + (16 * sb + lr) * YS + 16 * yb + 4 * lq);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) d = mfma_f32(yf[r], xf[yb][r], d);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              d[r] = (sb < tb || lr >= 4 * lq + r) ? d[r] * dec[tb - sb][r] : 0.0f;
-#pragma unroll
-              for (int nz = 0; nz < NZ; ++nz) o[nz] = mfma_f32(zf[sb][nz][r], d[r], o[nz]);
-            }
-          }
-          store_out(tb, o);
         }
+        const f32x4 wv = *(const f32x4*)(wtab + 16 * sb + 4 * lq);
+#pragma unroll
+        for (int nz = 0; nz < NZ; ++nz) zf[sb][nz] *= wv;
       }
-#pragma unroll
-      for (int sb = 0; sb < NB; ++sb) {
-#pragma unroll
-        for (int nz = 0; nz < NZ; ++nz) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) zf[sb][nz][r] *= wz[sb][r];
-        }
-      }
+      const float f = n == C ? lam.next() : power(log_decay, h, n).hi;
 #pragma unroll
       for (int yb = 0; yb < NY; ++yb) {
 #pragma unroll
-        for (int nz = 0; nz < NZ; ++nz) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) m[yb][nz][r] = times(lam_n, m[yb][nz][r]);
-        }
+        for (int nz = 0; nz < NZ; ++nz) m[yb][nz] *= f;
 #pragma unroll
         for (int sb = 0; sb < NB; ++sb) {
 #pragma unroll
@@ -495,6 +591,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           }
         }
       }
+      if constexpr (OUT) store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave);
     }
   }
 
@@ -521,20 +618,23 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   }
 }
 
-// Workgroup (item, head, walk), the walk fastest, then the head: what shares
-// operands runs on one XCD at about the same time.
+// Workgroup (item, walk, head), the head fastest.  Blocks are dealt to the 8 XCDs
+// in turn, so with H a multiple of 8 every XCD gets the walks of H/8 consecutive
+// heads, which share operands.  Items without a run (up to nseq of them) come
+// last: in between they would leave CUs with one workgroup and others with three.
 template <int K, int V, bool BF16, int NW, bool OUT>
-__global__ __launch_bounds__(kThreads) void walk_kernel(Walks ws, Seqs sq,
+__global__ __launch_bounds__(kThreads, 2) void walk_kernel(Walks ws, Seqs sq,
                                                         const float* __restrict__ log_decay,
                                                         int H) {
   using SA = Shape2<K, V, BF16>;
   using SB = Shape2<V, K, BF16>;
-  constexpr int XA = (OUT ? 2 : 1) * SA::XBYTES + SA::ZBYTES;
-  constexpr int XB = (OUT ? 2 : 1) * SB::XBYTES + SB::ZBYTES;
+  constexpr int XA = OUT ? SA::BYTES : SA::STATE_BYTES;
+  constexpr int XB = OUT ? SB::BYTES : SB::STATE_BYTES;
   __shared__ __attribute__((aligned(16))) char lds[NW == 1 || XA > XB ? XA : XB];
-  const int id = xcd_map(blockIdx.x, gridDim.x);
-  const Walk& w = ws.w[NW == 1 ? 0 : id % NW];
-  const int h = id / NW % H, item = id / NW / H;
+  const int b = (int)(blockIdx.x % H), id = (int)(blockIdx.x / H);
+  const int h = H % 8 ? b : b % 8 * (H / 8) + b / 8;
+  const Walk& w = ws.w[id % NW];
+  const int item = id / NW;
   const Run run = find_run(sq, item);
   if (run.seq < 0 || (!OUT && run.r + 1 >= run.nruns)) return;
   if constexpr (NW == 1 || K == V) {
@@ -614,16 +714,19 @@ __global__ __launch_bounds__(256) void sum_heads_kernel(const float* __restrict_
   }
 }
 
-// Tokens of a run: two workgroups per CU over all walks, whole chunks, and
-// at least four chunks (the states at a run's ends cost about as much traffic
-// as four chunks' tokens).
+// Tokens of a run: whole chunks, as few as keep the runs of all walks within
+// two workgroups per CU (a few more would wait for a second round), with two
+// thirds of a run allowed for the end of each sequence; at least four chunks (the
+// states at a run's ends cost about as much traffic as four chunks' tokens).
 constexpr int64_t kWantRuns = 512;
 constexpr int64_t kMinChunks = 4;
 
 int run_tokens(const LinattnShape& s, bool bf16, int walks) {
   const int64_t C = bf16 ? 64 : 32;
-  const int64_t all = s.tokens * s.nheads * walks;
-  int64_t chunks = (all + kWantRuns * C - 1) / (kWantRuns * C);
+  const int64_t each = 3 * kWantRuns / (s.nheads * walks);     // thirds of runs for a head
+  const int64_t ends = 2 * s.nseq < each / 2 ? 2 * s.nseq : each / 2;
+  int64_t chunks = each > ends ? (3 * s.tokens + (each - ends) * C - 1) / ((each - ends) * C)
+                               : (s.tokens + C - 1) / C;
   if (chunks < kMinChunks) chunks = kMinChunks;
   const int64_t most = (s.tokens + C - 1) / C;
   return (int)((chunks < most ? chunks : most) * C);
