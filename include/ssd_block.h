@@ -64,8 +64,9 @@ size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims *dims, ssd_dtype d
  * Whole sequences.  init_state [nseq, H, K, V] fp32 or NULL (zeros);
  * final_state [nseq, H, K, V] fp32 (written; an empty sequence's is its
  * initial state) or NULL.  They may be the same buffer (sequences continued
- * in place).  For bf16 tensors the masked scores and the state are rounded
- * to bf16 as operands of the matrix products; sums and states are fp32.
+ * in place).  Sums and states are fp32; for bf16 tensors the state is rounded to
+ * bf16 as an operand of q_t^T S.  A value of v that is not finite also reaches
+ * the outputs of up to 63 tokens of its sequence and head before it.
  */
 ssd_status ssd_linattn_fwd(const void *q, const void *k, const void *v,
                            const float *log_decay, const float *init_state,
@@ -81,8 +82,9 @@ ssd_status ssd_linattn_fwd(const void *q, const void *k, const void *v,
  *     dq_t = scale sum_h S_t dout_t     dk_t = sum_h R_t v_t   (h over the group)
  *     dv_t = R_t^T k_t                  dinit = lam R_1
  * dq, dk [tokens, G, K], dv [tokens, H, V] in dtype (written); dinit
- * [nseq, H, K, V] fp32 (written) or NULL; it may be the same buffer as
- * dfinal.  log_decay is a constant of the model: it has no gradient here.
+ * [nseq, H, K, V] fp32 (written) or NULL, and must not overlap dfinal
+ * (SSD_ERR_INVALID_ARGUMENT).  log_decay is a constant of the model: it has no
+ * gradient here.
  */
 ssd_status ssd_linattn_bwd(const void *q, const void *k, const void *v,
                            const float *log_decay, const float *init_state,

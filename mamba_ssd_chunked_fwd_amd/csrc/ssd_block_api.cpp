@@ -43,6 +43,13 @@ bool ok_lengths(const int32_t* cu, const ssd::LinattnShape& s) {
   return cu != nullptr ? (reinterpret_cast<uintptr_t>(cu) & 3u) == 0 : s.tokens % s.nseq == 0;
 }
 
+// Whether two byte ranges of length n (either may be null) share any byte.
+bool overlap(const void* a, const void* b, size_t n) {
+  if (a == nullptr || b == nullptr) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + n && y < x + n;
+}
+
 bool ok_workspace(const void* ws, size_t have, size_t need) {
   return ok_ptr(ws) && have >= need;
 }
@@ -109,6 +116,9 @@ ssd_status ssd_linattn_bwd(const void* q, const void* k, const void* v, const fl
   if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(log_decay) || !ok_opt(init_state) ||
       !ok_ptr(dout) || !ok_opt(dfinal) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) ||
       !ok_opt(dinit))
+    return SSD_ERR_INVALID_ARGUMENT;
+  // dk is walked from dfinal while dv's walk writes dinit
+  if (overlap(dfinal, dinit, sizeof(float) * (size_t)(s.nseq * s.nheads) * (size_t)(s.dk * s.dv)))
     return SSD_ERR_INVALID_ARGUMENT;
   const bool bf16 = dtype == SSD_BF16;
   if (!ok_workspace(workspace, workspace_bytes, ssd::linattn_workspace(s, bf16, true)))

@@ -41,15 +41,18 @@
 // calls are bound by the matrix pipe).
 //
 // The chains of a call are few (sequences x heads) and long, so each is cut
-// into runs of `run` tokens, walked at once by (about) two workgroups per CU:
-//   1. run_states: what every run but the last adds to M from zero;
-//   2. run_starts: M at the start of every run, in place (lam^run from run to
-//      run, an element per thread);
-//   3. walks: the runs.
+// into runs of equal numbers of chunks, walked at once by (about) two workgroups
+// per CU:
+//   1. run_states: M at the end of the first run, and what every later run but
+//      the last adds to M from zero, into a slot each;
+//   2. run_starts, for sequences of more than kFold runs: M at the start of every
+//      run, in place (lam^run from run to run, an element per thread);
+//   3. walks: the runs.  In a sequence of few runs each walk goes through the
+//      slots before its own itself.
 // A call whose chains are all no longer than a run goes straight to 3.  The
 // powers of lam that are multiplied up along a chain are taken in 64 bits and
-// kept as two fp32 terms: the rounding of one factor would otherwise grow with
-// the number of chunks.
+// kept as two fp32 terms, or corrected from chunk to chunk: the rounding of one
+// factor would otherwise grow with the number of chunks.
 #include "ssd_block_launch.h"
 #include "ssd_device.h"
 #include "ssd_host.h"
@@ -61,6 +64,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
+// A walk goes through the slots before its own itself in sequences of up to this
+// many runs: up to kFold - 1 slots are then read by each run, where run_starts
+// reads and writes each once and costs a launch (some 10 us at 4 runs of 16 heads
+// and 8 sequences; the walks get 3 us longer).
+constexpr int kFold = 4;
 constexpr uint32_t kPastRange = 0x7FFF0000u;
 
 // One walk.  Head h of an operand is its head h / share.
@@ -70,6 +78,7 @@ struct Walk {
   const float* start;   // [nseq, H, K, V] or null
   float* end;           // [nseq, H, K, V] or null
   float* slots;         // states at the runs' starts, in accumulator order
+  float* slots_t;       // the slots of the walk with the transposed M, or null
   int xshare, yshare, zshare, oshare;
   float cx, cz;
   bool down;
@@ -89,7 +98,7 @@ struct Walks {
 struct Seqs {
   const int32_t* cu;
   int64_t tokens, len;
-  int nseq, run;
+  int nseq, run, chunk;
   __device__ __forceinline__ int64_t at(int i) const {
     if (cu == nullptr) return i * len;
     const int64_t v = cu[i];
@@ -97,12 +106,20 @@ struct Seqs {
   }
 };
 
-// A workgroup's run: sequence, its first token and length, the run's number
-// and how many there are; seq < 0: none.
+// Tokens of each run of a sequence of `len`: at most s.run, whole chunks, the
+// same for all runs but the last.
+__device__ __forceinline__ int run_length(const Seqs& s, int64_t len) {
+  const int64_t chunks = (len + s.chunk - 1) / s.chunk;
+  const int64_t n = (len + s.run - 1) / s.run;
+  return n > 1 ? (int)((chunks + n - 1) / n) * s.chunk : s.run;
+}
+
+// A workgroup's run: sequence, its first token and length, the run's number,
+// how many there are and how many tokens each has; seq < 0: none.
 struct Run {
-  int seq, r, nruns;
+  int seq, r, nruns, each;
   int64_t t0, len;
-  int64_t slot;
+  int64_t slot;           // of the sequence's first run
 };
 
 __device__ __forceinline__ Run find_run(const Seqs& s, int item) {
@@ -113,15 +130,16 @@ __device__ __forceinline__ Run find_run(const Seqs& s, int item) {
     before += n;
     if (n < kThreads) break;
   }
-  Run out{before - 1, 0, 0, 0, 0, 0};
+  Run out{before - 1, 0, 0, 0, 0, 0, 0};
   if (out.seq < 0) return out;
   out.t0 = s.at(out.seq);
   const int64_t end = s.at(out.seq + 1);
   out.len = end > out.t0 ? end - out.t0 : 0;
-  out.nruns = out.len > s.run ? (int)((out.len + s.run - 1) / s.run) : 1;
+  out.each = run_length(s, out.len);
+  out.nruns = out.len > out.each ? (int)((out.len + out.each - 1) / out.each) : 1;
   const int64_t r = item - (out.t0 / s.run + out.seq);
   out.r = (int)r;
-  out.slot = 2 * out.t0 / s.run + r;
+  out.slot = 2 * out.t0 / s.run;
   if (r < 0 || r >= out.nruns) out.seq = -1;
   return out;
 }
@@ -168,6 +186,14 @@ struct Shape2 {
   static __device__ __forceinline__ int zcol(int wave, int nz, int rho) {
     if constexpr (BF16) return 16 * NZ * wave + 4 * NZ * (rho >> 2) + 4 * nz + (rho & 3);
     return 16 * NZ * wave + 16 * nz + rho;
+  }
+  // Place of M[y][z] in a slot: blocks (yb, nz) of a value per thread and row.
+  static __device__ __forceinline__ int order(int y, int z) {
+    const int wave = z / (16 * NZ), in = z % (16 * NZ);
+    const int nz = BF16 ? in % (4 * NZ) / 4 : in / 16;
+    const int rho = BF16 ? in / (4 * NZ) * 4 + in % 4 : in % 16;
+    const int thread = wave * kWave + (y % 16) / 4 * 16 + rho;
+    return ((y / 16 * NZ + nz) * kThreads + thread) * 4 + y % 4;
   }
 };
 
@@ -292,33 +318,68 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
 
   // Whether M goes on to a state in memory, where fp32 is asked for, or only
   // into outputs of the tensors' type.
-  const bool exact = w.end != nullptr && (!OUT || run.r == run.nruns - 1);
+  const bool exact = w.end != nullptr && run.r == run.nruns - 1;
   const float l2 = log2_decay(log_decay, h);
   const int a = w.down ? 0 : 1;
-  const int64_t p0 = (int64_t)run.r * sq.run;
-  const int len = (int)(run.len - p0 < sq.run ? run.len - p0 : sq.run);
+  const int64_t p0 = (int64_t)run.r * run.each;
+  const int len = (int)(run.len - p0 < run.each ? run.len - p0 : run.each);
 
   // M[y][z]: block (yb, nz) holds rows 16 yb + 4 lq + r, column zcol(nz, lr).
   f32x4 m[NY][NZ];
   const int64_t sbase = ((int64_t)run.seq * H + h) * YD * ZD;
-  const bool from_slot = OUT && run.nruns > 1;
+  const int64_t step = (int64_t)H * YD * ZD;               // from slot to slot
+  float* slot = w.slots + run.slot * step + (int64_t)h * YD * ZD + tid * 4;
+  // States taken on in place: the first run's start is kept in slot 0, because
+  // the last run may write its end before the first has read it.
+  const bool kept = w.start != nullptr && w.start == w.end && run.nruns > 1;
+  if (OUT && run.nruns > 1 && (run.r > 0 || kept)) {
+    const bool folded = run.nruns <= kFold;
+    const int from = run.r == 0 ? 0 : folded ? 1 : run.r;
 #pragma unroll
-  for (int yb = 0; yb < NY; ++yb) {
+    for (int i = 0; i < NY * NZ; ++i)
+      m[i / NZ][i % NZ] = *(const f32x4*)(slot + from * step + i * kThreads * 4);
+    if (folded && run.r > 1) {
+      const Power lam = power(log_decay, h, run.each);
+      for (int r = 2; r <= run.r; ++r) {
 #pragma unroll
-    for (int nz = 0; nz < NZ; ++nz) {
-      m[yb][nz] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-      if (from_slot) {
-        m[yb][nz] = *(const f32x4*)(w.slots + (run.slot * H + h) * YD * ZD +
-                                    ((yb * NZ + nz) * kThreads + tid) * 4);
-      } else if (OUT && w.start != nullptr) {
-        const int y = 16 * yb + 4 * lq, z = S::zcol(wave, nz, lr);
-        if (w.turned) {
-          m[yb][nz] = *(const f32x4*)(w.start + sbase + z * YD + y);
-        } else {
+        for (int i = 0; i < NY * NZ; ++i) {
+          const f32x4 add = *(const f32x4*)(slot + r * step + i * kThreads * 4);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) m[yb][nz][r] = w.start[sbase + (y + r) * ZD + z];
+          for (int e = 0; e < 4; ++e)
+            m[i / NZ][i % NZ][e] = times(lam, m[i / NZ][i % NZ][e]) + add[e];
         }
       }
+    }
+  } else if (run.r == 0 && w.start != nullptr && w.turned) {
+#pragma unroll
+    for (int yb = 0; yb < NY; ++yb) {
+#pragma unroll
+      for (int nz = 0; nz < NZ; ++nz)
+        m[yb][nz] = *(const f32x4*)(w.start + sbase + S::zcol(wave, nz, lr) * YD + 16 * yb +
+                                    4 * lq);
+    }
+  } else if (run.r == 0 && w.start != nullptr) {
+#pragma unroll
+    for (int yb = 0; yb < NY; ++yb) {
+#pragma unroll
+      for (int nz = 0; nz < NZ; ++nz) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          m[yb][nz][r] =
+              w.start[sbase + (16 * yb + 4 * lq + r) * ZD + S::zcol(wave, nz, lr)];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int yb = 0; yb < NY; ++yb) {
+#pragma unroll
+      for (int nz = 0; nz < NZ; ++nz) m[yb][nz] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
+  if constexpr (!OUT) {
+    if (run.r == 0 && kept) {
+#pragma unroll
+      for (int i = 0; i < NY * NZ; ++i) *(f32x4*)(slot + i * kThreads * 4) = m[i / NZ][i % NZ];
     }
   }
 
@@ -387,14 +448,12 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           for (int kk = 0; kk < NY / 2; ++kk)
             d = mfma_bf16(row_frag(yl, YS, 16 * sb + lr, kk), row_frag(xl, YS, 16 * tb + lr, kk),
                           d);
-          if (tb > sb) {
-            d *= exp2_hw(l2 * (float)(16 * (tb - sb - 1)));
+          const float far = exp2_hw(l2 * (float)(16 * (tb > sb ? tb - sb - 1 : 0)));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) d[r] *= dec1[r];
-          } else {
+          for (int r = 0; r < 4; ++r) {
             // where j > i the score is selected away, never multiplied by 0
-#pragma unroll
-            for (int r = 0; r < 4; ++r) d[r] = lr >= 4 * lq + r ? d[r] * dec0[r] : 0.0f;
+            const float v = d[r] * (tb > sb ? dec1[r] * far : dec0[r]);
+            d[r] = tb > sb || lr >= 4 * lq + r ? v : 0.0f;
           }
           u32x2 hi, lo;
           split4(d, hi, lo);
@@ -404,6 +463,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         };
         score(wave);
         score(wave + 4);
+        __builtin_amdgcn_sched_barrier(0);
         if (wave < 2) score(wave + 8);
         __builtin_amdgcn_sched_barrier(0);
         // (2) X^T M, transposed, for all tokens
@@ -423,6 +483,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
 #pragma unroll
             for (int nz = 0; nz < NZ; ++nz) o[tb][nz] = mfma_bf16(mb[nz], xf[tb], o[tb][nz]);
           }
+          if (kk % 2) __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
@@ -458,55 +519,65 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         __builtin_amdgcn_sched_barrier(0);   // o's registers are free from here on
       }
       if (p + C < len) issue(p + C);
-      // (4) M = lam^n M + Y^T (wz o Z), the decayed Z as three bf16 terms where
-      // `exact`, else as two
+      // (4) M = lam^n M + Y^T (wz o Z), the decayed Z as two bf16 terms, and a third
+      // where `exact`
       const float f = n == C ? lam.next() : power(log_decay, h, n).hi;
 #pragma unroll
       for (int yb = 0; yb < NY; ++yb) {
 #pragma unroll
         for (int nz = 0; nz < NZ; ++nz) m[yb][nz] *= f;
       }
+      auto update = [&](auto first, auto last) {
+        constexpr int T0 = decltype(first)::value, T1 = decltype(last)::value;
 #pragma unroll
-      for (int kk = 0; kk < NB / 2; ++kk) {
-        u32x4 zh[NZ], zm[NZ], zl3[NZ];
-        const f32x4 w0 = *(const f32x4*)(wtab + 32 * kk + 4 * lq);
-        const f32x4 w1 = *(const f32x4*)(wtab + 32 * kk + 16 + 4 * lq);
+        for (int kk = 0; kk < NB / 2; ++kk) {
+          u32x4 zt[3][NZ];
+          const f32x4 w0 = *(const f32x4*)(wtab + 32 * kk + 4 * lq);
+          const f32x4 w1 = *(const f32x4*)(wtab + 32 * kk + 16 + 4 * lq);
 #pragma unroll
-        for (int nz = 0; nz < NZ; ++nz) {
-          const u32x4 zf = z_frag(kk, nz);
-          uint32_t t[3][4];
+          for (int nz = 0; nz < NZ; ++nz) {
+            const u32x4 zf = z_frag(kk, nz);
+            uint32_t t[3][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a0 = e < 2 ? w0[2 * e] : w1[2 * e - 4];
-            const float a1 = e < 2 ? w0[2 * e + 1] : w1[2 * e - 3];
-            split3_bf16(bf16_lo(zf[e]) * a0, bf16_hi(zf[e]) * a1, t[0][e], t[1][e], t[2][e]);
+            for (int e = 0; e < 4; ++e) {
+              const float v0 = bf16_lo(zf[e]) * (e < 2 ? w0[2 * e] : w1[2 * e - 4]);
+              const float v1 = bf16_hi(zf[e]) * (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]);
+              split3_bf16(v0, v1, t[0][e], t[1][e], t[2][e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 3; ++e) zt[e][nz] = make_u32x4(t[e]);
           }
-          zh[nz] = make_u32x4(t[0]);
-          zm[nz] = make_u32x4(t[1]);
-          zl3[nz] = make_u32x4(t[2]);
-        }
-constexpr int YG = 4;                  // row blocks at a time: independent products
+          constexpr int YG = 4;                // row blocks at a time: independent products
 #pragma unroll
-        for (int y0 = 0; y0 < NY; y0 += YG) {
-          u32x4 yf[YG];
-#pragma unroll
-          for (int y = 0; y < YG; ++y) {
-            const uint16_t* yp = yl + (32 * kk + 4 * lq + (lr >> 2)) * YS +
-                                 slot_of(16 * (y0 + y) + 4 * (lr & 3));
-            yf[y] = join(lds_read_tr16(yp), lds_read_tr16(yp + 16 * YS));
-          }
-#pragma unroll
-          for (int term = 0; term < 3; ++term) {
-            if (term == 2 && !exact) break;
+          for (int y0 = 0; y0 < NY; y0 += YG) {
+            u32x4 yf[YG];
 #pragma unroll
             for (int y = 0; y < YG; ++y) {
+              const uint16_t* yp = yl + (32 * kk + 4 * lq + (lr >> 2)) * YS +
+                                   slot_of(16 * (y0 + y) + 4 * (lr & 3));
+              yf[y] = join(lds_read_tr16(yp), lds_read_tr16(yp + 16 * YS));
+            }
 #pragma unroll
-              for (int nz = 0; nz < NZ; ++nz)
-                m[y0 + y][nz] = mfma_bf16(yf[y], term == 0 ? zh[nz] : term == 1 ? zm[nz] : zl3[nz],
-                                          m[y0 + y][nz]);
+            for (int e = T0; e <= T1; ++e) {
+#pragma unroll
+              for (int y = 0; y < YG; ++y) {
+#pragma unroll
+                for (int nz = 0; nz < NZ; ++nz)
+                  m[y0 + y][nz] = mfma_bf16(yf[y], zt[e][nz], m[y0 + y][nz]);
+              }
             }
           }
         }
+      };
+      using Term0 = std::integral_constant<int, 0>;
+      using Term1 = std::integral_constant<int, 1>;
+      using Term2 = std::integral_constant<int, 2>;
+      if constexpr (OUT) {
+        update(Term0{}, Term1{});
+        __builtin_amdgcn_sched_barrier(0);
+        if (exact) update(Term2{}, Term2{});
+      } else {
+        update(Term0{}, Term2{});
       }
     } else {
       const float* xl = (const float*)xs;
@@ -608,12 +679,21 @@ constexpr int YG = 4;                  // row blocks at a time: independent prod
       }
     }
   } else {
-    float* slot = w.slots + ((run.slot + 1) * H + h) * YD * ZD;
+    slot += (run.r + 1) * step;
 #pragma unroll
-    for (int yb = 0; yb < NY; ++yb) {
+    for (int i = 0; i < NY * NZ; ++i) *(f32x4*)(slot + i * kThreads * 4) = m[i / NZ][i % NZ];
+    if (w.slots_t != nullptr) {
+      float* st = w.slots_t + (run.slot + run.r + 1) * step + (int64_t)h * YD * ZD;
+      using T = Shape2<ZD, YD, BF16>;
 #pragma unroll
-      for (int nz = 0; nz < NZ; ++nz)
-        *(f32x4*)(slot + ((yb * NZ + nz) * kThreads + tid) * 4) = m[yb][nz];
+      for (int yb = 0; yb < NY; ++yb) {
+#pragma unroll
+        for (int nz = 0; nz < NZ; ++nz) {
+          const int z = S::zcol(wave, nz, lr);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) st[T::order(z, 16 * yb + 4 * lq + r)] = m[yb][nz][r];
+        }
+      }
     }
   }
 }
@@ -647,43 +727,29 @@ __global__ __launch_bounds__(kThreads, 2) void walk_kernel(Walks ws, Seqs sq,
   }
 }
 
-// M at the start of each run of the sequences that have more than one:
-// slot 0 = start, slot r = lam^run slot r-1 + slot r.  One thread per four
-// elements; blockIdx.x = (walk, head, part of the state), blockIdx.y strides over
-// the sequences.
-template <int K, int V, bool BF16>
+// M at the start of each run of the sequences of more than kFold runs: slot r =
+// lam^run slot r-1 + slot r, from slot 1 on.  One thread per four elements;
+// blockIdx.x = (walk, head, part of the state), blockIdx.y strides over the
+// sequences.
 __global__ __launch_bounds__(kThreads) void run_starts_kernel(Walks ws, Seqs sq,
                                                               const float* __restrict__ log_decay,
-                                                              int H) {
-  constexpr int PARTS = K * V / 4 / kThreads;
-  const int part = blockIdx.x % PARTS, h = blockIdx.x / PARTS % H;
-  const Walk& w = ws.w[blockIdx.x / PARTS / H];
-  const int tid = threadIdx.x, wave = tid / kWave, lr = tid & 15, lq = (tid % kWave) >> 4;
-  const Power lam = power(log_decay, h, sq.run);
+                                                              int H, int state) {
+  const int parts = state / 4 / kThreads;
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % H;
+  float* slots = ws.w[blockIdx.x / parts / H].slots;
+  const int64_t step = (int64_t)H * state;
   for (int i = blockIdx.y; i < sq.nseq; i += gridDim.y) {
     const int64_t t0 = sq.at(i), len = sq.at(i + 1) - t0;
     if (len <= sq.run) continue;
-    const int nruns = (int)((len + sq.run - 1) / sq.run);
-    float* slot = w.slots + (2 * t0 / sq.run * H + h) * K * V + (part * kThreads + tid) * 4;
-    const int64_t step = (int64_t)H * K * V;
-    f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (w.start != nullptr) {
-      const float* start = w.start + ((int64_t)i * H + h) * K * V;
-      // `part` is yb NZ + nz of the walk's own shape
-      if (w.turned) {
-        using S = Shape2<V, K, BF16>;
-        const int y = 16 * (part / S::NZ) + 4 * lq, z = S::zcol(wave, part % S::NZ, lr);
-        m = *(const f32x4*)(start + z * V + y);
-      } else {
-        using S = Shape2<K, V, BF16>;
-        const int y = 16 * (part / S::NZ) + 4 * lq, z = S::zcol(wave, part % S::NZ, lr);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[r] = start[(y + r) * V + z];
-      }
-    }
-    *(f32x4*)slot = m;
-#pragma unroll 4
-    for (int r = 1; r < nruns; ++r) {
+    const int each = run_length(sq, len);
+    const int nruns = (int)((len + each - 1) / each);
+    if (nruns <= kFold) continue;
+    const Power lam = power(log_decay, h, each);
+    float* slot = slots + 2 * t0 / sq.run * step + (int64_t)h * state +
+                  (part * kThreads + (int)threadIdx.x) * 4;
+    f32x4 m = *(const f32x4*)(slot + step);
+#pragma unroll 8
+    for (int r = 2; r < nruns; ++r) {
       const f32x4 add = *(const f32x4*)(slot + r * step);
 #pragma unroll
       for (int e = 0; e < 4; ++e) m[e] = times(lam, m[e]) + add[e];
@@ -719,7 +785,7 @@ __global__ __launch_bounds__(256) void sum_heads_kernel(const float* __restrict_
 // thirds of a run allowed for the end of each sequence; at least four chunks (the
 // states at a run's ends cost about as much traffic as four chunks' tokens).
 constexpr int64_t kWantRuns = 512;
-constexpr int64_t kMinChunks = 4;
+constexpr int64_t kMinChunks = 8;
 
 int run_tokens(const LinattnShape& s, bool bf16, int walks) {
   const int64_t C = bf16 ? 64 : 32;
@@ -736,32 +802,36 @@ int64_t slots_of(const LinattnShape& s, int run) {
   return s.tokens <= run ? 0 : 2 * s.tokens / run + 2;
 }
 
-template <int K, int V, bool BF16, int NW>
-int launch_walks(const Walks& w, const Seqs& sq, const float* ld, const LinattnShape& s,
-                 hipStream_t st) {
+// `states`: the walks whose runs' states are formed (their slots_t serve the
+// others).
+template <int K, int V, bool BF16, int NW, int NS>
+int launch_walks(const Walks& w, const Walks& states, const Seqs& sq, const float* ld,
+                 const LinattnShape& s, hipStream_t st) {
   const int H = (int)s.nheads;
   const int64_t items = s.tokens / sq.run + s.nseq;
-  const dim3 grid((unsigned)(items * H * NW)), block(kThreads);
-  // no sequence of these is longer than a run
-  const bool whole = (sq.cu == nullptr ? sq.len : s.tokens) <= sq.run;
-  if (!whole) {
-    hipLaunchKernelGGL((walk_kernel<K, V, BF16, NW, false>), grid, block, 0, st, w, sq, ld, H);
-    const unsigned parts = (unsigned)(K * V / 4 / kThreads * H * NW);
-    hipLaunchKernelGGL((run_starts_kernel<K, V, BF16>),
-                       dim3(parts, (unsigned)(s.nseq < 8 ? s.nseq : 8)), block, 0, st, w, sq, ld,
-                       H);
+  const dim3 block(kThreads);
+  const int64_t longest = sq.cu == nullptr ? sq.len : s.tokens;   // that a sequence may be
+  if (longest > sq.run) {
+    hipLaunchKernelGGL((walk_kernel<K, V, BF16, NS, false>), dim3((unsigned)(items * H * NS)),
+                       block, 0, st, states, sq, ld, H);
+    if (longest > (int64_t)kFold * sq.run) {
+      const unsigned parts = (unsigned)(K * V / 4 / kThreads * H * NW);
+      hipLaunchKernelGGL(run_starts_kernel, dim3(parts, (unsigned)(s.nseq < 8 ? s.nseq : 8)),
+                         block, 0, st, w, sq, ld, H, K * V);
+    }
   }
-  hipLaunchKernelGGL((walk_kernel<K, V, BF16, NW, true>), grid, block, 0, st, w, sq, ld, H);
+  hipLaunchKernelGGL((walk_kernel<K, V, BF16, NW, true>), dim3((unsigned)(items * H * NW)), block,
+                     0, st, w, sq, ld, H);
   return (int)hipGetLastError();
 }
 
-template <int NW>
-int walks_of(const Walks& w, const Seqs& sq, const float* ld, bool bf16, const LinattnShape& s,
-             hipStream_t st) {
+template <int NW, int NS>
+int walks_of(const Walks& w, const Walks& states, const Seqs& sq, const float* ld, bool bf16,
+             const LinattnShape& s, hipStream_t st) {
   auto go = [&](auto k, auto v) {
     constexpr int K = decltype(k)::value, V = decltype(v)::value;
-    return bf16 ? launch_walks<K, V, true, NW>(w, sq, ld, s, st)
-                : launch_walks<K, V, false, NW>(w, sq, ld, s, st);
+    return bf16 ? launch_walks<K, V, true, NW, NS>(w, states, sq, ld, s, st)
+                : launch_walks<K, V, false, NW, NS>(w, states, sq, ld, s, st);
   };
   using I64 = std::integral_constant<int, 64>;
   using I128 = std::integral_constant<int, 128>;
@@ -783,8 +853,8 @@ int sum_heads(const float* part, void* out, const Seqs& sq, bool bf16, const Lin
   return (int)hipGetLastError();
 }
 
-Seqs seqs_of(const int32_t* cu, const LinattnShape& s, int run) {
-  return Seqs{cu, s.tokens, s.tokens / s.nseq, (int)s.nseq, run};
+Seqs seqs_of(const int32_t* cu, const LinattnShape& s, int run, bool bf16) {
+  return Seqs{cu, s.tokens, s.tokens / s.nseq, (int)s.nseq, run, bf16 ? 64 : 32};
 }
 
 size_t slot_floats(const LinattnShape& s, int run) {
@@ -806,10 +876,10 @@ int launch_linattn_fwd(const void* q, const void* k, const void* v, const float*
   clear_launch_error();
   const int share = (int)(s.nheads / s.ngroups);
   Walks w{};
-  w.w[0] = Walk{q, k, v, o, init, fin, (float*)ws, share, share, 1, 1, scale, 1.0f, false, false,
-                false};
-  return walks_of<1>(w, seqs_of(cu, s, run_tokens(s, bf16, 1)), log_decay, bf16, s,
-                     (hipStream_t)stream);
+  w.w[0] = Walk{q,     k,     v, o, init,  fin,  (float*)ws, nullptr,
+                share, share, 1, 1, scale, 1.0f, false,      false, false};
+  return walks_of<1, 1>(w, w, seqs_of(cu, s, run_tokens(s, bf16, 1), bf16), log_decay, bf16, s,
+                        (hipStream_t)stream);
 }
 
 int launch_linattn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -825,15 +895,19 @@ int launch_linattn_bwd(const void* q, const void* k, const void* v, const float*
   float* slots = (float*)ws;
   float* pq = slots + 3 * one;
   float* pk = pq + (size_t)s.tokens * s.nheads * s.dk;
-  const Seqs sq = seqs_of(cu, s, run);
-  Walks w{};
-  w.w[0] = Walk{dout, v,     k, parts ? (void*)pq : dq, init, nullptr, slots,
-                1,    1, share, parts ? 1 : share,      scale, 1.0f,   false, true, parts};
-  w.w[1] = Walk{v, dout,  q, parts ? (void*)pk : dk, dfinal, nullptr, slots + one,
-                1, 1, share, parts ? 1 : share,      1.0f,   scale,   true, true, parts};
-  w.w[2] = Walk{k,     q,     dout, dv, dfinal, dinit, slots + 2 * one,
-                share, share, 1,    1,  1.0f,   scale, true, false, false};
-  int err = walks_of<3>(w, sq, log_decay, bf16, s, st);
+  const Seqs sq = seqs_of(cu, s, run, bf16);
+  Walks w{}, states{};
+  w.w[0] = Walk{dout, v,     k, parts ? (void*)pq : dq, init,  nullptr, slots, nullptr, 1,
+                1,    share, parts ? 1 : share,         scale, 1.0f,    false, true,    parts};
+  w.w[1] = Walk{v, dout,  q, parts ? (void*)pk : dk, dfinal, nullptr, slots + one, nullptr, 1,
+                1, share, parts ? 1 : share,         1.0f,   scale,   true,        true,    parts};
+  w.w[2] = Walk{k,     q, dout, dv,   dfinal, dinit, slots + 2 * one, nullptr, share,
+                share, 1, 1,    1.0f, scale,  true,  false,           false};
+  // dk walks with the transpose of dv's M, whose runs' states serve both
+  states.w[0] = w.w[0];
+  states.w[1] = w.w[2];
+  states.w[1].slots_t = w.w[1].slots;
+  int err = walks_of<3, 2>(w, states, sq, log_decay, bf16, s, st);
   if (err == 0 && parts) err = sum_heads(pq, dq, sq, bf16, s, st);
   if (err == 0 && parts) err = sum_heads(pk, dk, sq, bf16, s, st);
   return err;

@@ -94,6 +94,9 @@ def test_linattn_rejects_bad_arguments():
     assert bwd(d, init=MISALIGNED) == INV and bwd(d, dfin=MISALIGNED) == INV
     assert bwd(d, dinit=MISALIGNED) == INV
     assert fwd(d, cu=ODD) == INV and bwd(d, cu=ODD) == INV
+    # dinit over dfinal, whole or in part
+    assert bwd(d, dfin=FAKE, dinit=FAKE) == INV
+    assert bwd(d, dfin=FAKE, dinit=ctypes.c_void_p(FAKE.value + 4096)) == INV
     # sequences of equal length: tokens must divide by their number
     assert fwd(ldims(nseq=3)) == INV and bwd(ldims(nseq=3)) == INV
     assert fwd(ldims(nseq=0)) == INV and bwd(ldims(nseq=1 << 31)) == INV
