@@ -178,7 +178,9 @@ struct Shape2 {
   static constexpr int ZBYTES = C * ZS * ES;
   static constexpr int PBYTES = (BF16 ? 2 : 1) * C * PS * ES;   // the scores, bf16 as two terms
   static constexpr int WBYTES = C * 4;                          // the weights of Z
-  static constexpr int BYTES = 2 * XBYTES + ZBYTES + PBYTES + WBYTES;
+  // the scores take the place of X once it is read
+  static constexpr int BYTES =
+      WBYTES + XBYTES + ZBYTES + (XBYTES > PBYTES ? XBYTES : PBYTES);
   static constexpr int STATE_BYTES = XBYTES + ZBYTES + WBYTES;
   static constexpr int YU = C * YD * ES / 16 / kThreads;   // 16-byte units per thread
   static constexpr int ZU = C * ZD * ES / 16 / kThreads;
@@ -212,23 +214,23 @@ template <int D, int C, int ES, int U>
 struct Tile {
   u32x4 v[U];
   __device__ __forceinline__ void issue(const void* base, int64_t heads, int head, int64_t lowest,
-                                        int n, bool down) {
+                                        int n, bool down, int tid) {
     const uint32_t row = (uint32_t)(heads * D * ES);
     const rsrc_t r = make_rsrc((const char*)base + (lowest * heads + head) * (D * ES),
                                (uint32_t)(n - 1) * row + D * ES);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int u = (int)threadIdx.x + kThreads * j;
+      const int u = tid + kThreads * j;
       const int i = u / (D * ES / 16), c = u % (D * ES / 16);
       const uint32_t off = (uint32_t)(down ? n - 1 - i : i) * row + c * 16;
       v[j] = load_b128(r, i < n ? off : kPastRange);
     }
   }
   template <bool SLOTS>
-  __device__ __forceinline__ void commit(char* lds, int stride) const {
+  __device__ __forceinline__ void commit(char* lds, int stride, int tid) const {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int u = (int)threadIdx.x + kThreads * j;
+      const int u = tid + kThreads * j;
       const int i = u / (D * ES / 16), c = u % (D * ES / 16);
       char* row = lds + i * stride * ES;
       if constexpr (SLOTS) {
@@ -245,9 +247,9 @@ struct Tile {
 // chunk and four columns of the wave's block nz.
 template <int YD, int ZD, bool BF16, int NB, int NZ>
 __device__ __forceinline__ void store_rows(const Walk& w, const f32x4 (&o)[NB][NZ],
-                                           int64_t lowest, int n, int h, int H, int wave) {
+                                           int64_t lowest, int n, int h, int H, int wave,
+                                           int lr, int lq) {
   using S = Shape2<YD, ZD, BF16>;
-  const int lane = threadIdx.x % kWave, lr = lane & 15, lq = lane >> 4;
   const int64_t oheads = H / w.oshare;
   const bool f32o = !BF16 || w.f32out;
   const int oes = f32o ? 4 : 2;
@@ -314,7 +316,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   char* ys = lds + S::WBYTES;
   char* zs = ys + S::XBYTES;
   char* xs = zs + S::ZBYTES;
-  char* ps = xs + S::XBYTES;
+  char* ps = xs;
 
   // Whether M goes on to a state in memory, where fp32 is asked for, or only
   // into outputs of the tensors' type.
@@ -383,50 +385,51 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     }
   }
 
-  // Decays of the scores, on the diagonal block and one block below it (each
-  // further block: lam^16 more), and of X^T M by token.
-  float dec0[4], dec1[4], ex[NB];
   const float cs = w.cx * w.cz;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int d = lr - 4 * lq - r;
-    dec0[r] = d >= 0 ? cs * exp2_hw(l2 * (float)d) : 0.0f;
-    dec1[r] = cs * exp2_hw(l2 * (float)(16 + d));
-  }
-#pragma unroll
-  for (int b = 0; b < NB; ++b) ex[b] = w.cx * exp2_hw(l2 * (float)(16 * b + lr + a));
   Factor lam{power(log_decay, h, C), 0.0f};
-
-  if constexpr (OUT && BF16) {
-    // score blocks (0, 1) and (2, 3) lie above the diagonal and are read
-    for (int u = tid; u < C * PS / 4; u += kThreads) *(u32x4*)(ps + 16 * u) = (u32x4){0, 0, 0, 0};
-  }
 
   Tile<YD, C, ES, S::YU> tx, ty;
   Tile<ZD, C, ES, S::ZU> tz;
   auto lowest_of = [&](int p, int n) {
     return w.down ? run.t0 + run.len - p0 - p - n : run.t0 + p0 + p;
   };
-  auto issue = [&](int p) {
+  auto issue = [&](int p, int tid) {
     const int n = len - p < C ? len - p : C;
     const int64_t lowest = lowest_of(p, n);
-    if constexpr (OUT) tx.issue(w.x, H / w.xshare, h / w.xshare, lowest, n, w.down);
-    ty.issue(w.y, H / w.yshare, h / w.yshare, lowest, n, w.down);
-    tz.issue(w.z, H / w.zshare, h / w.zshare, lowest, n, w.down);
+    if constexpr (OUT) tx.issue(w.x, H / w.xshare, h / w.xshare, lowest, n, w.down, tid);
+    ty.issue(w.y, H / w.yshare, h / w.yshare, lowest, n, w.down, tid);
+    tz.issue(w.z, H / w.zshare, h / w.zshare, lowest, n, w.down, tid);
   };
-  if (len > 0) issue(0);
+  if (len > 0) issue(0, tid);
   for (int p = 0; p < len; p += C) {
     const int n = len - p < C ? len - p : C;
+    // The thread's addresses are formed anew for every chunk: kept across chunks
+    // they would take some 50 registers and be spilled.
+    int fresh = tid;
+    asm volatile("" : "+v"(fresh));
+    const int lr = fresh & 15, lq = fresh >> 4 & 3;
     __syncthreads();
-    if constexpr (OUT) tx.template commit<BF16>(xs, YS);
-    ty.template commit<BF16>(ys, YS);
-    tz.template commit<false>(zs, ZS);
+    if constexpr (OUT) tx.template commit<BF16>(xs, YS, fresh);
+    ty.template commit<BF16>(ys, YS, fresh);
+    tz.template commit<false>(zs, ZS, fresh);
     if (tid < C) wtab[tid] = tid < n ? w.cz * exp2_hw(l2 * (float)(n - a - tid)) : 0.0f;
     __syncthreads();
     if constexpr (!BF16) {
-      if (p + C < len) issue(p + C);
+      if (p + C < len) issue(p + C, fresh);
     }
 
+    // Scores of tokens j = 4 lq + 0..3 of a block for token i = lr of the block
+    // `far` tokens on.  Where j > i the score is selected away, never multiplied
+    // by 0.
+    auto decayed = [&](f32x4& d, int far) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int dist = far + lr - 4 * lq - r;
+        const float v = d[r] * (cs * exp2_hw(l2 * (float)dist));
+        d[r] = dist >= 0 ? v : 0.0f;
+      }
+    };
+    auto out_decay = [&](int tb) { return w.cx * exp2_hw(l2 * (float)(16 * tb + lr + a)); };
     if constexpr (BF16) {
       const uint16_t* xl = (const uint16_t*)xs;
       const uint16_t* yl = (const uint16_t*)ys;
@@ -440,31 +443,21 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
       f32x4 o[NB][NZ] = {};
       if constexpr (OUT) {
         // (1) the ten score blocks on and below the diagonal, transposed (Y X^T),
-        // two or three per wave
-        auto score = [&](int id) {
+        // two or three per wave; they wait in registers until X is read
+        u32x2 sh[3], sl[3];
+        auto score = [&](int id, u32x2& hi, u32x2& lo) {
           const int tb = id > 5 ? 3 : id > 2 ? 2 : id > 0 ? 1 : 0, sb = id - tb * (tb + 1) / 2;
           f32x4 d = {};
 #pragma unroll
           for (int kk = 0; kk < NY / 2; ++kk)
             d = mfma_bf16(row_frag(yl, YS, 16 * sb + lr, kk), row_frag(xl, YS, 16 * tb + lr, kk),
                           d);
-          const float far = exp2_hw(l2 * (float)(16 * (tb > sb ? tb - sb - 1 : 0)));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            // where j > i the score is selected away, never multiplied by 0
-            const float v = d[r] * (tb > sb ? dec1[r] * far : dec0[r]);
-            d[r] = tb > sb || lr >= 4 * lq + r ? v : 0.0f;
-          }
-          u32x2 hi, lo;
+          decayed(d, 16 * (tb - sb));
           split4(d, hi, lo);
-          const int at = (16 * tb + lr) * PS + slot_of(16 * sb + 4 * lq);
-          *(u32x2*)(ph + at) = hi;
-          *(u32x2*)(pl + at) = lo;
         };
-        score(wave);
-        score(wave + 4);
-        __builtin_amdgcn_sched_barrier(0);
-        if (wave < 2) score(wave + 8);
+        score(wave, sh[0], sl[0]);
+        score(wave + 4, sh[1], sl[1]);
+        if (wave < 2) score(wave + 8, sh[2], sl[2]);
         __builtin_amdgcn_sched_barrier(0);
         // (2) X^T M, transposed, for all tokens
 #pragma unroll
@@ -487,8 +480,23 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
+          const float ex = out_decay(tb);
 #pragma unroll
-          for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex[tb];
+          for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          const int id = wave + 4 * e;
+          if (id > 9) break;
+          const int tb = id > 5 ? 3 : id > 2 ? 2 : id > 0 ? 1 : 0, sb = id - tb * (tb + 1) / 2;
+          const int at = (16 * tb + lr) * PS + slot_of(16 * sb) + 8 * lq;
+          *(u32x2*)(ph + at) = sh[e];
+          *(u32x2*)(pl + at) = sl[e];
+          if (sb == tb && tb % 2 == 0) {   // the block above the diagonal is read too
+            *(u32x2*)(ph + at + 4) = (u32x2){0, 0};
+            *(u32x2*)(pl + at + 4) = (u32x2){0, 0};
+          }
         }
         __syncthreads();
       }
@@ -515,13 +523,13 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
             }
           }
         }
-        store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave);
+        store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave, lr, lq);
         __builtin_amdgcn_sched_barrier(0);   // o's registers are free from here on
       }
-      if (p + C < len) issue(p + C);
+      if (p + C < len) issue(p + C, fresh);
       // (4) M = lam^n M + Y^T (wz o Z), the decayed Z as two bf16 terms, and a third
       // where `exact`
-      const float f = n == C ? lam.next() : power(log_decay, h, n).hi;
+      const float f = n == C ? lam.next() : exp2_hw(l2 * (float)n);
 #pragma unroll
       for (int yb = 0; yb < NY; ++yb) {
 #pragma unroll
@@ -553,8 +561,8 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
             u32x4 yf[YG];
 #pragma unroll
             for (int y = 0; y < YG; ++y) {
-              const uint16_t* yp = yl + (32 * kk + 4 * lq + (lr >> 2)) * YS +
-                                   slot_of(16 * (y0 + y) + 4 * (lr & 3));
+              const uint16_t* yp = yl + (32 * kk + 4 * lq + (lr >> 2)) * YS + 8 * (lr & 3) +
+                                   slot_of(16 * (y0 + y));
               yf[y] = join(lds_read_tr16(yp), lds_read_tr16(yp + 16 * YS));
             }
 #pragma unroll
@@ -587,9 +595,10 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
       f32x4 o[NB][NZ] = {};
       if constexpr (OUT) {
         // (1) the three score blocks of a chunk, one per wave
+        const int tb3 = (wave + 1) / 2, sb3 = wave / 2;
+        f32x4 d = {};
         if (wave < 3) {
-          const int tb = (wave + 1) / 2, sb = wave / 2;
-          f32x4 d = {};
+          const int tb = tb3, sb = sb3;
 #pragma unroll
           for (int yb = 0; yb < NY; ++yb) {
             const f32x4 xf = *(const f32x4*)(xl + (16 * tb + lr) * YS + 16 * yb + 4 * lq);
@@ -597,10 +606,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
 #pragma unroll
             for (int r = 0; r < 4; ++r) d = mfma_f32(yf[r], xf[r], d);
           }
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            d[r] = sb < tb ? d[r] * dec1[r] : lr >= 4 * lq + r ? d[r] * dec0[r] : 0.0f;
-          *(f32x4*)(pl + (16 * tb + lr) * PS + 16 * sb + 4 * lq) = d;
+          decayed(d, 16 * (tb - sb));
         }
         // (2) X^T M
 #pragma unroll
@@ -617,9 +623,12 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
+          const float ex = out_decay(tb);
 #pragma unroll
-          for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex[tb];
+          for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex;
         }
+        __syncthreads();
+        if (wave < 3) *(f32x4*)(pl + (16 * tb3 + lr) * PS + 16 * sb3 + 4 * lq) = d;
         __syncthreads();
       }
       // (3)
@@ -647,7 +656,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
 #pragma unroll
         for (int nz = 0; nz < NZ; ++nz) zf[sb][nz] *= wv;
       }
-      const float f = n == C ? lam.next() : power(log_decay, h, n).hi;
+      const float f = n == C ? lam.next() : exp2_hw(l2 * (float)n);
 #pragma unroll
       for (int yb = 0; yb < NY; ++yb) {
 #pragma unroll
@@ -662,7 +671,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           }
         }
       }
-      if constexpr (OUT) store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave);
+      if constexpr (OUT) store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave, lr, lq);
     }
   }
 
@@ -698,12 +707,17 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   }
 }
 
+// Workgroups of a CU: what the registers of M leave room for (a workgroup has one
+// wave on each SIMD), and the LDS.
+template <int K, int V>
+constexpr int resident() { return K == 128 && V == 128 ? 2 : 3; }
+
 // Workgroup (item, walk, head), the head fastest.  Blocks are dealt to the 8 XCDs
 // in turn, so with H a multiple of 8 every XCD gets the walks of H/8 consecutive
 // heads, which share operands.  Items without a run (up to nseq of them) come
 // last: in between they would leave CUs with one workgroup and others with three.
 template <int K, int V, bool BF16, int NW, bool OUT>
-__global__ __launch_bounds__(kThreads, 2) void walk_kernel(Walks ws, Seqs sq,
+__global__ __launch_bounds__(kThreads, (resident<K, V>())) void walk_kernel(Walks ws, Seqs sq,
                                                         const float* __restrict__ log_decay,
                                                         int H) {
   using SA = Shape2<K, V, BF16>;
@@ -780,16 +794,18 @@ __global__ __launch_bounds__(256) void sum_heads_kernel(const float* __restrict_
   }
 }
 
-// Tokens of a run: whole chunks, as few as keep the runs of all walks within
-// two workgroups per CU (a few more would wait for a second round), with two
-// thirds of a run allowed for the end of each sequence; at least four chunks (the
-// states at a run's ends cost about as much traffic as four chunks' tokens).
-constexpr int64_t kWantRuns = 512;
+// Tokens of a run: whole chunks, as few as keep the runs of all walks within the
+// workgroups the 256 CUs hold at once (a few more would wait for a second round),
+// with two thirds of a run allowed for the end of each sequence; at least eight
+// chunks (a shorter run costs more in states and in the launch that forms them
+// than it saves).
+constexpr int64_t kCus = 256;
 constexpr int64_t kMinChunks = 8;
 
 int run_tokens(const LinattnShape& s, bool bf16, int walks) {
   const int64_t C = bf16 ? 64 : 32;
-  const int64_t each = 3 * kWantRuns / (s.nheads * walks);     // thirds of runs for a head
+  const int64_t wgs = kCus * (s.dk == 128 && s.dv == 128 ? resident<128, 128>() : resident<64, 64>());
+  const int64_t each = 3 * wgs / (s.nheads * walks);           // thirds of runs for a head
   const int64_t ends = 2 * s.nseq < each / 2 ? 2 * s.nseq : each / 2;
   int64_t chunks = each > ends ? (3 * s.tokens + (each - ends) * C - 1) / ((each - ends) * C)
                                : (s.tokens + C - 1) / C;
