@@ -547,30 +547,44 @@ _FLOATS = (torch.float32, torch.bfloat16)
 _F32 = (torch.float32,)
 
 
+def _arg(t, name: str, shape, dtypes, device, optional: bool = False):
+    """The address of a tensor that passes ``_check`` (None of an optional one).
+    These calls take some microseconds: what is checked is looked at once here,
+    and ``_check`` finds the words where something is wrong."""
+    if type(t) is torch.Tensor and t.dtype in dtypes and t.device == device and \
+            (shape is None or t.shape == shape) and t.is_cuda and t.is_contiguous():
+        p = t.data_ptr()
+        if p % 16 == 0:
+            return p
+    _check(t, name, shape, dtypes, device, optional)
+    return None if t is None else t.data_ptr()
+
+
 def _call(where: str, dev: torch.device, *args) -> None:
     """The entry point on the current stream of ``dev``, which need not be the
     current device."""
     f = getattr(_lib, where)
+    # the handle that torch.cuda.current_stream(dev) wraps, without the wrapping
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index == torch.cuda.current_device():
-        st = f(*args, _stream(dev))
+        st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream(dev))
-    _raise(st, where)
+            st = f(*args, stream)
+    if st != SSD_OK:
+        raise SsdError(st, where)
 
 
-def _linattn_check(q, k, v, log_decay, init_state, cu_seqlens) -> LinattnDims:
-    """The dims of a linear attention call, its inputs checked."""
+def _linattn_args(q, k, v, log_decay, init_state, cu_seqlens):
+    """The dims of a linear attention call and the addresses of its inputs."""
     for t, name in ((q, "q"), (v, "v")):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a tensor [batch, seqlen, heads, size]")
     b, L, G, K = q.shape
     H, V = v.shape[2:]
-    dev = q.device
-    _check(q, "q", None, _FLOATS)
-    _check(k, "k", (b, L, G, K), (q.dtype,), dev)
-    _check(v, "v", (b, L, H, V), (q.dtype,), dev)
-    _check(log_decay, "log_decay", (H,), _F32, dev)
+    dev, own = q.device, (q.dtype,)
+    ptrs = [_arg(q, "q", None, _FLOATS, dev), _arg(k, "k", (b, L, G, K), own, dev),
+            _arg(v, "v", (b, L, H, V), own, dev), _arg(log_decay, "log_decay", (H,), _F32, dev)]
     nseq = b
     if cu_seqlens is not None:
         if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 \
@@ -578,10 +592,10 @@ def _linattn_check(q, k, v, log_decay, init_state, cu_seqlens) -> LinattnDims:
             raise ValueError("cu_seqlens must be a tensor [sequences + 1]")
         if b != 1:
             raise ValueError(f"packed sequences need a batch of 1, not {b}")
-        _check(cu_seqlens, "cu_seqlens", None, (torch.int32,), dev)
         nseq = cu_seqlens.numel() - 1
-    _check(init_state, "init_state", (nseq, H, K, V), _F32, dev, optional=True)
-    return LinattnDims(b * L, nseq, H, G, K, V)
+    cu = _arg(cu_seqlens, "cu_seqlens", None, (torch.int32,), dev, optional=True)
+    ptrs += [_arg(init_state, "init_state", (nseq, H, K, V), _F32, dev, optional=True), cu]
+    return LinattnDims(b * L, nseq, H, G, K, V), ptrs
 
 
 def linattn_workspace_bytes(d: LinattnDims, dtype: torch.dtype, backward: bool = False) -> int:
@@ -590,8 +604,27 @@ def linattn_workspace_bytes(d: LinattnDims, dtype: torch.dtype, backward: bool =
     return int(f(ctypes.byref(d), _dtype_code(dtype)))
 
 
-def _scale(scale: Optional[float], K: int):
-    return ctypes.c_float(K ** -0.5 if scale is None else scale)
+def _workspace(t: torch.Tensor, dev: torch.device):
+    p = _arg(t, "workspace", None, (torch.uint8, torch.float32), dev)
+    return p, t.numel() * t.element_size()
+
+
+def _run_linattn_fwd(d, ins, v, o, final_state, workspace, scale) -> None:
+    dev = v.device
+    _call("ssd_linattn_fwd", dev, *ins, _arg(o, "o", v.shape, (v.dtype,), dev),
+          _arg(final_state, "final_state", (d.nseq, d.nheads, d.dk, d.dv), _F32, dev, True),
+          *_workspace(workspace, dev), d.dk ** -0.5 if scale is None else scale,
+          _dtype_code(v.dtype), d)
+
+
+def _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit, workspace, scale) -> None:
+    dev, own = v.device, (v.dtype,)
+    state = (d.nseq, d.nheads, d.dk, d.dv)
+    _call("ssd_linattn_bwd", dev, *ins, _arg(dout, "dout", v.shape, own, dev),
+          _arg(dfinal, "dfinal", state, _F32, dev, True), _arg(dq, "dq", q.shape, own, dev),
+          _arg(dk, "dk", q.shape, own, dev), _arg(dv, "dv", v.shape, own, dev),
+          _arg(dinit, "dinit", state, _F32, dev, True), *_workspace(workspace, dev),
+          d.dk ** -0.5 if scale is None else scale, _dtype_code(v.dtype), d)
 
 
 def ssd_linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -606,16 +639,8 @@ def ssd_linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     the sequences are packed in a batch of 1; else each batch row is one.
     ``workspace`` has linattn_workspace_bytes(dims, dtype) bytes.  scale None:
     K^-0.5."""
-    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
-    dev = q.device
-    _check(o, "o", tuple(v.shape), (q.dtype,), dev)
-    _check(final_state, "final_state", (d.nseq, d.nheads, d.dk, d.dv), _F32, dev, optional=True)
-    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
-    nbytes = workspace.numel() * workspace.element_size()
-    _call("ssd_linattn_fwd", dev,
-          _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(init_state), _ptr(cu_seqlens),
-          _ptr(o), _ptr(final_state), _ptr(workspace), nbytes, _scale(scale, d.dk),
-          _dtype_code(q.dtype), ctypes.byref(d))
+    d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
+    _run_linattn_fwd(d, ins, v, o, final_state, workspace, scale)
 
 
 def ssd_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -626,22 +651,8 @@ def ssd_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     workspace: torch.Tensor, scale: Optional[float] = None) -> None:
     """Gradients of ``ssd_linattn_fwd`` for dout [b, L, H, V] and dfinal (or
     None) into dq, dk, dv and dinit (or None).  log_decay has none."""
-    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
-    dev = q.device
-    own = (q.dtype,)
-    state = (d.nseq, d.nheads, d.dk, d.dv)
-    _check(dout, "dout", tuple(v.shape), own, dev)
-    _check(dfinal, "dfinal", state, _F32, dev, optional=True)
-    _check(dq, "dq", tuple(q.shape), own, dev)
-    _check(dk, "dk", tuple(q.shape), own, dev)
-    _check(dv, "dv", tuple(v.shape), own, dev)
-    _check(dinit, "dinit", state, _F32, dev, optional=True)
-    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
-    nbytes = workspace.numel() * workspace.element_size()
-    _call("ssd_linattn_bwd", dev,
-          _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(init_state), _ptr(cu_seqlens),
-          _ptr(dout), _ptr(dfinal), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dinit), _ptr(workspace),
-          nbytes, _scale(scale, d.dk), _dtype_code(q.dtype), ctypes.byref(d))
+    d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
+    _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit, workspace, scale)
 
 
 def ssd_linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -655,17 +666,13 @@ def ssd_linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             raise ValueError(f"{name} must be a tensor [batch, heads, size]")
     b, G, K = q.shape
     H, V = v.shape[1:]
-    dev = q.device
-    _check(q, "q", None, _FLOATS)
-    _check(k, "k", (b, G, K), (q.dtype,), dev)
-    _check(v, "v", (b, H, V), (q.dtype,), dev)
-    _check(log_decay, "log_decay", (H,), _F32, dev)
-    _check(state, "state", (b, H, K, V), _F32, dev)
-    _check(o, "o", (b, H, V), (q.dtype,), dev)
-    d = LinattnDims(b, b, H, G, K, V)
-    _call("ssd_linattn_step", dev,
-          _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o), _scale(scale, K),
-          _dtype_code(q.dtype), ctypes.byref(d))
+    dev, own = q.device, (q.dtype,)
+    _call("ssd_linattn_step", dev, _arg(q, "q", None, _FLOATS, dev),
+          _arg(k, "k", q.shape, own, dev), _arg(v, "v", (b, H, V), own, dev),
+          _arg(log_decay, "log_decay", (H,), _F32, dev),
+          _arg(state, "state", (b, H, K, V), _F32, dev), _arg(o, "o", v.shape, own, dev),
+          K ** -0.5 if scale is None else scale, _dtype_code(q.dtype),
+          LinattnDims(b, b, H, G, K, V))
 
 
 def _rows(x: torch.Tensor, name: str) -> Tuple[int, int]:
@@ -684,21 +691,15 @@ def ssd_add_norm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor],
     one (fp32 or bf16 each); res_scale and weight [dim] fp32.  residual,
     res_scale, weight and residual_out may be None."""
     rows, D = _rows(x, "x")
-    dev = x.device
-    shape = tuple(x.shape)
-    _check(x, "x", None, _FLOATS)
-    _check(residual, "residual", shape, _FLOATS, dev, optional=True)
-    _check(res_scale, "res_scale", (D,), _F32, dev, optional=True)
-    _check(weight, "weight", (D,), _F32, dev, optional=True)
-    _check(y, "y", shape, (x.dtype,), dev)
-    rdt = residual.dtype if residual is not None else None
-    _check(residual_out, "residual_out", shape, _FLOATS if rdt is None else (rdt,), dev,
-           optional=True)
-    if rdt is None:
-        rdt = x.dtype if residual_out is None else residual_out.dtype
-    _call("ssd_add_norm_fwd", dev,
-          _ptr(x), _ptr(residual), _ptr(res_scale), _ptr(weight), _ptr(y), _ptr(residual_out),
-          rows, D, eps, _dtype_code(x.dtype), _dtype_code(rdt))
+    dev, shape, own = x.device, x.shape, (x.dtype,)
+    rdts = _FLOATS if residual is None else (residual.dtype,)
+    rdt = next((t.dtype for t in (residual, residual_out) if t is not None), x.dtype)
+    _call("ssd_add_norm_fwd", dev, _arg(x, "x", None, _FLOATS, dev),
+          _arg(residual, "residual", shape, _FLOATS, dev, True),
+          _arg(res_scale, "res_scale", (D,), _F32, dev, True),
+          _arg(weight, "weight", (D,), _F32, dev, True), _arg(y, "y", shape, own, dev),
+          _arg(residual_out, "residual_out", shape, rdts, dev, True), rows, D, eps,
+          _dtype_code(x.dtype), _dtype_code(rdt))
 
 
 def ssd_add_norm_bwd(x: torch.Tensor, residual: Optional[torch.Tensor],
@@ -710,26 +711,19 @@ def ssd_add_norm_bwd(x: torch.Tensor, residual: Optional[torch.Tensor],
     """Gradients of ``ssd_add_norm_fwd`` from its inputs.  ``workspace`` has
     add_norm_workspace_bytes(rows, dim) bytes."""
     rows, D = _rows(x, "x")
-    dev = x.device
-    shape = tuple(x.shape)
-    _check(x, "x", None, _FLOATS)
-    _check(residual, "residual", shape, _FLOATS, dev, optional=True)
-    _check(res_scale, "res_scale", (D,), _F32, dev, optional=True)
-    _check(weight, "weight", (D,), _F32, dev, optional=True)
-    _check(dy, "dy", shape, (x.dtype,), dev)
-    rdts = _FLOATS if residual is None else (residual.dtype,)
-    _check(dresidual_out, "dresidual_out", shape, rdts, dev, optional=True)
-    _check(dx, "dx", shape, (x.dtype,), dev)
-    _check(dresidual, "dresidual", shape, rdts, dev, optional=True)
-    _check(dres_scale, "dres_scale", (D,), _F32, dev, optional=True)
-    _check(dweight, "dweight", (D,), _F32, dev, optional=True)
-    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
+    dev, shape, own = x.device, x.shape, (x.dtype,)
     rdt = next((t.dtype for t in (residual, dresidual_out) if t is not None), x.dtype)
-    nbytes = workspace.numel() * workspace.element_size()
-    _call("ssd_add_norm_bwd", dev,
-          _ptr(x), _ptr(residual), _ptr(res_scale), _ptr(weight), _ptr(dy), _ptr(dresidual_out),
-          _ptr(dx), _ptr(dresidual), _ptr(dres_scale), _ptr(dweight), _ptr(workspace), nbytes,
-          rows, D, eps, _dtype_code(x.dtype), _dtype_code(rdt))
+    rdts = _FLOATS if residual is None else (rdt,)
+    _call("ssd_add_norm_bwd", dev, _arg(x, "x", None, _FLOATS, dev),
+          _arg(residual, "residual", shape, _FLOATS, dev, True),
+          _arg(res_scale, "res_scale", (D,), _F32, dev, True),
+          _arg(weight, "weight", (D,), _F32, dev, True), _arg(dy, "dy", shape, own, dev),
+          _arg(dresidual_out, "dresidual_out", shape, rdts, dev, True),
+          _arg(dx, "dx", shape, own, dev),
+          _arg(dresidual, "dresidual", shape, (rdt,), dev, True),
+          _arg(dres_scale, "dres_scale", (D,), _F32, dev, True),
+          _arg(dweight, "dweight", (D,), _F32, dev, True), *_workspace(workspace, dev), rows, D,
+          eps, _dtype_code(x.dtype), _dtype_code(rdt))
 
 
 def add_norm_workspace_bytes(rows: int, dim: int) -> int:
@@ -742,20 +736,20 @@ def _gate(gate: str) -> int:
     return SSD_GATES[gate]
 
 
-def _gated_check(x, z, weight, group) -> GatedNormDims:
+def _gated_args(x, z, weight, group):
+    """The dims of a gated norm and the addresses of its inputs."""
     rows, D = _rows(x, "x")
     dev = x.device
     group = D if group is None else int(group)
-    _check(x, "x", None, _FLOATS)
-    _check(z, "z", tuple(x.shape), _FLOATS, dev, optional=True)
     wdim = D
     if weight is not None:
         if not isinstance(weight, torch.Tensor) or weight.dim() != 1 \
                 or weight.numel() not in (D, group):
             raise ValueError(f"weight must be a tensor [{D}] or [{group}]")
-        _check(weight, "weight", None, _F32, dev)
         wdim = weight.numel()
-    return GatedNormDims(rows, D, group, wdim)
+    return GatedNormDims(rows, D, group, wdim), [
+        _arg(x, "x", None, _FLOATS, dev), _arg(z, "z", x.shape, _FLOATS, dev, True),
+        _arg(weight, "weight", None, _F32, dev, True)]
 
 
 def ssd_gated_norm_fwd(x: torch.Tensor, z: Optional[torch.Tensor],
@@ -767,12 +761,11 @@ def ssd_gated_norm_fwd(x: torch.Tensor, z: Optional[torch.Tensor],
     y = norm(x) o weight o act(z).  z (or None: no gate) and y share a type,
     which x need not have; weight [dim] or [group] fp32 or None; gate "silu"
     or "sigmoid"."""
-    d = _gated_check(x, z, weight, group)
+    d, ins = _gated_args(x, z, weight, group)
     dev = x.device
-    _check(y, "y", tuple(x.shape), _FLOATS if z is None else (z.dtype,), dev)
-    _call("ssd_gated_norm_fwd", dev,
-          _ptr(x), _ptr(z), _ptr(weight), _ptr(y), eps, _gate(gate), int(gate_first),
-          _dtype_code(x.dtype), _dtype_code(y.dtype), ctypes.byref(d))
+    _call("ssd_gated_norm_fwd", dev, *ins,
+          _arg(y, "y", x.shape, _FLOATS if z is None else (z.dtype,), dev), eps, _gate(gate),
+          int(gate_first), _dtype_code(x.dtype), _dtype_code(y.dtype), d)
 
 
 def gated_norm_workspace_bytes(d: GatedNormDims) -> int:
@@ -787,23 +780,18 @@ def ssd_gated_norm_bwd(x: torch.Tensor, z: Optional[torch.Tensor],
                        gate_first: bool = False) -> None:
     """Gradients of ``ssd_gated_norm_fwd`` from its inputs.  ``workspace`` has
     gated_norm_workspace_bytes(dims) bytes."""
-    d = _gated_check(x, z, weight, group)
-    dev = x.device
-    shape = tuple(x.shape)
-    _check(dy, "dy", shape, _FLOATS if z is None else (z.dtype,), dev)
-    _check(dx, "dx", shape, (x.dtype,), dev)
+    d, ins = _gated_args(x, z, weight, group)
+    dev, shape = x.device, x.shape
     if (z is None) != (dz is None):
         raise ValueError("dz is given exactly when z is")
-    _check(dz, "dz", shape, (dy.dtype,), dev, optional=True)
-    if dweight is not None and dweight.dim() == 1 and weight is None:
+    if isinstance(dweight, torch.Tensor) and weight is None:
         d.weight_dim = dweight.numel()
-    _check(dweight, "dweight", (d.weight_dim,), _F32, dev, optional=True)
-    _check(workspace, "workspace", None, (torch.uint8, torch.float32), dev)
-    nbytes = workspace.numel() * workspace.element_size()
-    _call("ssd_gated_norm_bwd", dev,
-          _ptr(x), _ptr(z), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dweight),
-          _ptr(workspace), nbytes, eps, _gate(gate), int(gate_first), _dtype_code(x.dtype),
-          _dtype_code(dy.dtype), ctypes.byref(d))
+    _call("ssd_gated_norm_bwd", dev, *ins,
+          _arg(dy, "dy", shape, _FLOATS if z is None else (z.dtype,), dev),
+          _arg(dx, "dx", shape, (x.dtype,), dev), _arg(dz, "dz", shape, (dy.dtype,), dev, True),
+          _arg(dweight, "dweight", (d.weight_dim,), _F32, dev, True),
+          *_workspace(workspace, dev), eps, _gate(gate), int(gate_first), _dtype_code(x.dtype),
+          _dtype_code(dy.dtype), d)
 
 
 # ------------------------------------------------------------ convenience
@@ -845,11 +833,11 @@ def linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.
             scale: Optional[float] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Allocate and run ``ssd_linattn_fwd``: (o, final_state).  Rows of o outside
     every packed sequence are not written."""
-    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
+    d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
     o = torch.empty_like(v)
     final = torch.empty((d.nseq, d.nheads, d.dk, d.dv), dtype=torch.float32, device=q.device)
     ws = _bytes(linattn_workspace_bytes(d, q.dtype), q.device)
-    ssd_linattn_fwd(q, k, v, log_decay, init_state, cu_seqlens, o, final, ws, scale)
+    _run_linattn_fwd(d, ins, v, o, final, ws, scale)
     return o, final
 
 
@@ -861,12 +849,11 @@ def linattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                      scale: Optional[float] = None
                      ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """Allocate and run ``ssd_linattn_bwd``: (dq, dk, dv, dinit)."""
-    d = _linattn_check(q, k, v, log_decay, init_state, cu_seqlens)
+    d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dinit = torch.empty((d.nseq, d.nheads, d.dk, d.dv), dtype=torch.float32, device=q.device)
     ws = _bytes(linattn_workspace_bytes(d, q.dtype, backward=True), q.device)
-    ssd_linattn_bwd(q, k, v, log_decay, init_state, cu_seqlens, dout, dfinal, dq, dk, dv, dinit,
-                    ws, scale)
+    _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit, ws, scale)
     return dq, dk, dv, dinit
 
 
@@ -914,7 +901,7 @@ def gated_norm_backward(x: torch.Tensor, z: Optional[torch.Tensor],
                         gate_first: bool = False) -> Tuple[Optional[torch.Tensor], ...]:
     """Allocate and run ``ssd_gated_norm_bwd``: (dx, dz, dweight), None for each
     of the last two whose input is None."""
-    d = _gated_check(x, z, weight, group)
+    d, _ = _gated_args(x, z, weight, group)
     dx = torch.empty_like(x)
     dz, dw = (None if t is None else torch.empty_like(t) for t in (z, weight))
     ws = _bytes(gated_norm_workspace_bytes(d), x.device)

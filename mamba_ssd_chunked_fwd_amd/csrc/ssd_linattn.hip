@@ -800,7 +800,7 @@ __global__ __launch_bounds__(256) void sum_heads_kernel(const float* __restrict_
 // chunks (a shorter run costs more in states and in the launch that forms them
 // than it saves).
 constexpr int64_t kCus = 256;
-constexpr int64_t kMinChunks = 8;
+constexpr int64_t kMinChunks = 2;
 
 int run_tokens(const LinattnShape& s, bool bf16, int walks) {
   const int64_t C = bf16 ? 64 : 32;
