@@ -177,10 +177,11 @@ struct Shape2 {
   static constexpr int XBYTES = C * YS * ES;
   static constexpr int ZBYTES = C * ZS * ES;
   static constexpr int PBYTES = (BF16 ? 2 : 1) * C * PS * ES;   // the scores, bf16 as two terms
+  static constexpr int DBYTES = 3 * kWave * 16;                 // decays, four per lane
   static constexpr int WBYTES = C * 4;                          // the weights of Z
   // the scores take the place of X once it is read
   static constexpr int BYTES =
-      WBYTES + XBYTES + ZBYTES + (XBYTES > PBYTES ? XBYTES : PBYTES);
+      WBYTES + XBYTES + ZBYTES + (XBYTES > PBYTES ? XBYTES : PBYTES) + DBYTES;
   static constexpr int STATE_BYTES = XBYTES + ZBYTES + WBYTES;
   static constexpr int YU = C * YD * ES / 16 / kThreads;   // 16-byte units per thread
   static constexpr int ZU = C * ZD * ES / 16 / kThreads;
@@ -218,21 +219,31 @@ struct Tile {
     const uint32_t row = (uint32_t)(heads * D * ES);
     const rsrc_t r = make_rsrc((const char*)base + (lowest * heads + head) * (D * ES),
                                (uint32_t)(n - 1) * row + D * ES);
+    constexpr int PER = D * ES / 16, STEP = kThreads / PER;    // units of a row, rows at a time
+    const int i = tid / PER, c = tid % PER;
+    if (n == C) {                                              // the units' rows are STEP apart
+      const uint32_t off = (uint32_t)(down ? C - 1 - (U - 1) * STEP - i : i) * row + c * 16;
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int u = tid + kThreads * j;
-      const int i = u / (D * ES / 16), c = u % (D * ES / 16);
-      const uint32_t off = (uint32_t)(down ? n - 1 - i : i) * row + c * 16;
-      v[j] = load_b128(r, i < n ? off : kPastRange);
+      for (int j = 0; j < U; ++j)
+        v[j] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       r, (int)off, (int)((uint32_t)((down ? U - 1 - j : j) * STEP) * row), 0));
+    } else {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int ij = i + j * STEP;
+        const uint32_t off = (uint32_t)(down ? n - 1 - ij : ij) * row + c * 16;
+        v[j] = load_b128(r, ij < n ? off : kPastRange);
+      }
     }
   }
   template <bool SLOTS>
   __device__ __forceinline__ void commit(char* lds, int stride, int tid) const {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int u = tid + kThreads * j;
-      const int i = u / (D * ES / 16), c = u % (D * ES / 16);
-      char* row = lds + i * stride * ES;
+      constexpr int PER = D * ES / 16, STEP = kThreads / PER;
+      const int c = tid % PER;
+      char* row = lds + (tid / PER + j * STEP) * stride * ES;
       if constexpr (SLOTS) {
         *(u32x2*)(row + slot_of(8 * c) * 2) = (u32x2){v[j][0], v[j][1]};
         *(u32x2*)(row + slot_of(8 * c + 4) * 2) = (u32x2){v[j][2], v[j][3]};
@@ -256,25 +267,34 @@ __device__ __forceinline__ void store_rows(const Walk& w, const f32x4 (&o)[NB][N
   const uint32_t orow = (uint32_t)(oheads * ZD * oes);
   const rsrc_t orr = make_rsrc((char*)w.out + (lowest * oheads + h / w.oshare) * (ZD * oes),
                                (uint32_t)(n - 1) * orow + ZD * oes);
-#pragma unroll
-  for (int tb = 0; tb < NB; ++tb) {
-    const int i = 16 * tb + lr;
-    const uint32_t at = i < n ? (uint32_t)(w.down ? n - 1 - i : i) * orow : kPastRange;
+  auto store = [&](int tb, uint32_t at, int more) {
     if (f32o) {
 #pragma unroll
       for (int nz = 0; nz < NZ; ++nz)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[tb][nz]), orr,
-                                               (int)(at + S::zcol(wave, nz, 4 * lq) * 4), 0, 0);
+                                               (int)(at + S::zcol(wave, nz, 4 * lq) * 4), more, 0);
     } else {
       const int off = (int)(at + S::zcol(wave, 0, 4 * lq) * 2);
       const u32x2 a = {pack_bf16(o[tb][0][0], o[tb][0][1]), pack_bf16(o[tb][0][2], o[tb][0][3])};
       if constexpr (NZ == 2) {
         const u32x2 b = {pack_bf16(o[tb][1][0], o[tb][1][1]),
                          pack_bf16(o[tb][1][2], o[tb][1][3])};
-        __builtin_amdgcn_raw_buffer_store_b128((u32x4){a[0], a[1], b[0], b[1]}, orr, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128((u32x4){a[0], a[1], b[0], b[1]}, orr, off, more, 0);
       } else {
-        __builtin_amdgcn_raw_buffer_store_b64(a, orr, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(a, orr, off, more, 0);
       }
+    }
+  };
+  if (n == S::C) {                                             // blocks are 16 rows apart
+    const uint32_t at = (uint32_t)(w.down ? 15 - lr : lr) * orow;
+#pragma unroll
+    for (int tb = 0; tb < NB; ++tb)
+      store(tb, at, (int)((uint32_t)(w.down ? NB - 1 - tb : tb) * 16 * orow));
+  } else {
+#pragma unroll
+    for (int tb = 0; tb < NB; ++tb) {
+      const int i = 16 * tb + lr;
+      store(tb, i < n ? (uint32_t)(w.down ? n - 1 - i : i) * orow : kPastRange, 0);
     }
   }
 }
@@ -317,6 +337,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   char* zs = ys + S::XBYTES;
   char* xs = zs + S::ZBYTES;
   char* ps = xs;
+  f32x4* dtab = (f32x4*)(xs + (S::XBYTES > S::PBYTES ? S::XBYTES : S::PBYTES));
 
   // Whether M goes on to a state in memory, where fp32 is asked for, or only
   // into outputs of the tensors' type.
@@ -385,7 +406,21 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     }
   }
 
-  const float cs = w.cx * w.cz;
+  if (OUT && wave == 0) {
+    // Per lane: the decays of its four scores in a diagonal block, in the block
+    // below it, and those of X^T M for its token of each block.
+    f32x4 d0, d1, dx = {};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int d = lr - 4 * lq - r;
+      d0[r] = d >= 0 ? w.cx * w.cz * exp2_hw(l2 * (float)d) : 0.0f;
+      d1[r] = w.cx * w.cz * exp2_hw(l2 * (float)(16 + d));
+      if (r < NB) dx[r] = w.cx * exp2_hw(l2 * (float)(16 * r + lr + a));
+    }
+    dtab[lane] = d0;
+    dtab[kWave + lane] = d1;
+    dtab[2 * kWave + lane] = dx;
+  }
   Factor lam{power(log_decay, h, C), 0.0f};
 
   Tile<YD, C, ES, S::YU> tx, ty;
@@ -419,17 +454,17 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     }
 
     // Scores of tokens j = 4 lq + 0..3 of a block for token i = lr of the block
-    // `far` tokens on.  Where j > i the score is selected away, never multiplied
+    // `apart` blocks on.  Where j > i the score is selected away, never multiplied
     // by 0.
-    auto decayed = [&](f32x4& d, int far) {
+    auto decayed = [&](f32x4& d, int apart) {
+      const f32x4 dec = dtab[(apart > 0 ? kWave : 0) + (fresh & (kWave - 1))];
+      const float far = exp2_hw(l2 * (float)(16 * (apart > 1 ? apart - 1 : 0)));
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int dist = far + lr - 4 * lq - r;
-        const float v = d[r] * (cs * exp2_hw(l2 * (float)dist));
-        d[r] = dist >= 0 ? v : 0.0f;
+        const float v = d[r] * (dec[r] * far);
+        d[r] = apart > 0 || lr >= 4 * lq + r ? v : 0.0f;
       }
     };
-    auto out_decay = [&](int tb) { return w.cx * exp2_hw(l2 * (float)(16 * tb + lr + a)); };
     if constexpr (BF16) {
       const uint16_t* xl = (const uint16_t*)xs;
       const uint16_t* yl = (const uint16_t*)ys;
@@ -452,7 +487,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           for (int kk = 0; kk < NY / 2; ++kk)
             d = mfma_bf16(row_frag(yl, YS, 16 * sb + lr, kk), row_frag(xl, YS, 16 * tb + lr, kk),
                           d);
-          decayed(d, 16 * (tb - sb));
+          decayed(d, tb - sb);
           split4(d, hi, lo);
         };
         score(wave, sh[0], sl[0]);
@@ -480,7 +515,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
-          const float ex = out_decay(tb);
+          const float ex = dtab[2 * kWave + (fresh & (kWave - 1))][tb];
 #pragma unroll
           for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex;
         }
@@ -606,7 +641,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
 #pragma unroll
             for (int r = 0; r < 4; ++r) d = mfma_f32(yf[r], xf[r], d);
           }
-          decayed(d, 16 * (tb - sb));
+          decayed(d, tb - sb);
         }
         // (2) X^T M
 #pragma unroll
@@ -623,7 +658,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
-          const float ex = out_decay(tb);
+          const float ex = dtab[2 * kWave + (fresh & (kWave - 1))][tb];
 #pragma unroll
           for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex;
         }
