@@ -11,10 +11,10 @@
 // nothing is kept from the forward call.
 //
 // MI355X design.  Each call reads its inputs once and writes its outputs
-// once: HBM-bound.  A team of TS lanes owns a segment: NV vectors of VE
-// elements per lane stay in registers between the sums and the outputs
-// (VE = 8, 16-byte loads, where the segment length is a multiple of 8; single
-// elements otherwise, whose rows are not 16-byte aligned).  The sums of a team
+// once: HBM-bound.  A team of TS lanes owns a segment: NV vectors of eight
+// elements per lane stay in registers between the sums and the outputs (where the
+// segment length is no multiple of 8 the vectors start at any element, and the
+// last one overlaps the one before).  The sums of a team
 // within a wave are lane exchanges; teams of four waves meet once in LDS.
 // Teams are tied to a group of channels and walk the rows with the stride of
 // the grid, so weights are loaded once per team, and the gradients of weights
@@ -30,27 +30,38 @@ namespace ssd {
 namespace {
 
 constexpr int kNormThreads = 256;
+constexpr int kVec = 8;                // elements of a lane's vector
 // Workgroups of a launch: four per CU (measured against two and eight).
 constexpr int kNormBlocks = 1024;
 
-// VE elements at element offset `i`, as floats, and back (rounded once).
-template <bool BF16, int VE>
-__device__ __forceinline__ void load_n(const void* p, int64_t i, float* v) {
-  if constexpr (VE == 1) {
-    if constexpr (BF16)
-      v[0] = __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
-    else
-      v[0] = ((const float*)p)[i];
+// The eight elements at element offset `i`, as floats, and back (rounded once).
+// RAGGED: the segment length is no multiple of 8, so a vector may start at any
+// element, and a segment may have fewer than eight (zeros stand for the rest).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+template <bool BF16, bool RAGGED>
+__device__ __forceinline__ void load_n(const void* p, int64_t i, int left, float* v) {
+  if (RAGGED && left < kVec) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      v[e] = 0.0f;
+      if (e < left)
+        v[e] = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i + e] << 16)
+                    : ((const float*)p)[i + e];
+    }
   } else if constexpr (BF16) {
-    const u32x4 u = *(const u32x4*)((const uint16_t*)p + i);
+    const uint16_t* q = (const uint16_t*)p + i;
+    const u32x4 u = RAGGED ? (u32x4) * (const u32x4_any*)q : *(const u32x4*)q;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[2 * k] = bf16_lo(u[k]);
       v[2 * k + 1] = bf16_hi(u[k]);
     }
   } else {
-    const f32x4 a = *(const f32x4*)((const float*)p + i);
-    const f32x4 b = *(const f32x4*)((const float*)p + i + 4);
+    const float* q = (const float*)p + i;
+    const f32x4 a = RAGGED ? (f32x4) * (const f32x4_any*)q : *(const f32x4*)q;
+    const f32x4 b = RAGGED ? (f32x4) * (const f32x4_any*)(q + 4) : *(const f32x4*)(q + 4);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[k] = a[k];
@@ -58,19 +69,36 @@ __device__ __forceinline__ void load_n(const void* p, int64_t i, float* v) {
     }
   }
 }
-template <bool BF16, int VE>
-__device__ __forceinline__ void store_n(void* p, int64_t i, const float* v) {
-  if constexpr (VE == 1) {
-    if constexpr (BF16)
-      ((uint16_t*)p)[i] = (uint16_t)(pack_bf16(v[0], 0.0f) & 0xFFFFu);
-    else
-      ((float*)p)[i] = v[0];
+template <bool BF16, bool RAGGED>
+__device__ __forceinline__ void store_n(void* p, int64_t i, int left, const float* v) {
+  if (RAGGED && left < kVec) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      if (e < left) {
+        if constexpr (BF16)
+          ((uint16_t*)p)[i + e] = (uint16_t)(pack_bf16(v[e], 0.0f) & 0xFFFFu);
+        else
+          ((float*)p)[i + e] = v[e];
+      }
+    }
   } else if constexpr (BF16) {
-    *(u32x4*)((uint16_t*)p + i) = (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                          pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    const u32x4 u = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                     pack_bf16(v[6], v[7])};
+    uint16_t* q = (uint16_t*)p + i;
+    if constexpr (RAGGED)
+      *(u32x4_any*)q = u;
+    else
+      *(u32x4*)q = u;
   } else {
-    *(f32x4*)((float*)p + i) = (f32x4){v[0], v[1], v[2], v[3]};
-    *(f32x4*)((float*)p + i + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+    const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    float* q = (float*)p + i;
+    if constexpr (RAGGED) {
+      *(f32x4_any*)q = a;
+      *(f32x4_any*)(q + 4) = b;
+    } else {
+      *(f32x4*)q = a;
+      *(f32x4*)(q + 4) = b;
+    }
   }
 }
 
@@ -126,22 +154,40 @@ struct Team {
   }
 };
 
-template <int NV, int VE, int TS>
+// A lane's vector of a segment of n elements.  In a RAGGED segment the last vector
+// ends with the segment and shares its first `skip` elements with the one before:
+// both lanes form and store the same values there, and only one adds them to the
+// segment's sums.  (A segment of less than eight elements is one short vector.)
+template <bool RAGGED>
+struct Span {
+  int c, skip;
+  bool on;
+  __device__ __forceinline__ Span(int vec, int n) : c(vec * kVec), skip(0), on(vec * kVec < n) {
+    if (RAGGED && n >= kVec && c + kVec > n) {
+      skip = c - (n - kVec);
+      c = n - kVec;
+    }
+  }
+  __device__ __forceinline__ bool counts(int e) const { return !RAGGED || e >= skip; }
+};
+
+template <int NV, bool RAGGED, int TS>
 __device__ __forceinline__ void load_weights(const float* p, const NormGrid& g, const Team<TS>& t,
                                              bool shared, float other, float* w) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (t.lane + TS * j) * VE;
+    const Span<RAGGED> sp(t.lane + TS * j, g.n);
+    const int c = sp.c;
 #pragma unroll
-    for (int e = 0; e < VE; ++e) w[j * VE + e] = other;
-    if (p != nullptr && t.on && c < g.n)
-      load_n<false, VE>(p, (shared ? 0 : (int64_t)t.group * g.n) + c, w + j * VE);
+    for (int e = 0; e < kVec; ++e) w[j * kVec + e] = other;
+    if (p != nullptr && t.on && sp.on)
+      load_n<false, RAGGED>(p, (shared ? 0 : (int64_t)t.group * g.n) + c, g.n - c, w + j * kVec);
   }
 }
 
 // One row of partial sums of this workgroup: over its teams of one group, or
 // of every group where the weights are shared.
-template <int TS, int NV, int VE>
+template <int TS, int NV, bool RAGGED>
 __device__ __forceinline__ void store_partial(const float* acc, float* part, const NormGrid& g,
                                               const Team<TS>& t, float* buf) {
   constexpr int kTeams = Team<TS>::kTeams;
@@ -153,103 +199,109 @@ __device__ __forceinline__ void store_partial(const float* acc, float* part, con
                         : part + (int64_t)blockIdx.x * g.dim + (int64_t)t.group * g.n;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    float v[VE];
+    float v[kVec];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) v[e] = acc[j * VE + e];
+    for (int e = 0; e < kVec; ++e) v[e] = acc[j * kVec + e];
     if constexpr (kTeams > 1) {
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < VE; ++e) buf[e * kNormThreads + threadIdx.x] = v[e];
+      for (int e = 0; e < kVec; ++e) buf[e * kNormThreads + threadIdx.x] = v[e];
       __syncthreads();
       if (writes) {
         for (int k = 1; k < span; ++k) {
 #pragma unroll
-          for (int e = 0; e < VE; ++e) v[e] += buf[e * kNormThreads + threadIdx.x + k * step * TS];
+          for (int e = 0; e < kVec; ++e) v[e] += buf[e * kNormThreads + threadIdx.x + k * step * TS];
         }
       }
     }
-    const int c = (t.lane + TS * j) * VE;
-    if (writes && c < g.n) store_n<false, VE>(row, c, v);
+    const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+    if (writes && sp.on) store_n<false, RAGGED>(row, c, g.n - c, v);
   }
 }
 
 // ---------------------------------------------------------------- add norm
-template <int TS, int NV, int VE, bool XB, bool RB>
+template <int TS, int NV, bool RAGGED, bool XB, bool RB>
 __global__ __launch_bounds__(kNormThreads) void add_norm_fwd_kernel(
     const void* x, const void* res, const float* __restrict__ scale,
     const float* __restrict__ weight, void* y, void* res_out, NormGrid g) {
   __shared__ float red[2][4][2];
   int turn = 0;
   Team<TS> t(g);
-  float w[NV * VE], s[NV * VE];
-  load_weights<NV, VE, TS>(weight, g, t, false, 1.0f, w);
-  load_weights<NV, VE, TS>(scale, g, t, false, 1.0f, s);
+  float w[NV * kVec], s[NV * kVec];
+  load_weights<NV, RAGGED, TS>(weight, g, t, false, 1.0f, w);
+  load_weights<NV, RAGGED, TS>(scale, g, t, false, 1.0f, s);
   for (int64_t row = t.row; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim;
-    float h[NV * VE], sum[1] = {0.0f};
+    float h[NV * kVec], sum[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      float xv[VE] = {}, rv[VE] = {};
-      if (c < g.n) {
-        load_n<XB, VE>(x, base + c, xv);
-        if (res) load_n<RB, VE>(res, base + c, rv);
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      float xv[kVec] = {}, rv[kVec] = {};
+      if (sp.on) {
+        load_n<XB, RAGGED>(x, base + c, g.n - c, xv);
+        if (res) load_n<RB, RAGGED>(res, base + c, g.n - c, rv);
       }
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        h[j * VE + e] = __builtin_fmaf(s[j * VE + e], xv[e], rv[e]);
-        sum[0] = __builtin_fmaf(h[j * VE + e], h[j * VE + e], sum[0]);
+      for (int e = 0; e < kVec; ++e) {
+        h[j * kVec + e] = __builtin_fmaf(s[j * kVec + e], xv[e], rv[e]);
+        if (sp.counts(e)) sum[0] = __builtin_fmaf(h[j * kVec + e], h[j * kVec + e], sum[0]);
       }
     }
     team_sum<TS, 1>(sum, red, turn);
     const float r = rsqrtf(__builtin_fmaf(sum[0], g.inv_n, g.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      if (c < g.n) {
-        float v[VE];
-        if (res_out) store_n<RB, VE>(res_out, base + c, h + j * VE);
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      if (sp.on) {
+        float v[kVec];
+        if (res_out) store_n<RB, RAGGED>(res_out, base + c, g.n - c, h + j * kVec);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[e] = h[j * VE + e] * r * w[j * VE + e];
-        store_n<XB, VE>(y, base + c, v);
+        for (int e = 0; e < kVec; ++e) v[e] = h[j * kVec + e] * r * w[j * kVec + e];
+        store_n<XB, RAGGED>(y, base + c, g.n - c, v);
       }
     }
   }
 }
 
-template <int TS, int NV, int VE, bool XB, bool RB>
+template <int TS, int NV, bool RAGGED, bool XB, bool RB>
 __global__ __launch_bounds__(kNormThreads) void add_norm_bwd_kernel(
     const void* x, const void* res, const float* __restrict__ scale,
     const float* __restrict__ weight, const void* dy, const void* dres_out, void* dx, void* dres,
     float* __restrict__ dscale, float* __restrict__ dweight, NormGrid g) {
   __shared__ float red[2][4][2];
-  __shared__ float buf[Team<TS>::kTeams > 1 ? VE * kNormThreads : 1];
+  __shared__ float buf[Team<TS>::kTeams > 1 ? kVec * kNormThreads : 1];
   int turn = 0;
   Team<TS> t(g);
-  float w[NV * VE], s[NV * VE], dw[NV * VE] = {}, ds[NV * VE] = {};
-  load_weights<NV, VE, TS>(weight, g, t, false, 1.0f, w);
-  load_weights<NV, VE, TS>(scale, g, t, false, 1.0f, s);
+  float w[NV * kVec], s[NV * kVec], dw[NV * kVec] = {}, ds[NV * kVec] = {};
+  load_weights<NV, RAGGED, TS>(weight, g, t, false, 1.0f, w);
+  load_weights<NV, RAGGED, TS>(scale, g, t, false, 1.0f, s);
   for (int64_t row = t.row; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim;
-    float h[NV * VE], xs[NV * VE], dv[NV * VE], gv[NV * VE], sum[2] = {0.0f, 0.0f};
+    float h[NV * kVec], xs[NV * kVec], dv[NV * kVec], gv[NV * kVec], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      float rv[VE] = {};
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      float rv[kVec] = {};
 #pragma unroll
-      for (int e = 0; e < VE; ++e) xs[j * VE + e] = dv[j * VE + e] = gv[j * VE + e] = 0.0f;
-      if (c < g.n) {
-        load_n<XB, VE>(x, base + c, xs + j * VE);
-        load_n<XB, VE>(dy, base + c, dv + j * VE);
-        if (res) load_n<RB, VE>(res, base + c, rv);
-        if (dres_out) load_n<RB, VE>(dres_out, base + c, gv + j * VE);
+      for (int e = 0; e < kVec; ++e) xs[j * kVec + e] = dv[j * kVec + e] = gv[j * kVec + e] = 0.0f;
+      if (sp.on) {
+        load_n<XB, RAGGED>(x, base + c, g.n - c, xs + j * kVec);
+        load_n<XB, RAGGED>(dy, base + c, g.n - c, dv + j * kVec);
+        if (res) load_n<RB, RAGGED>(res, base + c, g.n - c, rv);
+        if (dres_out) load_n<RB, RAGGED>(dres_out, base + c, g.n - c, gv + j * kVec);
       }
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int i = j * VE + e;
+      for (int e = 0; e < kVec; ++e) {
+        const int i = j * kVec + e;
         h[i] = __builtin_fmaf(s[i], xs[i], rv[e]);
-        sum[0] = __builtin_fmaf(h[i], h[i], sum[0]);
-        sum[1] = __builtin_fmaf(w[i] * dv[i], h[i], sum[1]);
+        if (sp.counts(e)) {
+          sum[0] = __builtin_fmaf(h[i], h[i], sum[0]);
+          sum[1] = __builtin_fmaf(w[i] * dv[i], h[i], sum[1]);
+        }
       }
     }
     team_sum<TS, 2>(sum, red, turn);
@@ -257,25 +309,26 @@ __global__ __launch_bounds__(kNormThreads) void add_norm_bwd_kernel(
     const float m = sum[1] * g.inv_n * r;              // mean(w dy n)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      float dxv[VE];
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      float dxv[kVec];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int i = j * VE + e;
+      for (int e = 0; e < kVec; ++e) {
+        const int i = j * kVec + e;
         const float n = h[i] * r;
         gv[i] = __builtin_fmaf(r, __builtin_fmaf(-n, m, w[i] * dv[i]), gv[i]);
         dxv[e] = s[i] * gv[i];
         dw[i] = __builtin_fmaf(dv[i], n, dw[i]);
         ds[i] = __builtin_fmaf(gv[i], xs[i], ds[i]);
       }
-      if (c < g.n) {
-        if (dres) store_n<RB, VE>(dres, base + c, gv + j * VE);
-        store_n<XB, VE>(dx, base + c, dxv);
+      if (sp.on) {
+        if (dres) store_n<RB, RAGGED>(dres, base + c, g.n - c, gv + j * kVec);
+        store_n<XB, RAGGED>(dx, base + c, g.n - c, dxv);
       }
     }
   }
-  if (dweight) store_partial<TS, NV, VE>(dw, dweight, g, t, buf);
-  if (dscale) store_partial<TS, NV, VE>(ds, dscale, g, t, buf);
+  if (dweight) store_partial<TS, NV, RAGGED>(dw, dweight, g, t, buf);
+  if (dscale) store_partial<TS, NV, RAGGED>(ds, dscale, g, t, buf);
 }
 
 // -------------------------------------------------------------- gated norm
@@ -290,84 +343,89 @@ __device__ __forceinline__ float gate_act(float z, bool silu, float& d) {
   return silu ? z * sig : sig;
 }
 
-template <int TS, int NV, int VE, bool XB, bool ZB>
+template <int TS, int NV, bool RAGGED, bool XB, bool ZB>
 __global__ __launch_bounds__(kNormThreads) void gated_norm_fwd_kernel(
     const void* x, const void* z, const float* __restrict__ weight, void* y, bool silu,
     bool first, NormGrid g) {
   __shared__ float red[2][4][2];
   int turn = 0;
   Team<TS> t(g);
-  float w[NV * VE];
-  load_weights<NV, VE, TS>(weight, g, t, g.shared, 1.0f, w);
+  float w[NV * kVec];
+  load_weights<NV, RAGGED, TS>(weight, g, t, g.shared, 1.0f, w);
   if (!t.on) return;            // whole teams; a team of four waves is always on
   for (int64_t row = t.row; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim + (int64_t)t.group * g.n;
-    float u[NV * VE], a[NV * VE], sum[1] = {0.0f};
+    float u[NV * kVec], a[NV * kVec], sum[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      float xv[VE] = {}, zv[VE] = {}, d;
-      if (c < g.n) {
-        load_n<XB, VE>(x, base + c, xv);
-        if (z) load_n<ZB, VE>(z, base + c, zv);
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      float xv[kVec] = {}, zv[kVec] = {}, d;
+      if (sp.on) {
+        load_n<XB, RAGGED>(x, base + c, g.n - c, xv);
+        if (z) load_n<ZB, RAGGED>(z, base + c, g.n - c, zv);
       }
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int i = j * VE + e;
+      for (int e = 0; e < kVec; ++e) {
+        const int i = j * kVec + e;
         const float act = z ? gate_act(zv[e], silu, d) : 1.0f;
         u[i] = first ? xv[e] * act : xv[e];
         a[i] = first ? 1.0f : act;
-        sum[0] = __builtin_fmaf(u[i], u[i], sum[0]);
+        if (sp.counts(e)) sum[0] = __builtin_fmaf(u[i], u[i], sum[0]);
       }
     }
     team_sum<TS, 1>(sum, red, turn);
     const float r = rsqrtf(__builtin_fmaf(sum[0], g.inv_n, g.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      if (c < g.n) {
-        float v[VE];
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      if (sp.on) {
+        float v[kVec];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[e] = u[j * VE + e] * r * w[j * VE + e] * a[j * VE + e];
-        store_n<ZB, VE>(y, base + c, v);
+        for (int e = 0; e < kVec; ++e) v[e] = u[j * kVec + e] * r * w[j * kVec + e] * a[j * kVec + e];
+        store_n<ZB, RAGGED>(y, base + c, g.n - c, v);
       }
     }
   }
 }
 
-template <int TS, int NV, int VE, bool XB, bool ZB>
+template <int TS, int NV, bool RAGGED, bool XB, bool ZB>
 __global__ __launch_bounds__(kNormThreads) void gated_norm_bwd_kernel(
     const void* x, const void* z, const float* __restrict__ weight, const void* dy, void* dx,
     void* dz, float* __restrict__ dweight, bool silu, bool first, NormGrid g) {
   __shared__ float red[2][4][2];
-  __shared__ float buf[Team<TS>::kTeams > 1 ? VE * kNormThreads : 1];
+  __shared__ float buf[Team<TS>::kTeams > 1 ? kVec * kNormThreads : 1];
   int turn = 0;
   Team<TS> t(g);
-  float w[NV * VE], dw[NV * VE] = {};
-  load_weights<NV, VE, TS>(weight, g, t, g.shared, 1.0f, w);
+  float w[NV * kVec], dw[NV * kVec] = {};
+  load_weights<NV, RAGGED, TS>(weight, g, t, g.shared, 1.0f, w);
   for (int64_t row = t.on ? t.row : g.rows; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim + (int64_t)t.group * g.n;
-    float xs[NV * VE], act[NV * VE], der[NV * VE], dv[NV * VE], sum[2] = {0.0f, 0.0f};
+    float xs[NV * kVec], act[NV * kVec], der[NV * kVec], dv[NV * kVec], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      float zv[VE] = {};
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      float zv[kVec] = {};
 #pragma unroll
-      for (int e = 0; e < VE; ++e) xs[j * VE + e] = dv[j * VE + e] = 0.0f;
-      if (c < g.n) {
-        load_n<XB, VE>(x, base + c, xs + j * VE);
-        load_n<ZB, VE>(dy, base + c, dv + j * VE);
-        if (z) load_n<ZB, VE>(z, base + c, zv);
+      for (int e = 0; e < kVec; ++e) xs[j * kVec + e] = dv[j * kVec + e] = 0.0f;
+      if (sp.on) {
+        load_n<XB, RAGGED>(x, base + c, g.n - c, xs + j * kVec);
+        load_n<ZB, RAGGED>(dy, base + c, g.n - c, dv + j * kVec);
+        if (z) load_n<ZB, RAGGED>(z, base + c, g.n - c, zv);
       }
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int i = j * VE + e;
+      for (int e = 0; e < kVec; ++e) {
+        const int i = j * kVec + e;
         der[i] = 0.0f;
         act[i] = z ? gate_act(zv[e], silu, der[i]) : 1.0f;
         const float u = first ? xs[i] * act[i] : xs[i];
         const float en = dv[i] * w[i] * (first ? 1.0f : act[i]);
-        sum[0] = __builtin_fmaf(u, u, sum[0]);
-        sum[1] = __builtin_fmaf(en, u, sum[1]);
+        if (sp.counts(e)) {
+          sum[0] = __builtin_fmaf(u, u, sum[0]);
+          sum[1] = __builtin_fmaf(en, u, sum[1]);
+        }
       }
     }
     team_sum<TS, 2>(sum, red, turn);
@@ -375,11 +433,12 @@ __global__ __launch_bounds__(kNormThreads) void gated_norm_bwd_kernel(
     const float m = sum[1] * g.inv_n * r;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t.lane + TS * j) * VE;
-      float dxv[VE], dzv[VE];
+      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const int c = sp.c;
+      float dxv[kVec], dzv[kVec];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int i = j * VE + e;
+      for (int e = 0; e < kVec; ++e) {
+        const int i = j * kVec + e;
         const float n = (first ? xs[i] * act[i] : xs[i]) * r;
         const float dn = first ? dv[i] : dv[i] * act[i];
         const float du = r * __builtin_fmaf(-n, m, dn * w[i]);
@@ -387,20 +446,25 @@ __global__ __launch_bounds__(kNormThreads) void gated_norm_bwd_kernel(
         dzv[e] = (first ? du * xs[i] : dv[i] * n * w[i]) * der[i];
         dw[i] = __builtin_fmaf(dn, n, dw[i]);
       }
-      if (c < g.n) {
-        store_n<XB, VE>(dx, base + c, dxv);
-        if (z) store_n<ZB, VE>(dz, base + c, dzv);
+      if (sp.on) {
+        store_n<XB, RAGGED>(dx, base + c, g.n - c, dxv);
+        if (z) store_n<ZB, RAGGED>(dz, base + c, g.n - c, dzv);
       }
     }
   }
-  if (dweight) store_partial<TS, NV, VE>(dw, dweight, g, t, buf);
+  if (dweight) store_partial<TS, NV, RAGGED>(dw, dweight, g, t, buf);
 }
 
 // Adds `parts` rows of `cols` partial sums in a fixed order: 16 slices of the
-// rows, each added in turn, then the slices in order.
-__global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict__ part,
-                                                        float* __restrict__ out, int parts,
+// rows, each added in turn, then the slices in order.  blockIdx.y: which of two
+// sums.
+__global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict__ part0,
+                                                        float* __restrict__ out0,
+                                                        const float* __restrict__ part1,
+                                                        float* __restrict__ out1, int parts,
                                                         int cols) {
+  const float* part = blockIdx.y ? part1 : part0;
+  float* out = blockIdx.y ? out1 : out0;
   __shared__ float buf[16][kWave];
   const int lane = threadIdx.x % kWave, slice = threadIdx.x / kWave;
   const int c = blockIdx.x * kWave + lane;
@@ -425,29 +489,22 @@ struct NormLaunch {
   int cols;
 };
 
-// The lanes of a team: enough for one vector each up to a wave, then up to
-// four vectors per lane of a wave, then a workgroup.
+// The lanes of a team: enough for one vector each up to a wave, then up to two
+// vectors per lane of a wave, then a workgroup.
 struct TeamPlan {
-  int ts, nv, ve;
+  int ts, nv;
 };
 TeamPlan team_plan(int64_t n) {
-  if (n % 8 == 0) {
-    const int64_t u = n / 8;
-    if (u <= 8) return {8, 1, 8};
-    if (u <= 16) return {16, 1, 8};
-    if (u <= 32) return {32, 1, 8};
-    if (u <= 64) return {64, 1, 8};
-    if (u <= 128) return {64, 2, 8};
-    if (u <= 256) return {256, 1, 8};
-    if (u <= 512) return {256, 2, 8};
-    if (u <= 1024) return {256, 4, 8};
-    return {256, 8, 8};
-  }
-  if (n <= 64) return {64, 1, 1};
-  if (n <= 256) return {64, 4, 1};
-  if (n <= 1024) return {256, 4, 1};
-  if (n <= 4096) return {256, 16, 1};
-  return {256, 64, 1};
+  const int64_t u = (n + kVec - 1) / kVec;
+  if (u <= 8) return {8, 1};
+  if (u <= 16) return {16, 1};
+  if (u <= 32) return {32, 1};
+  if (u <= 64) return {64, 1};
+  if (u <= 128) return {64, 2};
+  if (u <= 256) return {256, 1};
+  if (u <= 512) return {256, 2};
+  if (u <= 1024) return {256, 4};
+  return {256, 8};
 }
 
 NormLaunch norm_launch(const NormShape& s, float eps) {
@@ -469,30 +526,27 @@ NormLaunch norm_launch(const NormShape& s, float eps) {
   return l;
 }
 
-// f(TeamPlan constants) for the plan of a segment of n channels.
+// f(TeamPlan constants, ragged) for the plan of a segment of n channels.
 template <class F>
 void with_plan(int64_t n, F f) {
   const TeamPlan p = team_plan(n);
-  auto is = [&](int ts, int nv, int ve) { return p.ts == ts && p.nv == nv && p.ve == ve; };
-#define SSD_NORM_PLAN(TS, NV, VE)                                       \
-  if (is(TS, NV, VE)) {                                                 \
-    return f(std::integral_constant<int, TS>{}, std::integral_constant<int, NV>{}, \
-             std::integral_constant<int, VE>{});                        \
+#define SSD_NORM_PLAN(TS, NV)                                                          \
+  if (p.ts == TS && p.nv == NV) {                                                      \
+    if (n % kVec)                                                                      \
+      return f(std::integral_constant<int, TS>{}, std::integral_constant<int, NV>{},   \
+               std::true_type{});                                                      \
+    return f(std::integral_constant<int, TS>{}, std::integral_constant<int, NV>{},     \
+             std::false_type{});                                                       \
   }
-  SSD_NORM_PLAN(8, 1, 8)
-  SSD_NORM_PLAN(16, 1, 8)
-  SSD_NORM_PLAN(32, 1, 8)
-  SSD_NORM_PLAN(64, 1, 8)
-  SSD_NORM_PLAN(64, 2, 8)
-  SSD_NORM_PLAN(256, 1, 8)
-  SSD_NORM_PLAN(256, 2, 8)
-  SSD_NORM_PLAN(256, 4, 8)
-  SSD_NORM_PLAN(256, 8, 8)
-  SSD_NORM_PLAN(64, 1, 1)
-  SSD_NORM_PLAN(64, 4, 1)
-  SSD_NORM_PLAN(256, 4, 1)
-  SSD_NORM_PLAN(256, 16, 1)
-  SSD_NORM_PLAN(256, 64, 1)
+  SSD_NORM_PLAN(8, 1)
+  SSD_NORM_PLAN(16, 1)
+  SSD_NORM_PLAN(32, 1)
+  SSD_NORM_PLAN(64, 1)
+  SSD_NORM_PLAN(64, 2)
+  SSD_NORM_PLAN(256, 1)
+  SSD_NORM_PLAN(256, 2)
+  SSD_NORM_PLAN(256, 4)
+  SSD_NORM_PLAN(256, 8)
 #undef SSD_NORM_PLAN
 }
 template <class F>
@@ -501,10 +555,17 @@ void with_bool(bool b, F f) {
   f(std::false_type{});
 }
 
-int add_rows(const float* part, float* out, const NormLaunch& l, hipStream_t st) {
-  const unsigned blocks = (unsigned)((l.cols + kWave - 1) / kWave);
-  hipLaunchKernelGGL(sum_rows_kernel, dim3(blocks), dim3(1024), 0, st, part, out, l.parts,
-                     l.cols);
+// The sums whose outputs are asked for, in one launch.
+int add_rows(const float* p0, float* o0, const float* p1, float* o1, const NormLaunch& l,
+             hipStream_t st) {
+  if (o0 == nullptr) {
+    p0 = p1;
+    o0 = o1;
+    o1 = nullptr;
+  }
+  if (o0 == nullptr) return 0;
+  const dim3 grid((unsigned)((l.cols + kWave - 1) / kWave), o1 != nullptr ? 2u : 1u);
+  hipLaunchKernelGGL(sum_rows_kernel, grid, dim3(1024), 0, st, p0, o0, p1, o1, l.parts, l.cols);
   return (int)hipGetLastError();
 }
 
@@ -521,10 +582,10 @@ int launch_add_norm_fwd(const void* x, const void* res, const float* scale, cons
                         const NormShape& s, void* stream) {
   clear_launch_error();
   const NormLaunch l = norm_launch(s, eps);
-  with_plan(s.group, [&](auto ts, auto nv, auto ve) {
+  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
-        hipLaunchKernelGGL((add_norm_fwd_kernel<ts(), nv(), ve(), xb(), rb()>), l.grid,
+        hipLaunchKernelGGL((add_norm_fwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
                            dim3(kNormThreads), 0, (hipStream_t)stream, x, res, scale, weight, y,
                            res_out, l.g);
       });
@@ -541,19 +602,17 @@ int launch_add_norm_bwd(const void* x, const void* res, const float* scale, cons
   const NormLaunch l = norm_launch(s, eps);
   float* pw = dweight ? (float*)ws : nullptr;
   float* ps = dscale ? (float*)((char*)ws + norm_bwd_workspace(s, 1)) : nullptr;
-  with_plan(s.group, [&](auto ts, auto nv, auto ve) {
+  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
-        hipLaunchKernelGGL((add_norm_bwd_kernel<ts(), nv(), ve(), xb(), rb()>), l.grid,
+        hipLaunchKernelGGL((add_norm_bwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
                            dim3(kNormThreads), 0, (hipStream_t)stream, x, res, scale, weight, dy,
                            dres_out, dx, dres, ps, pw, l.g);
       });
     });
   });
-  int err = (int)hipGetLastError();
-  if (err == 0 && dweight) err = add_rows(pw, dweight, l, (hipStream_t)stream);
-  if (err == 0 && dscale) err = add_rows(ps, dscale, l, (hipStream_t)stream);
-  return err;
+  const int err = (int)hipGetLastError();
+  return err ? err : add_rows(pw, dweight, ps, dscale, l, (hipStream_t)stream);
 }
 
 int launch_gated_norm_fwd(const void* x, const void* z, const float* weight, void* y, float eps,
@@ -561,10 +620,10 @@ int launch_gated_norm_fwd(const void* x, const void* z, const float* weight, voi
                           void* stream) {
   clear_launch_error();
   const NormLaunch l = norm_launch(s, eps);
-  with_plan(s.group, [&](auto ts, auto nv, auto ve) {
+  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(zbf16, [&](auto zb) {
-        hipLaunchKernelGGL((gated_norm_fwd_kernel<ts(), nv(), ve(), xb(), zb()>), l.grid,
+        hipLaunchKernelGGL((gated_norm_fwd_kernel<ts(), nv(), rag(), xb(), zb()>), l.grid,
                            dim3(kNormThreads), 0, (hipStream_t)stream, x, z, weight, y, silu,
                            first, l.g);
       });
@@ -579,18 +638,17 @@ int launch_gated_norm_bwd(const void* x, const void* z, const float* weight, con
   clear_launch_error();
   const NormLaunch l = norm_launch(s, eps);
   float* pw = dweight ? (float*)ws : nullptr;
-  with_plan(s.group, [&](auto ts, auto nv, auto ve) {
+  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(zbf16, [&](auto zb) {
-        hipLaunchKernelGGL((gated_norm_bwd_kernel<ts(), nv(), ve(), xb(), zb()>), l.grid,
+        hipLaunchKernelGGL((gated_norm_bwd_kernel<ts(), nv(), rag(), xb(), zb()>), l.grid,
                            dim3(kNormThreads), 0, (hipStream_t)stream, x, z, weight, dy, dx, dz,
                            pw, silu, first, l.g);
       });
     });
   });
-  int err = (int)hipGetLastError();
-  if (err == 0 && dweight) err = add_rows(pw, dweight, l, (hipStream_t)stream);
-  return err;
+  const int err = (int)hipGetLastError();
+  return err ? err : add_rows(pw, dweight, nullptr, nullptr, l, (hipStream_t)stream);
 }
 
 }  // namespace ssd
