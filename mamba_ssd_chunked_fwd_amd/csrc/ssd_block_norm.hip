@@ -15,7 +15,7 @@
 // elements per lane stay in registers between the sums and the outputs (where the
 // segment length is no multiple of 8 the vectors start at any element, and the
 // last one overlaps the one before).  The sums of a team
-// within a wave are lane exchanges; teams of four waves meet once in LDS.
+// within a wave are lane exchanges; teams of several waves meet once in LDS.
 // Teams are tied to a group of channels and walk the rows with the stride of
 // the grid, so weights are loaded once per team, and the gradients of weights
 // and scales are summed in registers: each workgroup writes one row of
@@ -31,8 +31,9 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kVec = 8;                // elements of a lane's vector
-// Workgroups of a launch: four per CU (measured against two and eight).
-constexpr int kNormBlocks = 1024;
+// Waves of a launch: 16 per CU (measured against 8, 12 and 32: with 8 the forward
+// calls lose up to 40%, with 32 the gradients' calls 10%).
+constexpr int kNormWaves = 4096;
 
 // The eight elements at element offset `i`, as floats, and back (rounded once).
 // RAGGED: the segment length is no multiple of 8, so a vector may start at any
@@ -102,27 +103,38 @@ __device__ __forceinline__ void store_n(void* p, int64_t i, int left, const floa
   }
 }
 
-// Sums of K values over the TS lanes of a team.  Teams of one workgroup
-// (TS = 256) alternate between two LDS rows, so one barrier per call is
-// enough: a row is written again only after the next call's barrier.
+// The lanes of a team: TS of a wave, or (TS = kBlockTeam) the whole workgroup, of
+// as many waves as the launch gives it.
+constexpr int kBlockTeam = 0;
+constexpr int kMaxWaves = 16;
+template <int TS>
+constexpr int max_threads() { return TS == kBlockTeam ? kMaxWaves * kWave : kNormThreads; }
+template <int TS>
+__device__ __forceinline__ int team_lanes() { return TS == kBlockTeam ? (int)blockDim.x : TS; }
+
+// Sums of K values over the lanes of a team.  Teams of a workgroup alternate
+// between two LDS rows, so one barrier per call is enough: a row is written again
+// only after the next call's barrier.
 template <int TS, int K>
-__device__ __forceinline__ void team_sum(float (&v)[K], float (*red)[4][2], int& turn) {
-  constexpr int W = TS < kWave ? TS : kWave;
+__device__ __forceinline__ void team_sum(float (&v)[K], float (*red)[kMaxWaves][2], int& turn) {
+  constexpr int W = TS == kBlockTeam || TS > kWave ? kWave : TS;
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], off, kWave);
   }
-  if constexpr (TS > kWave) {
-    const int wave = threadIdx.x / kWave;
+  if constexpr (TS == kBlockTeam || TS > kWave) {
+    const int waves = team_lanes<TS>() / kWave;
     if (threadIdx.x % kWave == 0) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) red[turn][wave][k] = v[k];
+      for (int k = 0; k < K; ++k) red[turn][threadIdx.x / kWave][k] = v[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      v[k] = (red[turn][0][k] + red[turn][1][k]) + (red[turn][2][k] + red[turn][3][k]);
+    for (int k = 0; k < K; ++k) {
+      v[k] = red[turn][0][k];
+      for (int i = 1; i < waves; ++i) v[k] += red[turn][i][k];
+    }
     turn ^= 1;
   }
 }
@@ -139,13 +151,13 @@ struct NormGrid {
 
 template <int TS>
 struct Team {
-  static constexpr int kTeams = kNormThreads / TS;
+  static constexpr int kTeams = TS == kBlockTeam ? 1 : kNormThreads / (TS ? TS : 1);
   int lane, group, rows_per_block;
   int64_t row, step;
   bool on;
   __device__ __forceinline__ explicit Team(const NormGrid& g) {
-    const int team = threadIdx.x / TS;
-    lane = threadIdx.x % TS;
+    const int team = threadIdx.x / team_lanes<TS>();
+    lane = threadIdx.x % team_lanes<TS>();
     group = blockIdx.y * g.per_block + team % g.per_block;
     rows_per_block = kTeams / g.per_block;
     row = (int64_t)blockIdx.x * rows_per_block + team / g.per_block;
@@ -176,7 +188,7 @@ __device__ __forceinline__ void load_weights(const float* p, const NormGrid& g, 
                                              bool shared, float other, float* w) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const Span<RAGGED> sp(t.lane + TS * j, g.n);
+    const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
     const int c = sp.c;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) w[j * kVec + e] = other;
@@ -191,7 +203,7 @@ template <int TS, int NV, bool RAGGED>
 __device__ __forceinline__ void store_partial(const float* acc, float* part, const NormGrid& g,
                                               const Team<TS>& t, float* buf) {
   constexpr int kTeams = Team<TS>::kTeams;
-  const int team = threadIdx.x / TS;
+  const int team = threadIdx.x / team_lanes<TS>();
   const int span = g.shared ? kTeams : t.rows_per_block;       // teams added up
   const int step = g.shared ? 1 : g.per_block;
   const bool writes = g.shared ? team == 0 : (team < g.per_block && t.on);
@@ -214,7 +226,7 @@ __device__ __forceinline__ void store_partial(const float* acc, float* part, con
         }
       }
     }
-    const Span<RAGGED> sp(t.lane + TS * j, g.n);
+    const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
     if (writes && sp.on) store_n<false, RAGGED>(row, c, g.n - c, v);
   }
@@ -222,10 +234,10 @@ __device__ __forceinline__ void store_partial(const float* acc, float* part, con
 
 // ---------------------------------------------------------------- add norm
 template <int TS, int NV, bool RAGGED, bool XB, bool RB>
-__global__ __launch_bounds__(kNormThreads) void add_norm_fwd_kernel(
+__global__ __launch_bounds__(max_threads<TS>()) void add_norm_fwd_kernel(
     const void* x, const void* res, const float* __restrict__ scale,
     const float* __restrict__ weight, void* y, void* res_out, NormGrid g) {
-  __shared__ float red[2][4][2];
+  __shared__ float red[2][kMaxWaves][2];
   int turn = 0;
   Team<TS> t(g);
   float w[NV * kVec], s[NV * kVec];
@@ -236,7 +248,7 @@ __global__ __launch_bounds__(kNormThreads) void add_norm_fwd_kernel(
     float h[NV * kVec], sum[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float xv[kVec] = {}, rv[kVec] = {};
       if (sp.on) {
@@ -253,7 +265,7 @@ __global__ __launch_bounds__(kNormThreads) void add_norm_fwd_kernel(
     const float r = rsqrtf(__builtin_fmaf(sum[0], g.inv_n, g.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       if (sp.on) {
         float v[kVec];
@@ -267,11 +279,11 @@ __global__ __launch_bounds__(kNormThreads) void add_norm_fwd_kernel(
 }
 
 template <int TS, int NV, bool RAGGED, bool XB, bool RB>
-__global__ __launch_bounds__(kNormThreads) void add_norm_bwd_kernel(
+__global__ __launch_bounds__(max_threads<TS>()) void add_norm_bwd_kernel(
     const void* x, const void* res, const float* __restrict__ scale,
     const float* __restrict__ weight, const void* dy, const void* dres_out, void* dx, void* dres,
     float* __restrict__ dscale, float* __restrict__ dweight, NormGrid g) {
-  __shared__ float red[2][4][2];
+  __shared__ float red[2][kMaxWaves][2];
   __shared__ float buf[Team<TS>::kTeams > 1 ? kVec * kNormThreads : 1];
   int turn = 0;
   Team<TS> t(g);
@@ -283,7 +295,7 @@ __global__ __launch_bounds__(kNormThreads) void add_norm_bwd_kernel(
     float h[NV * kVec], xs[NV * kVec], dv[NV * kVec], gv[NV * kVec], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float rv[kVec] = {};
 #pragma unroll
@@ -309,7 +321,7 @@ __global__ __launch_bounds__(kNormThreads) void add_norm_bwd_kernel(
     const float m = sum[1] * g.inv_n * r;              // mean(w dy n)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float dxv[kVec];
 #pragma unroll
@@ -344,21 +356,21 @@ __device__ __forceinline__ float gate_act(float z, bool silu, float& d) {
 }
 
 template <int TS, int NV, bool RAGGED, bool XB, bool ZB>
-__global__ __launch_bounds__(kNormThreads) void gated_norm_fwd_kernel(
+__global__ __launch_bounds__(max_threads<TS>()) void gated_norm_fwd_kernel(
     const void* x, const void* z, const float* __restrict__ weight, void* y, bool silu,
     bool first, NormGrid g) {
-  __shared__ float red[2][4][2];
+  __shared__ float red[2][kMaxWaves][2];
   int turn = 0;
   Team<TS> t(g);
   float w[NV * kVec];
   load_weights<NV, RAGGED, TS>(weight, g, t, g.shared, 1.0f, w);
-  if (!t.on) return;            // whole teams; a team of four waves is always on
+  if (!t.on) return;            // whole teams; one of a workgroup is always on
   for (int64_t row = t.row; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim + (int64_t)t.group * g.n;
     float u[NV * kVec], a[NV * kVec], sum[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float xv[kVec] = {}, zv[kVec] = {}, d;
       if (sp.on) {
@@ -378,7 +390,7 @@ __global__ __launch_bounds__(kNormThreads) void gated_norm_fwd_kernel(
     const float r = rsqrtf(__builtin_fmaf(sum[0], g.inv_n, g.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       if (sp.on) {
         float v[kVec];
@@ -391,10 +403,10 @@ __global__ __launch_bounds__(kNormThreads) void gated_norm_fwd_kernel(
 }
 
 template <int TS, int NV, bool RAGGED, bool XB, bool ZB>
-__global__ __launch_bounds__(kNormThreads) void gated_norm_bwd_kernel(
+__global__ __launch_bounds__(max_threads<TS>()) void gated_norm_bwd_kernel(
     const void* x, const void* z, const float* __restrict__ weight, const void* dy, void* dx,
     void* dz, float* __restrict__ dweight, bool silu, bool first, NormGrid g) {
-  __shared__ float red[2][4][2];
+  __shared__ float red[2][kMaxWaves][2];
   __shared__ float buf[Team<TS>::kTeams > 1 ? kVec * kNormThreads : 1];
   int turn = 0;
   Team<TS> t(g);
@@ -405,7 +417,7 @@ __global__ __launch_bounds__(kNormThreads) void gated_norm_bwd_kernel(
     float xs[NV * kVec], act[NV * kVec], der[NV * kVec], dv[NV * kVec], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float zv[kVec] = {};
 #pragma unroll
@@ -433,7 +445,7 @@ __global__ __launch_bounds__(kNormThreads) void gated_norm_bwd_kernel(
     const float m = sum[1] * g.inv_n * r;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + TS * j, g.n);
+      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float dxv[kVec], dzv[kVec];
 #pragma unroll
@@ -485,42 +497,50 @@ __global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict_
 struct NormLaunch {
   NormGrid g;
   dim3 grid;
+  int threads;
   int parts;      // rows of partial sums
   int cols;
 };
 
-// The lanes of a team: enough for one vector each up to a wave, then up to two
-// vectors per lane of a wave, then a workgroup.
+// The lanes of a team: enough for one vector each up to a wave, then two vectors
+// per lane of a wave, one or two per lane of four waves, and from there on as many
+// waves as the segment has vectors for one, then two, per lane.  (Measured for the
+// gradients' call: at 5000 channels ten waves of one vector take 50 us where four
+// of four took 76; at 2560 five waves of one take 55 us where four of two, of which
+// every third lane idles, take 49.)
 struct TeamPlan {
-  int ts, nv;
+  int ts, nv, threads;
 };
 TeamPlan team_plan(int64_t n) {
   const int64_t u = (n + kVec - 1) / kVec;
-  if (u <= 8) return {8, 1};
-  if (u <= 16) return {16, 1};
-  if (u <= 32) return {32, 1};
-  if (u <= 64) return {64, 1};
-  if (u <= 128) return {64, 2};
-  if (u <= 256) return {256, 1};
-  if (u <= 512) return {256, 2};
-  if (u <= 1024) return {256, 4};
-  return {256, 8};
+  if (u <= 8) return {8, 1, kNormThreads};
+  if (u <= 16) return {16, 1, kNormThreads};
+  if (u <= 32) return {32, 1, kNormThreads};
+  if (u <= 64) return {64, 1, kNormThreads};
+  if (u <= 128) return {64, 2, kNormThreads};
+  if (u <= 256) return {256, 1, 256};
+  if (u <= 512) return {256, 2, 256};
+  const int nv = u <= kMaxWaves * kWave ? 1 : 2;
+  return {kBlockTeam, nv, (int)((u + nv * kWave - 1) / (nv * kWave)) * kWave};
 }
 
 NormLaunch norm_launch(const NormShape& s, float eps) {
   NormLaunch l;
-  const int teams = kNormThreads / team_plan(s.group).ts;
+  const TeamPlan plan = team_plan(s.group);
+  const int teams = plan.ts == kBlockTeam ? 1 : kNormThreads / plan.ts;
   const int64_t groups = s.dim / s.group;
   int per = 1;
   while (per < teams && per < groups) per *= 2;
   const int64_t gy = (groups + per - 1) / per;
   const int64_t rows_per = teams / per;
   int64_t gx = (s.rows + rows_per - 1) / rows_per;
-  const int64_t want = (kNormBlocks + gy - 1) / gy;
+  const int64_t all = (int64_t)kNormWaves * kWave / plan.threads;
+  const int64_t want = (all + gy - 1) / gy;
   if (gx > want) gx = want;
   l.g = NormGrid{s.rows,     s.dim, (int)s.group, (int)groups, per, s.wdim != s.dim,
                  1.0f / (float)s.group, eps};
   l.grid = dim3((unsigned)gx, (unsigned)gy);
+  l.threads = plan.threads;
   l.parts = (int)(l.g.shared ? gx * gy : gx);
   l.cols = (int)s.wdim;
   return l;
@@ -545,8 +565,8 @@ void with_plan(int64_t n, F f) {
   SSD_NORM_PLAN(64, 2)
   SSD_NORM_PLAN(256, 1)
   SSD_NORM_PLAN(256, 2)
-  SSD_NORM_PLAN(256, 4)
-  SSD_NORM_PLAN(256, 8)
+  SSD_NORM_PLAN(kBlockTeam, 1)
+  SSD_NORM_PLAN(kBlockTeam, 2)
 #undef SSD_NORM_PLAN
 }
 template <class F>
@@ -586,7 +606,7 @@ int launch_add_norm_fwd(const void* x, const void* res, const float* scale, cons
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
         hipLaunchKernelGGL((add_norm_fwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
-                           dim3(kNormThreads), 0, (hipStream_t)stream, x, res, scale, weight, y,
+                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale, weight, y,
                            res_out, l.g);
       });
     });
@@ -606,7 +626,7 @@ int launch_add_norm_bwd(const void* x, const void* res, const float* scale, cons
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
         hipLaunchKernelGGL((add_norm_bwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
-                           dim3(kNormThreads), 0, (hipStream_t)stream, x, res, scale, weight, dy,
+                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale, weight, dy,
                            dres_out, dx, dres, ps, pw, l.g);
       });
     });
@@ -624,7 +644,7 @@ int launch_gated_norm_fwd(const void* x, const void* z, const float* weight, voi
     with_bool(xbf16, [&](auto xb) {
       with_bool(zbf16, [&](auto zb) {
         hipLaunchKernelGGL((gated_norm_fwd_kernel<ts(), nv(), rag(), xb(), zb()>), l.grid,
-                           dim3(kNormThreads), 0, (hipStream_t)stream, x, z, weight, y, silu,
+                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, z, weight, y, silu,
                            first, l.g);
       });
     });
@@ -642,7 +662,7 @@ int launch_gated_norm_bwd(const void* x, const void* z, const float* weight, con
     with_bool(xbf16, [&](auto xb) {
       with_bool(zbf16, [&](auto zb) {
         hipLaunchKernelGGL((gated_norm_bwd_kernel<ts(), nv(), rag(), xb(), zb()>), l.grid,
-                           dim3(kNormThreads), 0, (hipStream_t)stream, x, z, weight, dy, dx, dz,
+                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, z, weight, dy, dx, dz,
                            pw, silu, first, l.g);
       });
     });
