@@ -613,8 +613,7 @@ def _run_linattn_fwd(d, ins, v, o, final_state, workspace, scale) -> None:
     dev = v.device
     _call("ssd_linattn_fwd", dev, *ins, _arg(o, "o", v.shape, (v.dtype,), dev),
           _arg(final_state, "final_state", (d.nseq, d.nheads, d.dk, d.dv), _F32, dev, True),
-          *_workspace(workspace, dev), d.dk ** -0.5 if scale is None else scale,
-          _dtype_code(v.dtype), d)
+          *workspace, d.dk ** -0.5 if scale is None else scale, _dtype_code(v.dtype), d)
 
 
 def _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit, workspace, scale) -> None:
@@ -623,7 +622,7 @@ def _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit, workspace, s
     _call("ssd_linattn_bwd", dev, *ins, _arg(dout, "dout", v.shape, own, dev),
           _arg(dfinal, "dfinal", state, _F32, dev, True), _arg(dq, "dq", q.shape, own, dev),
           _arg(dk, "dk", q.shape, own, dev), _arg(dv, "dv", v.shape, own, dev),
-          _arg(dinit, "dinit", state, _F32, dev, True), *_workspace(workspace, dev),
+          _arg(dinit, "dinit", state, _F32, dev, True), *workspace,
           d.dk ** -0.5 if scale is None else scale, _dtype_code(v.dtype), d)
 
 
@@ -640,7 +639,7 @@ def ssd_linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     ``workspace`` has linattn_workspace_bytes(dims, dtype) bytes.  scale None:
     K^-0.5."""
     d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
-    _run_linattn_fwd(d, ins, v, o, final_state, workspace, scale)
+    _run_linattn_fwd(d, ins, v, o, final_state, _workspace(workspace, v.device), scale)
 
 
 def ssd_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -652,7 +651,8 @@ def ssd_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Gradients of ``ssd_linattn_fwd`` for dout [b, L, H, V] and dfinal (or
     None) into dq, dk, dv and dinit (or None).  log_decay has none."""
     d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
-    _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit, workspace, scale)
+    _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit,
+                     _workspace(workspace, v.device), scale)
 
 
 def ssd_linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -710,6 +710,12 @@ def ssd_add_norm_bwd(x: torch.Tensor, residual: Optional[torch.Tensor],
                      workspace: torch.Tensor, eps: float = 1e-5) -> None:
     """Gradients of ``ssd_add_norm_fwd`` from its inputs.  ``workspace`` has
     add_norm_workspace_bytes(rows, dim) bytes."""
+    _run_add_norm_bwd(x, residual, res_scale, weight, dy, dresidual_out, dx, dresidual,
+                      dres_scale, dweight, _workspace(workspace, x.device), eps)
+
+
+def _run_add_norm_bwd(x, residual, res_scale, weight, dy, dresidual_out, dx, dresidual,
+                      dres_scale, dweight, workspace, eps) -> None:
     rows, D = _rows(x, "x")
     dev, shape, own = x.device, x.shape, (x.dtype,)
     rdt = next((t.dtype for t in (residual, dresidual_out) if t is not None), x.dtype)
@@ -722,8 +728,8 @@ def ssd_add_norm_bwd(x: torch.Tensor, residual: Optional[torch.Tensor],
           _arg(dx, "dx", shape, own, dev),
           _arg(dresidual, "dresidual", shape, (rdt,), dev, True),
           _arg(dres_scale, "dres_scale", (D,), _F32, dev, True),
-          _arg(dweight, "dweight", (D,), _F32, dev, True), *_workspace(workspace, dev), rows, D,
-          eps, _dtype_code(x.dtype), _dtype_code(rdt))
+          _arg(dweight, "dweight", (D,), _F32, dev, True), *workspace, rows, D, eps,
+          _dtype_code(x.dtype), _dtype_code(rdt))
 
 
 def add_norm_workspace_bytes(rows: int, dim: int) -> int:
@@ -781,17 +787,22 @@ def ssd_gated_norm_bwd(x: torch.Tensor, z: Optional[torch.Tensor],
     """Gradients of ``ssd_gated_norm_fwd`` from its inputs.  ``workspace`` has
     gated_norm_workspace_bytes(dims) bytes."""
     d, ins = _gated_args(x, z, weight, group)
+    if isinstance(dweight, torch.Tensor) and weight is None:
+        d.weight_dim = dweight.numel()
+    _run_gated_norm_bwd(d, ins, x, z, dy, dx, dz, dweight, _workspace(workspace, x.device), eps,
+                        gate, gate_first)
+
+
+def _run_gated_norm_bwd(d, ins, x, z, dy, dx, dz, dweight, workspace, eps, gate,
+                        gate_first) -> None:
     dev, shape = x.device, x.shape
     if (z is None) != (dz is None):
         raise ValueError("dz is given exactly when z is")
-    if isinstance(dweight, torch.Tensor) and weight is None:
-        d.weight_dim = dweight.numel()
     _call("ssd_gated_norm_bwd", dev, *ins,
           _arg(dy, "dy", shape, _FLOATS if z is None else (z.dtype,), dev),
           _arg(dx, "dx", shape, (x.dtype,), dev), _arg(dz, "dz", shape, (dy.dtype,), dev, True),
-          _arg(dweight, "dweight", (d.weight_dim,), _F32, dev, True),
-          *_workspace(workspace, dev), eps, _gate(gate), int(gate_first), _dtype_code(x.dtype),
-          _dtype_code(dy.dtype), d)
+          _arg(dweight, "dweight", (d.weight_dim,), _F32, dev, True), *workspace, eps,
+          _gate(gate), int(gate_first), _dtype_code(x.dtype), _dtype_code(dy.dtype), d)
 
 
 # ------------------------------------------------------------ convenience
@@ -821,10 +832,13 @@ def forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
     return y, states, final
 
 
-def _bytes(n: int, dev: torch.device) -> torch.Tensor:
-    # invalid or unsupported dims report 0 bytes; the call itself then returns
-    # the precise status before touching the (minimal) workspace
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+def _scratch(n: int, dev: torch.device):
+    """A workspace, its address and its bytes.  Invalid or unsupported dims report
+    0 bytes; the call itself then returns the precise status before touching the
+    (minimal) workspace."""
+    n = max(n, 16)
+    t = torch.empty(n, dtype=torch.uint8, device=dev)
+    return t, (t.data_ptr(), n)
 
 
 def linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -836,7 +850,7 @@ def linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.
     d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
     o = torch.empty_like(v)
     final = torch.empty((d.nseq, d.nheads, d.dk, d.dv), dtype=torch.float32, device=q.device)
-    ws = _bytes(linattn_workspace_bytes(d, q.dtype), q.device)
+    keep, ws = _scratch(linattn_workspace_bytes(d, q.dtype), q.device)
     _run_linattn_fwd(d, ins, v, o, final, ws, scale)
     return o, final
 
@@ -852,7 +866,7 @@ def linattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dinit = torch.empty((d.nseq, d.nheads, d.dk, d.dv), dtype=torch.float32, device=q.device)
-    ws = _bytes(linattn_workspace_bytes(d, q.dtype, backward=True), q.device)
+    keep, ws = _scratch(linattn_workspace_bytes(d, q.dtype, backward=True), q.device)
     _run_linattn_bwd(d, ins, q, v, dout, dfinal, dq, dk, dv, dinit, ws, scale)
     return dq, dk, dv, dinit
 
@@ -878,9 +892,9 @@ def add_norm_backward(x: torch.Tensor, residual: Optional[torch.Tensor],
     dx = torch.empty_like(x)
     dres, dscale, dw = (None if t is None else torch.empty_like(t)
                         for t in (residual, res_scale, weight))
-    ws = _bytes(add_norm_workspace_bytes(rows, D), x.device)
-    ssd_add_norm_bwd(x, residual, res_scale, weight, dy, dresidual_out, dx, dres, dscale, dw, ws,
-                     eps)
+    keep, ws = _scratch(add_norm_workspace_bytes(rows, D), x.device)
+    _run_add_norm_bwd(x, residual, res_scale, weight, dy, dresidual_out, dx, dres, dscale, dw,
+                      ws, eps)
     return dx, dres, dscale, dw
 
 
@@ -901,9 +915,9 @@ def gated_norm_backward(x: torch.Tensor, z: Optional[torch.Tensor],
                         gate_first: bool = False) -> Tuple[Optional[torch.Tensor], ...]:
     """Allocate and run ``ssd_gated_norm_bwd``: (dx, dz, dweight), None for each
     of the last two whose input is None."""
-    d, _ = _gated_args(x, z, weight, group)
+    d, ins = _gated_args(x, z, weight, group)
     dx = torch.empty_like(x)
     dz, dw = (None if t is None else torch.empty_like(t) for t in (z, weight))
-    ws = _bytes(gated_norm_workspace_bytes(d), x.device)
-    ssd_gated_norm_bwd(x, z, weight, dy, dx, dz, dw, ws, eps, group, gate, gate_first)
+    keep, ws = _scratch(gated_norm_workspace_bytes(d), x.device)
+    _run_gated_norm_bwd(d, ins, x, z, dy, dx, dz, dw, ws, eps, gate, gate_first)
     return dx, dz, dw
