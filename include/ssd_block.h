@@ -66,7 +66,8 @@ size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims *dims, ssd_dtype d
  * initial state) or NULL.  They may be the same buffer (sequences continued
  * in place).  Sums and states are fp32; for bf16 tensors the state is rounded to
  * bf16 as an operand of q_t^T S.  A value of v that is not finite also reaches
- * the outputs of up to 63 tokens of its sequence and head before it.
+ * the outputs of up to 63 tokens of its sequence and head before it (in the
+ * gradients: one of k, q or dout those of dq, dk or dv that it is a part of).
  */
 ssd_status ssd_linattn_fwd(const void *q, const void *k, const void *v,
                            const float *log_decay, const float *init_state,

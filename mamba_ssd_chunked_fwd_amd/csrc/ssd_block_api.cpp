@@ -50,6 +50,10 @@ bool overlap(const void* a, const void* b, size_t n) {
   return x < y + n && y < x + n;
 }
 
+size_t state_bytes(const ssd::LinattnShape& s) {
+  return sizeof(float) * (size_t)(s.nseq * s.nheads) * (size_t)(s.dk * s.dv);
+}
+
 bool ok_workspace(const void* ws, size_t have, size_t need) {
   return ok_ptr(ws) && have >= need;
 }
@@ -97,6 +101,9 @@ ssd_status ssd_linattn_fwd(const void* q, const void* k, const void* v, const fl
   if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(log_decay) || !ok_opt(init_state) ||
       !ok_ptr(o) || !ok_opt(final_state))
     return SSD_ERR_INVALID_ARGUMENT;
+  // the whole buffer in place, or apart from it
+  if (init_state != final_state && overlap(init_state, final_state, state_bytes(s)))
+    return SSD_ERR_INVALID_ARGUMENT;
   const bool bf16 = dtype == SSD_BF16;
   if (!ok_workspace(workspace, workspace_bytes, ssd::linattn_workspace(s, bf16, false)))
     return SSD_ERR_WORKSPACE;
@@ -118,8 +125,7 @@ ssd_status ssd_linattn_bwd(const void* q, const void* k, const void* v, const fl
       !ok_opt(dinit))
     return SSD_ERR_INVALID_ARGUMENT;
   // dk is walked from dfinal while dv's walk writes dinit
-  if (overlap(dfinal, dinit, sizeof(float) * (size_t)(s.nseq * s.nheads) * (size_t)(s.dk * s.dv)))
-    return SSD_ERR_INVALID_ARGUMENT;
+  if (overlap(dfinal, dinit, state_bytes(s))) return SSD_ERR_INVALID_ARGUMENT;
   const bool bf16 = dtype == SSD_BF16;
   if (!ok_workspace(workspace, workspace_bytes, ssd::linattn_workspace(s, bf16, true)))
     return SSD_ERR_WORKSPACE;

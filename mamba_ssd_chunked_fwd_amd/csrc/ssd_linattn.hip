@@ -144,17 +144,20 @@ __device__ __forceinline__ Run find_run(const Seqs& s, int item) {
   return out;
 }
 
-// log2 of lam.  The clamp keeps a head without memory (log_decay -inf) from
-// giving 0 * inf: 2^(-1e30) is 0 and 2^0 is 1.
+// log_decay of a head, and log2 of lam.  The clamp keeps a head without memory
+// (-inf) from giving 0 * inf: e^(-1e30) is 0 and e^0 is 1.  NaN stays NaN.
+__device__ __forceinline__ float decay_of(const float* ld, int h) {
+  return ld[h] < -1e30f ? -1e30f : ld[h];
+}
 __device__ __forceinline__ float log2_decay(const float* ld, int h) {
-  return fmaxf(ld[h], -1e30f) * kLog2e;
+  return decay_of(ld, h) * kLog2e;
 }
 // lam^n as two fp32 terms.
 struct Power {
   float hi, lo;
 };
 __device__ __forceinline__ Power power(const float* ld, int h, int n) {
-  const double d = exp((double)fmaxf(ld[h], -1e30f) * (double)n);
+  const double d = exp((double)decay_of(ld, h) * (double)n);
   const float hi = (float)d;
   return Power{hi, (float)(d - (double)hi)};
 }
@@ -307,7 +310,7 @@ struct Factor {
   __device__ __forceinline__ float next() {
     const float t = __builtin_fmaf(-p.hi, off, p.lo);
     const float f = p.hi + t;
-    off = p.hi > 0.0f ? ((f - p.hi) - t) * __builtin_amdgcn_rcpf(p.hi) : 0.0f;
+    off = p.hi == 0.0f ? 0.0f : ((f - p.hi) - t) * __builtin_amdgcn_rcpf(p.hi);
     return f;
   }
 };
@@ -807,11 +810,16 @@ __global__ __launch_bounds__(kThreads) void run_starts_kernel(Walks ws, Seqs sq,
   }
 }
 
-// Sums the partial rows of the heads of each group, in their order.
+// Sums the partial rows of the heads of each group, in their order; blockIdx.y:
+// which of two gradients.
 template <bool BF16>
-__global__ __launch_bounds__(256) void sum_heads_kernel(const float* __restrict__ part,
-                                                        void* __restrict__ out, Seqs sq, int G,
+__global__ __launch_bounds__(256) void sum_heads_kernel(const float* __restrict__ part0,
+                                                        void* __restrict__ out0,
+                                                        const float* __restrict__ part1,
+                                                        void* __restrict__ out1, Seqs sq, int G,
                                                         int share, int D) {
+  const float* part = blockIdx.y ? part1 : part0;
+  void* out = blockIdx.y ? out1 : out0;
   const int64_t t0 = sq.at(0), t1 = sq.at(sq.nseq);
   const int64_t row = (int64_t)G * D / 4;
   const int64_t end = t1 * row, step = (int64_t)gridDim.x * blockDim.x;
@@ -890,17 +898,17 @@ int walks_of(const Walks& w, const Walks& states, const Seqs& sq, const float* l
   return s.dv == 64 ? go(I128{}, I64{}) : go(I128{}, I128{});
 }
 
-int sum_heads(const float* part, void* out, const Seqs& sq, bool bf16, const LinattnShape& s,
-              hipStream_t st) {
+int sum_heads(const float* pq, void* dq, const float* pk, void* dk, const Seqs& sq, bool bf16,
+              const LinattnShape& s, hipStream_t st) {
   const int64_t units = s.tokens * s.ngroups * s.dk / 4;
   const unsigned blocks = (unsigned)(units < 256 * 2048 ? (units + 255) / 256 : 2048);
   const int share = (int)(s.nheads / s.ngroups);
   if (bf16)
-    hipLaunchKernelGGL((sum_heads_kernel<true>), dim3(blocks), dim3(256), 0, st, part, out, sq,
-                       (int)s.ngroups, share, (int)s.dk);
+    hipLaunchKernelGGL((sum_heads_kernel<true>), dim3(blocks, 2), dim3(256), 0, st, pq, dq, pk,
+                       dk, sq, (int)s.ngroups, share, (int)s.dk);
   else
-    hipLaunchKernelGGL((sum_heads_kernel<false>), dim3(blocks), dim3(256), 0, st, part, out, sq,
-                       (int)s.ngroups, share, (int)s.dk);
+    hipLaunchKernelGGL((sum_heads_kernel<false>), dim3(blocks, 2), dim3(256), 0, st, pq, dq, pk,
+                       dk, sq, (int)s.ngroups, share, (int)s.dk);
   return (int)hipGetLastError();
 }
 
@@ -958,10 +966,8 @@ int launch_linattn_bwd(const void* q, const void* k, const void* v, const float*
   states.w[0] = w.w[0];
   states.w[1] = w.w[2];
   states.w[1].slots_t = w.w[1].slots;
-  int err = walks_of<3, 2>(w, states, sq, log_decay, bf16, s, st);
-  if (err == 0 && parts) err = sum_heads(pq, dq, sq, bf16, s, st);
-  if (err == 0 && parts) err = sum_heads(pk, dk, sq, bf16, s, st);
-  return err;
+  const int err = walks_of<3, 2>(w, states, sq, log_decay, bf16, s, st);
+  return err || !parts ? err : sum_heads(pq, dq, pk, dk, sq, bf16, s, st);
 }
 
 }  // namespace ssd

@@ -94,6 +94,8 @@ def test_linattn_rejects_bad_arguments():
     assert bwd(d, init=MISALIGNED) == INV and bwd(d, dfin=MISALIGNED) == INV
     assert bwd(d, dinit=MISALIGNED) == INV
     assert fwd(d, cu=ODD) == INV and bwd(d, cu=ODD) == INV
+    # final over part of init (the whole of it is a sequence continued in place)
+    assert fwd(d, init=FAKE, fin=ctypes.c_void_p(FAKE.value + 4096)) == INV
     # dinit over dfinal, whole or in part
     assert bwd(d, dfin=FAKE, dinit=FAKE) == INV
     assert bwd(d, dfin=FAKE, dinit=ctypes.c_void_p(FAKE.value + 4096)) == INV

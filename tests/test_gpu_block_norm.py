@@ -55,6 +55,8 @@ ADD_CASES = [
     (3, 4104, "fp32", "fp32", True, True, False),
     (4, 5119, "bf16", "bf16", True, True, True),
     (2, 16384, "bf16", "fp32", True, True, True),
+    (3, 8200, "bf16", "bf16", True, True, True),
+    (3, 16383, "bf16", "fp32", True, True, True),
     (4, 128, "bf16", None, True, True, True),
     (4, 128, "fp32", None, False, True, False),
 ]
@@ -102,6 +104,10 @@ GATE_CASES = [
     (40, 512, 128, "dim", "bf16", "bf16", "silu", False, False),
     (40, 512, 128, "group", "fp32", "fp32", "silu", True, False),
     (2100, 40, 8, "dim", "bf16", "bf16", "silu", True, True),
+    (33, 30, 3, "group", "bf16", "bf16", "silu", False, True),      # less than a vector
+    (33, 77, 11, "dim", "bf16", "fp32", "silu", True, True),        # vectors that overlap
+    (5, 9000, 9000, "dim", "bf16", "bf16", "silu", True, True),
+    (5, 8193, 8193, "dim", "fp32", "bf16", "sigmoid", False, True),
 ]
 
 
@@ -162,17 +168,18 @@ def test_a_row_of_nan_stays_alone(ssd):
     assert torch.isnan(y[4]).all()
 
 
-def test_in_place(ssd):
+@pytest.mark.parametrize("dim", [768, 771, 4999])
+def test_in_place(ssd, dim):
     g = torch.Generator().manual_seed(6)
-    x, r, dy, dh = (torch.randn(50, 768, generator=g).to(torch.bfloat16).to(DEV) for _ in range(4))
-    w = torch.randn(768, generator=g).to(DEV)
+    x, r, dy, dh = (torch.randn(50, dim, generator=g).to(torch.bfloat16).to(DEV) for _ in range(4))
+    w = torch.randn(dim, generator=g).to(DEV)
     y, h = ssd.add_norm(x, r, None, w)
     x2, r2 = x.clone(), r.clone()
     ssd.ssd_add_norm_fwd(x2, r2, None, w, x2, r2)
     assert torch.equal(x2, y) and torch.equal(r2, h)
     dx, dres, _, dw = ssd.add_norm_backward(x, r, None, w, dy, dh)
     dy2, dh2, dw2 = dy.clone(), dh.clone(), torch.empty_like(w)
-    ws = torch.empty(ssd.add_norm_workspace_bytes(50, 768), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(ssd.add_norm_workspace_bytes(50, dim), dtype=torch.uint8, device=DEV)
     ssd.ssd_add_norm_bwd(x, r, None, w, dy2, dh2, dy2, dh2, None, dw2, ws)
     assert torch.equal(dy2, dx) and torch.equal(dh2, dres) and torch.equal(dw2, dw)
     y = ssd.gated_norm(x, r, w)
@@ -183,7 +190,7 @@ def test_in_place(ssd):
     dx, dz, dw = ssd.gated_norm_backward(x, r, w, dy)
     dy2 = dy.clone()
     dx2 = torch.empty_like(x)
-    d = ssd.GatedNormDims(50, 768, 768, 768)
+    d = ssd.GatedNormDims(50, dim, dim, dim)
     ws = torch.empty(ssd.gated_norm_workspace_bytes(d), dtype=torch.uint8, device=DEV)
     ssd.ssd_gated_norm_bwd(x, r, w, dy2, dx2, dy2, dw2, ws)
     assert torch.equal(dy2, dz) and torch.equal(dx2, dx) and torch.equal(dw2, dw)

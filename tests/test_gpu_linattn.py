@@ -181,6 +181,18 @@ def test_a_sequence_of_nan_and_inf_stays_alone(ssd, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_nan_decay_stays_in_its_head(ssd, dtype):
+    s = make((150,), 3, 3, 64, 64, dtype, seed=12, decays=[-0.1, float("nan"), -0.1])
+    d = on_gpu(s)
+    got = forward(ssd, d)
+    ref = reference(dict(s, ld=torch.tensor([-0.1, -0.1, -0.1])))
+    assert torch.isnan(got["final"][:, 1]).all() and torch.isnan(got["o"][1:, 1]).all()
+    keep = [0, 2]
+    check({"o": got["o"][:, keep], "final": got["final"][:, keep]},
+          {"o": ref["o"][:, keep], "final": ref["final"][:, keep]}, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_batch_form_equals_packed_form(ssd, dtype):
     s = make((150,) * 3, 4, 2, 64, 128, dtype, seed=13)
     d = on_gpu(s)
@@ -379,6 +391,16 @@ def test_refusals(ssd):
     assert e.value.status == ssd.SSD_ERR_WORKSPACE
 
 
+def test_many_sequences_and_heads(ssd):
+    """More sequences than a workgroup has threads, many of them empty, and
+    enough heads that a sequence is one run."""
+    lens = [(7 * i) % 5 if i % 3 else 0 for i in range(700)]
+    s = make(lens, 24, 8, 64, 64, "bf16", seed=47)
+    d, ref = on_gpu(s), reference(s)
+    check(forward(ssd, d), ref, "bf16")
+    check(backward(ssd, d), ref, "bf16")
+
+
 def test_bad_offsets_stay_in_range(ssd):
     """Offsets below zero, past the tokens, or descending are taken as the
     nearer end or as empty sequences; sequences that are sound keep their
@@ -392,3 +414,12 @@ def test_bad_offsets_stay_in_range(ssd):
     d["cu"] = torch.tensor([40, 40, 10], dtype=torch.int32, device=DEV)
     got = forward(ssd, d)                 # two empty ones
     assert torch.equal(got["final"], d["init"])
+    # sequences that overlap: any result, but a call that ends, and nothing else hurt
+    s = make((3000,), 2, 2, 64, 64, "bf16", seed=44)
+    d = on_gpu(s)
+    want = forward(ssd, d)
+    odd = dict(d, cu=torch.tensor([0, 2900, 100, 3000, 50], dtype=torch.int32, device=DEV),
+               init=None, dfinal=None)
+    forward(ssd, odd)
+    backward(ssd, odd)
+    assert torch.equal(forward(ssd, d)["o"], want["o"])
