@@ -222,7 +222,8 @@ __device__ __forceinline__ void store_partial(const float* acc, float* part, con
       if (writes) {
         for (int k = 1; k < span; ++k) {
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) v[e] += buf[e * kNormThreads + threadIdx.x + k * step * TS];
+          for (int e = 0; e < kVec; ++e)
+            v[e] += buf[e * kNormThreads + threadIdx.x + k * step * TS];
         }
       }
     }
@@ -395,7 +396,8 @@ __global__ __launch_bounds__(max_threads<TS>()) void gated_norm_fwd_kernel(
       if (sp.on) {
         float v[kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = u[j * kVec + e] * r * w[j * kVec + e] * a[j * kVec + e];
+        for (int e = 0; e < kVec; ++e)
+          v[e] = u[j * kVec + e] * r * w[j * kVec + e] * a[j * kVec + e];
         store_n<ZB, RAGGED>(y, base + c, g.n - c, v);
       }
     }
@@ -606,8 +608,8 @@ int launch_add_norm_fwd(const void* x, const void* res, const float* scale, cons
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
         hipLaunchKernelGGL((add_norm_fwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
-                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale, weight, y,
-                           res_out, l.g);
+                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale,
+                           weight, y, res_out, l.g);
       });
     });
   });
@@ -626,8 +628,8 @@ int launch_add_norm_bwd(const void* x, const void* res, const float* scale, cons
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
         hipLaunchKernelGGL((add_norm_bwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
-                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale, weight, dy,
-                           dres_out, dx, dres, ps, pw, l.g);
+                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale,
+                           weight, dy, dres_out, dx, dres, ps, pw, l.g);
       });
     });
   });
@@ -662,8 +664,8 @@ int launch_gated_norm_bwd(const void* x, const void* z, const float* weight, con
     with_bool(xbf16, [&](auto xb) {
       with_bool(zbf16, [&](auto zb) {
         hipLaunchKernelGGL((gated_norm_bwd_kernel<ts(), nv(), rag(), xb(), zb()>), l.grid,
-                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, z, weight, dy, dx, dz,
-                           pw, silu, first, l.g);
+                           dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, z, weight, dy,
+                           dx, dz, pw, silu, first, l.g);
       });
     });
   });

@@ -180,11 +180,16 @@ struct Shape2 {
   static constexpr int XBYTES = C * YS * ES;
   static constexpr int ZBYTES = C * ZS * ES;
   static constexpr int PBYTES = (BF16 ? 2 : 1) * C * PS * ES;   // the scores, bf16 as two terms
+  // A 128 x 128 M leaves registers for two workgroups of a CU only, whose LDS has
+  // room for the scores beside X (a barrier less per chunk) and whose registers
+  // have some left for the decays: 1 to 2% of such a walk.  The others keep three
+  // workgroups by letting the scores take X's place and the decays wait in LDS.
+  static constexpr bool ROOMY = YD == 128 && ZD == 128;
   static constexpr int DBYTES = 3 * kWave * 16;                 // decays, four per lane
   static constexpr int WBYTES = C * 4;                          // the weights of Z
-  // the scores take the place of X once it is read
-  static constexpr int BYTES =
-      WBYTES + XBYTES + ZBYTES + (XBYTES > PBYTES ? XBYTES : PBYTES) + DBYTES;
+  static constexpr int XPBYTES =
+      ROOMY ? XBYTES + PBYTES : XBYTES > PBYTES ? XBYTES : PBYTES;   // X and the scores
+  static constexpr int BYTES = WBYTES + XBYTES + ZBYTES + XPBYTES + (ROOMY ? 0 : DBYTES);
   static constexpr int STATE_BYTES = XBYTES + ZBYTES + WBYTES;
   static constexpr int YU = C * YD * ES / 16 / kThreads;   // 16-byte units per thread
   static constexpr int ZU = C * ZD * ES / 16 / kThreads;
@@ -224,20 +229,13 @@ struct Tile {
                                (uint32_t)(n - 1) * row + D * ES);
     constexpr int PER = D * ES / 16, STEP = kThreads / PER;    // units of a row, rows at a time
     const int i = tid / PER, c = tid % PER;
-    if (n == C) {                                              // the units' rows are STEP apart
-      const uint32_t off = (uint32_t)(down ? C - 1 - (U - 1) * STEP - i : i) * row + c * 16;
+    // (one form for whole and ragged tiles: a branch here keeps the loads from being
+    // spread over the products around them, and costs 10% of a 128 x 128 walk)
 #pragma unroll
-      for (int j = 0; j < U; ++j)
-        v[j] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       r, (int)off, (int)((uint32_t)((down ? U - 1 - j : j) * STEP) * row), 0));
-    } else {
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int ij = i + j * STEP;
-        const uint32_t off = (uint32_t)(down ? n - 1 - ij : ij) * row + c * 16;
-        v[j] = load_b128(r, ij < n ? off : kPastRange);
-      }
+    for (int j = 0; j < U; ++j) {
+      const int ij = i + j * STEP;
+      const uint32_t off = (uint32_t)(down ? n - 1 - ij : ij) * row + c * 16;
+      v[j] = load_b128(r, ij < n ? off : kPastRange);
     }
   }
   template <bool SLOTS>
@@ -270,34 +268,25 @@ __device__ __forceinline__ void store_rows(const Walk& w, const f32x4 (&o)[NB][N
   const uint32_t orow = (uint32_t)(oheads * ZD * oes);
   const rsrc_t orr = make_rsrc((char*)w.out + (lowest * oheads + h / w.oshare) * (ZD * oes),
                                (uint32_t)(n - 1) * orow + ZD * oes);
-  auto store = [&](int tb, uint32_t at, int more) {
+#pragma unroll
+  for (int tb = 0; tb < NB; ++tb) {
+    const int i = 16 * tb + lr;
+    const uint32_t at = i < n ? (uint32_t)(w.down ? n - 1 - i : i) * orow : kPastRange;
     if (f32o) {
 #pragma unroll
       for (int nz = 0; nz < NZ; ++nz)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[tb][nz]), orr,
-                                               (int)(at + S::zcol(wave, nz, 4 * lq) * 4), more, 0);
+                                               (int)(at + S::zcol(wave, nz, 4 * lq) * 4), 0, 0);
     } else {
       const int off = (int)(at + S::zcol(wave, 0, 4 * lq) * 2);
       const u32x2 a = {pack_bf16(o[tb][0][0], o[tb][0][1]), pack_bf16(o[tb][0][2], o[tb][0][3])};
       if constexpr (NZ == 2) {
         const u32x2 b = {pack_bf16(o[tb][1][0], o[tb][1][1]),
                          pack_bf16(o[tb][1][2], o[tb][1][3])};
-        __builtin_amdgcn_raw_buffer_store_b128((u32x4){a[0], a[1], b[0], b[1]}, orr, off, more, 0);
+        __builtin_amdgcn_raw_buffer_store_b128((u32x4){a[0], a[1], b[0], b[1]}, orr, off, 0, 0);
       } else {
-        __builtin_amdgcn_raw_buffer_store_b64(a, orr, off, more, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(a, orr, off, 0, 0);
       }
-    }
-  };
-  if (n == S::C) {                                             // blocks are 16 rows apart
-    const uint32_t at = (uint32_t)(w.down ? 15 - lr : lr) * orow;
-#pragma unroll
-    for (int tb = 0; tb < NB; ++tb)
-      store(tb, at, (int)((uint32_t)(w.down ? NB - 1 - tb : tb) * 16 * orow));
-  } else {
-#pragma unroll
-    for (int tb = 0; tb < NB; ++tb) {
-      const int i = 16 * tb + lr;
-      store(tb, i < n ? (uint32_t)(w.down ? n - 1 - i : i) * orow : kPastRange, 0);
     }
   }
 }
@@ -339,8 +328,8 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   char* ys = lds + S::WBYTES;
   char* zs = ys + S::XBYTES;
   char* xs = zs + S::ZBYTES;
-  char* ps = xs;
-  f32x4* dtab = (f32x4*)(xs + (S::XBYTES > S::PBYTES ? S::XBYTES : S::PBYTES));
+  char* ps = S::ROOMY ? xs + S::XBYTES : xs;
+  f32x4* dtab = (f32x4*)(xs + S::XPBYTES);
 
   // Whether M goes on to a state in memory, where fp32 is asked for, or only
   // into outputs of the tensors' type.
@@ -409,10 +398,10 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     }
   }
 
-  if (OUT && wave == 0) {
-    // Per lane: the decays of its four scores in a diagonal block, in the block
-    // below it, and those of X^T M for its token of each block.
-    f32x4 d0, d1, dx = {};
+  // Per lane: the decays of its four scores in a diagonal block, in the block below
+  // it, and those of X^T M for its token of each block.
+  f32x4 d0 = {}, d1 = {}, dx = {};
+  if (OUT && (S::ROOMY || wave == 0)) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int d = lr - 4 * lq - r;
@@ -420,9 +409,11 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
       d1[r] = w.cx * w.cz * exp2_hw(l2 * (float)(16 + d));
       if (r < NB) dx[r] = w.cx * exp2_hw(l2 * (float)(16 * r + lr + a));
     }
-    dtab[lane] = d0;
-    dtab[kWave + lane] = d1;
-    dtab[2 * kWave + lane] = dx;
+    if constexpr (!S::ROOMY) {
+      dtab[lane] = d0;
+      dtab[kWave + lane] = d1;
+      dtab[2 * kWave + lane] = dx;
+    }
   }
   Factor lam{power(log_decay, h, C), 0.0f};
 
@@ -460,7 +451,8 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     // `apart` blocks on.  Where j > i the score is selected away, never multiplied
     // by 0.
     auto decayed = [&](f32x4& d, int apart) {
-      const f32x4 dec = dtab[(apart > 0 ? kWave : 0) + (fresh & (kWave - 1))];
+      const f32x4 dec = S::ROOMY ? (apart > 0 ? d1 : d0)
+                                 : dtab[(apart > 0 ? kWave : 0) + (fresh & (kWave - 1))];
       const float far = exp2_hw(l2 * (float)(16 * (apart > 1 ? apart - 1 : 0)));
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -481,7 +473,7 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
       f32x4 o[NB][NZ] = {};
       if constexpr (OUT) {
         // (1) the ten score blocks on and below the diagonal, transposed (Y X^T),
-        // two or three per wave; they wait in registers until X is read
+        // two or three per wave; where they take X's place they wait until it is read
         u32x2 sh[3], sl[3];
         auto score = [&](int id, u32x2& hi, u32x2& lo) {
           const int tb = id > 5 ? 3 : id > 2 ? 2 : id > 0 ? 1 : 0, sb = id - tb * (tb + 1) / 2;
@@ -496,7 +488,22 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         score(wave, sh[0], sl[0]);
         score(wave + 4, sh[1], sl[1]);
         if (wave < 2) score(wave + 8, sh[2], sl[2]);
-        __builtin_amdgcn_sched_barrier(0);
+        auto write_scores = [&] {
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            const int id = wave + 4 * e;
+            if (id > 9) break;
+            const int tb = id > 5 ? 3 : id > 2 ? 2 : id > 0 ? 1 : 0, sb = id - tb * (tb + 1) / 2;
+            const int at = (16 * tb + lr) * PS + slot_of(16 * sb) + 8 * lq;
+            *(u32x2*)(ph + at) = sh[e];
+            *(u32x2*)(pl + at) = sl[e];
+            if (sb == tb && tb % 2 == 0) {   // the block above the diagonal is read too
+              *(u32x2*)(ph + at + 4) = (u32x2){0, 0};
+              *(u32x2*)(pl + at + 4) = (u32x2){0, 0};
+            }
+          }
+        };
+        if constexpr (S::ROOMY) write_scores();
         // (2) X^T M, transposed, for all tokens
 #pragma unroll
         for (int kk = 0; kk < NY / 2; ++kk) {
@@ -514,27 +521,16 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
 #pragma unroll
             for (int nz = 0; nz < NZ; ++nz) o[tb][nz] = mfma_bf16(mb[nz], xf[tb], o[tb][nz]);
           }
-          if (kk % 2) __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
-          const float ex = dtab[2 * kWave + (fresh & (kWave - 1))][tb];
+          const float ex = S::ROOMY ? dx[tb] : dtab[2 * kWave + (fresh & (kWave - 1))][tb];
 #pragma unroll
           for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex;
         }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          const int id = wave + 4 * e;
-          if (id > 9) break;
-          const int tb = id > 5 ? 3 : id > 2 ? 2 : id > 0 ? 1 : 0, sb = id - tb * (tb + 1) / 2;
-          const int at = (16 * tb + lr) * PS + slot_of(16 * sb) + 8 * lq;
-          *(u32x2*)(ph + at) = sh[e];
-          *(u32x2*)(pl + at) = sl[e];
-          if (sb == tb && tb % 2 == 0) {   // the block above the diagonal is read too
-            *(u32x2*)(ph + at + 4) = (u32x2){0, 0};
-            *(u32x2*)(pl + at + 4) = (u32x2){0, 0};
-          }
+        if constexpr (!S::ROOMY) {
+          __syncthreads();
+          write_scores();
         }
         __syncthreads();
       }
@@ -620,7 +616,6 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
       using Term2 = std::integral_constant<int, 2>;
       if constexpr (OUT) {
         update(Term0{}, Term1{});
-        __builtin_amdgcn_sched_barrier(0);
         if (exact) update(Term2{}, Term2{});
       } else {
         update(Term0{}, Term2{});
@@ -661,11 +656,11 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
-          const float ex = dtab[2 * kWave + (fresh & (kWave - 1))][tb];
+          const float ex = S::ROOMY ? dx[tb] : dtab[2 * kWave + (fresh & (kWave - 1))][tb];
 #pragma unroll
           for (int nz = 0; nz < NZ; ++nz) o[tb][nz] *= ex;
         }
-        __syncthreads();
+        if constexpr (!S::ROOMY) __syncthreads();
         if (wave < 3) *(f32x4*)(pl + (16 * tb3 + lr) * PS + 16 * sb3 + 4 * lq) = d;
         __syncthreads();
       }
@@ -847,7 +842,8 @@ constexpr int64_t kMinChunks = 2;
 
 int run_tokens(const LinattnShape& s, bool bf16, int walks) {
   const int64_t C = bf16 ? 64 : 32;
-  const int64_t wgs = kCus * (s.dk == 128 && s.dv == 128 ? resident<128, 128>() : resident<64, 64>());
+  const int64_t wgs =
+      kCus * (s.dk == 128 && s.dv == 128 ? resident<128, 128>() : resident<64, 64>());
   const int64_t each = 3 * wgs / (s.nheads * walks);           // thirds of runs for a head
   const int64_t ends = 2 * s.nseq < each / 2 ? 2 * s.nseq : each / 2;
   int64_t chunks = each > ends ? (3 * s.tokens + (each - ends) * C - 1) / ((each - ends) * C)
