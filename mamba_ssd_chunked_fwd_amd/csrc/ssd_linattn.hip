@@ -28,10 +28,11 @@
 //     consecutive rows of each block) is the operand of X^T M whose k slots
 //     run over those rows; X is read from LDS in the same slot order;
 //   - the scores are formed transposed (Y X^T: a lane holds one token i and four
-//     consecutive j), so decayed, masked by a select and rounded they are the
-//     operand of the sum over j as they sit; Z comes from the LDS transpose read;
-//   - the output comes out transposed too, one token and 8 (fp32: 4)
-//     consecutive columns per lane: 16-byte stores.
+//     consecutive j), the blocks on and below the diagonal shared out among the
+//     waves; decayed and masked by a select they go through LDS, in slot order
+//     again, to every wave; Z comes from the LDS transpose read;
+//   - the output comes out transposed too, one token and 8 (fp32, or 64 columns: 4)
+//     consecutive columns per lane: 16- or 8-byte stores.
 // bf16 tensors: 16x16x32 bf16 products, chunks of 64.  M is rounded to bf16 as the
 // operand of X^T M: that part of the output gets an error as large as the
 // output's own rounding.  The scores are split into two bf16 terms, and so is the
@@ -41,8 +42,8 @@
 // calls are bound by the matrix pipe).
 //
 // The chains of a call are few (sequences x heads) and long, so each is cut
-// into runs of equal numbers of chunks, walked at once by (about) two workgroups
-// per CU:
+// into runs of equal numbers of chunks, walked at once by the two or three
+// workgroups a CU holds:
 //   1. run_states: M at the end of the first run, and what every later run but
 //      the last adds to M from zero, into a slot each;
 //   2. run_starts, for sequences of more than kFold runs: M at the start of every
@@ -53,6 +54,14 @@
 // powers of lam that are multiplied up along a chain are taken in 64 bits and
 // kept as two fp32 terms, or corrected from chunk to chunk: the rounding of one
 // factor would otherwise grow with the number of chunks.
+//
+// Measured on MI355X (bf16; a device copy moves 5.1 TB/s).  8 x 2048 tokens, 16
+// heads of 128 x 128: run_states 36 us, walks 75 us (300 MB: 4.0 TB/s).  Gradients
+// of 16384 tokens, 32 heads of 128 x 128: run_states 187 us, the three walks 460 us
+// (1.5 GB: 3.2 TB/s; matrix pipe 24% busy, vector unit 30%, LDS 31%).  65536
+// tokens, 32 heads of 128 x 64 on one group: run_states 146 us, walks 325 us;
+// there q and k come from the caches and the LDS (54% busy), the vector unit (39%)
+// and the matrix pipe (24%) bound it together.
 #include "ssd_block_launch.h"
 #include "ssd_device.h"
 #include "ssd_host.h"

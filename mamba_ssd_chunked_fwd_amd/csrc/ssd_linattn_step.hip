@@ -11,6 +11,11 @@
 // columns, its four values of v and its part of o stay the same.  The
 // columns are what is split for small batches (they are independent; rows meet
 // in o): CB = 8, 4, 2 or 1, the smallest that gives every CU a workgroup.
+//
+// Measured on MI355X: 200 sequences of 32 heads of 128 x 64 (422 MB) 62 us under the
+// profiler, where half the state still lies in the last-level cache, 80 us over
+// rotating states (5.3 TB/s; a device copy moves 5.1); one sequence of 32 heads of
+// 128 x 128 4 us, of which a launch is the most.
 #include "ssd_block_launch.h"
 #include "ssd_device.h"
 #include "ssd_host.h"
