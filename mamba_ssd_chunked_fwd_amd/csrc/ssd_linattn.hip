@@ -308,7 +308,9 @@ struct Factor {
   __device__ __forceinline__ float next() {
     const float t = __builtin_fmaf(-p.hi, off, p.lo);
     const float f = p.hi + t;
-    off = p.hi == 0.0f ? 0.0f : ((f - p.hi) - t) * __builtin_amdgcn_rcpf(p.hi);
+    // (a power this small leaves nothing of the chunk before; the reciprocal of a
+    // denormal one would be infinite)
+    off = p.hi < 1e-30f ? 0.0f : ((f - p.hi) - t) * __builtin_amdgcn_rcpf(p.hi);
     return f;
   }
 };

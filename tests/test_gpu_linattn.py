@@ -138,6 +138,17 @@ def test_decays_from_none_to_no_memory(ssd, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_decays_whose_power_over_a_chunk_is_denormal(ssd, dtype):
+    """exp(log_decay) to the power of a chunk's 64 (32) tokens around and below the
+    smallest normal fp32 number, 1.2e-38 = e^-87.3."""
+    decays = [-1.36, -1.37, -1.5, -1.6, -1.62, -2.7, -2.75, -3.0, -3.2, -3.3]
+    s = make((300, 210), 10, 5, 64, 64, dtype, seed=6, decays=decays)
+    d, ref = on_gpu(s), reference(s)
+    check(forward(ssd, d), ref, dtype)
+    check(backward(ssd, d), ref, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_rows_outside_are_neither_read_nor_written(ssd, dtype):
     s = make((70, 0, 200), 4, 2, 128, 64, dtype, seed=9, before=5, after=67)
     d, ref = on_gpu(s), reference(s)
