@@ -285,3 +285,20 @@ def test_refusals(ssd):
         ssd.ssd_add_norm_bwd(x, None, None, w, x, None, torch.empty_like(x), None, None,
                              torch.empty_like(w), ws)
     assert e.value.status == ssd.SSD_ERR_WORKSPACE
+
+
+def test_offsets_past_32_bits(ssd):
+    """More than 2^31 elements, equal rows: the last has the first one's results."""
+    rows, dim, group = 70000, 31000, 248
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(1, dim, generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn(dim, generator=g, device=DEV)
+    want = ssd.gated_norm(x, x, w, EPS, group)
+    want_dx, want_dz, _ = ssd.gated_norm_backward(x, x, w, x, EPS, group)
+    x = x.expand(rows, dim).contiguous()
+    assert x.numel() > 2 ** 31
+    y = ssd.gated_norm(x, x, w, EPS, group)
+    assert torch.equal(y[:1], want) and torch.equal(y[-1:], want)
+    dx, dz, _ = ssd.gated_norm_backward(x, x, w, x, EPS, group)
+    for t, r in ((dx, want_dx), (dz, want_dz)):
+        assert torch.equal(t[:1], r) and torch.equal(t[-1:], r)

@@ -434,3 +434,29 @@ def test_bad_offsets_stay_in_range(ssd):
     forward(ssd, odd)
     backward(ssd, odd)
     assert torch.equal(forward(ssd, d)["o"], want["o"])
+
+
+def test_offsets_past_32_bits(ssd):
+    """More than 2^31 elements of v, o, dout and dv: the same sequence over and
+    over, whose last copy has the first one's results."""
+    n, L, H, G, K, V = 132, 1000, 128, 2, 64, 128
+    g = torch.Generator(device=DEV).manual_seed(1)
+
+    def rows(heads, size):
+        x = torch.randn(1, L, heads, size, generator=g, device=DEV).to(torch.bfloat16)
+        return x.expand(n, L, heads, size).contiguous()
+
+    q, k, v, do = rows(G, K), rows(G, K), rows(H, V), rows(H, V)
+    assert v.numel() > 2 ** 31
+    ld = -torch.exp2(-8.0 * torch.arange(1, H + 1, device=DEV) / H)
+    o, final = ssd.linattn(q, k, v, ld)
+    grads = ssd.linattn_backward(q, k, v, ld, do)
+    one = [t[:1].contiguous() for t in (q, k, v)]
+    want_o, want_final = ssd.linattn(*one, ld)
+    want = ssd.linattn_backward(*one, ld, do[:1].contiguous())
+    # (another number of runs: sums in another order)
+    for a, b, dt in ((o, want_o, "bf16"), (final, want_final, "fp32"),
+                     *zip(grads, want, ("bf16", "bf16", "bf16", "fp32"))):
+        assert torch.equal(a[-1], a[0])
+        err = float((a[-1].double() - b[0].double()).norm() / b[0].double().norm())
+        assert err <= 2 * max(TOL[DTYPES[dt]], STATE_TOL[DTYPES[dt]]), err
