@@ -39,12 +39,12 @@ extern "C" {
  * cu_seqlens[i] .. cu_seqlens[i+1]-1 and may be empty.  Rows outside
  * every sequence are not read and left as they are.  NULL: nseq sequences of
  * tokens / nseq tokens each.  Entries outside [0, tokens] are taken as the
- * nearer end, and descending ones as empty sequences; a call never reads or
- * writes out of range for them, but its results for overlapping sequences are
- * undefined.
+ * nearer end; where entries descend a call still reads and writes nothing out
+ * of range, but its results are undefined.
  *
- * Supported: K and V in {64, 128}; anything else valid returns
- * SSD_ERR_UNSUPPORTED.
+ * Supported: K and V in {64, 128}, up to 32768 heads, tokens * nheads below 2^27,
+ * nseq * nheads below 2^22 (of the recurrent form: tokens * nheads below 2^24);
+ * anything else valid returns SSD_ERR_UNSUPPORTED.
  */
 typedef struct {
     int64_t tokens;     /* T, rows of q, k, v and o               */
@@ -150,7 +150,8 @@ ssd_status ssd_add_norm_bwd(const void *x, const void *residual, const float *re
  * SSD_GATE_SIGMOID.  x [rows, dim] in x_dtype; z, y [rows, dim] in
  * z_dtype; z NULL: no gate.  weight [weight_dim] fp32 or NULL, weight_dim
  * being dim, or group (one set of weights for every group).  y may be the
- * same buffer as z, or as x where the types are equal.  eps > 0.  Supported: group up to 16384.
+ * same buffer as z, or as x where the types are equal.  eps > 0.
+ * Supported: group up to 16384, dim up to 2^27 and to 65535 groups.
  */
 typedef enum { SSD_GATE_SILU = 0, SSD_GATE_SIGMOID = 1 } ssd_gate;
 

@@ -18,8 +18,10 @@ bool ok_dtype(ssd_dtype t) { return t == SSD_F32 || t == SSD_BF16; }
 ssd_status from_hip(int err) { return err == 0 ? SSD_OK : SSD_ERR_HIP; }
 
 // Rows of one tensor are addressed with 64-bit offsets; what is bounded is
-// the number of workgroups of a launch (below 2^31) and each dimension.
-constexpr int64_t kMaxBlocks = INT32_MAX;
+// each dimension and the number of workgroups of a launch: of 256 threads below
+// 2^24, because a launch has at most 2^32 - 1 threads along an axis.
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+constexpr int64_t kMaxTokenHeads = (1 << 27) - 1;
 
 ssd_status check_linattn(const ssd_linattn_dims* d, bool step, ssd::LinattnShape* out) {
   if (d == nullptr) return SSD_ERR_INVALID_ARGUMENT;
@@ -28,9 +30,11 @@ ssd_status check_linattn(const ssd_linattn_dims* d, bool step, ssd::LinattnShape
   for (int64_t e : v)
     if (e < 1 || e > INT32_MAX) return SSD_ERR_INVALID_ARGUMENT;
   if (d->nheads % d->ngroups != 0) return SSD_ERR_INVALID_ARGUMENT;
-  // at most 16 workgroups for each head of a token or sequence
-  if (d->tokens > kMaxBlocks / 16 / d->nheads || nseq > kMaxBlocks / 16 / d->nheads)
-    return SSD_ERR_UNSUPPORTED;
+  // lengths in tokens, rounded up to chunks, and runs' numbers are 32-bit
+  if (d->tokens > kMaxTokenHeads / d->nheads) return SSD_ERR_UNSUPPORTED;
+  // a single token's call has one workgroup per head of a sequence where there are
+  // many; the others up to three, and below 2^20 more for the runs
+  if ((step ? d->tokens : 4 * nseq) > kMaxBlocks / d->nheads) return SSD_ERR_UNSUPPORTED;
   if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128)) return SSD_ERR_UNSUPPORTED;
   // one row of a tensor, and the 64 rows of a tile, stay below 2 GiB
   if (d->nheads > (1 << 15)) return SSD_ERR_UNSUPPORTED;
@@ -65,7 +69,8 @@ ssd_status check_norm(int64_t rows, int64_t dim, int64_t group, int64_t wdim, fl
   if (group > dim || dim % group != 0 || (wdim != dim && wdim != group))
     return SSD_ERR_INVALID_ARGUMENT;
   if (!(eps > 0.0f)) return SSD_ERR_INVALID_ARGUMENT;
-  if (group > ssd::kNormMaxGroup) return SSD_ERR_UNSUPPORTED;
+  // (dim: the row sums take 1024 threads for 64 channels)
+  if (group > ssd::kNormMaxGroup || dim > (1 << 27)) return SSD_ERR_UNSUPPORTED;
   // a row's groups are spread over the second grid axis, 65535 at most, of
   // at least one group each
   if (dim / group > 65535) return SSD_ERR_UNSUPPORTED;

@@ -845,7 +845,7 @@ __global__ __launch_bounds__(256) void sum_heads_kernel(const float* __restrict_
 
 // Tokens of a run: whole chunks, as few as keep the runs of all walks within the
 // workgroups the 256 CUs hold at once (a few more would wait for a second round),
-// with two thirds of a run allowed for the end of each sequence; at least eight
+// with two thirds of a run allowed for the end of each sequence; at least two
 // chunks (a shorter run costs more in states and in the launch that forms them
 // than it saves).
 constexpr int64_t kCus = 256;

@@ -80,6 +80,25 @@ def test_linattn_rejects_bad_dims(kw, expect):
     assert lib.ssd_linattn_bwd_workspace_bytes(_ref(d), ssd.SSD_BF16) == 0
 
 
+def test_linattn_rejects_launches_past_the_grid():
+    """A launch has fewer than 2^32 threads along an axis: 256 for each head of a
+    sequence, three times over for the gradients."""
+    d = ldims(tokens=1 << 22, nseq=1 << 20)
+    assert fwd(d, cu=FAKE) == UNS and bwd(d, cu=FAKE) == UNS and step(d) == UNS
+    assert lib.ssd_linattn_fwd_workspace_bytes(_ref(d), ssd.SSD_BF16) == 0
+    d = ldims(tokens=1 << 22, nseq=(1 << 20) - 1)
+    assert lib.ssd_linattn_fwd_workspace_bytes(_ref(d), ssd.SSD_BF16) > 0
+    # (within the limits, and refused for the argument)
+    assert fwd(d, cu=FAKE, ws=None) == WS and bwd(d, cu=FAKE, ws=None) == WS
+    assert step(ldims(tokens=(1 << 22) - 1), q=None) == INV
+
+
+def test_norms_reject_rows_past_the_grid():
+    for call in (gate_fwd, gate_bwd):
+        assert call(ndims(dim=1 << 28, group=1 << 14, weight_dim=1 << 28)) == UNS
+        assert call(ndims(dim=1 << 27, group=1 << 14, weight_dim=1 << 27), x=None) == INV
+
+
 def test_linattn_rejects_bad_arguments():
     d = ldims()
     assert fwd(None) == INV and bwd(None) == INV and step(None) == INV
