@@ -131,13 +131,16 @@ struct Run {
   int64_t slot;           // of the sequence's first run
 };
 
+// Sequences that begin at or before the item: a search in which every thread tests
+// the last of its share of those in question (one round up to 256 sequences, two up
+// to 65536).
 __device__ __forceinline__ Run find_run(const Seqs& s, int item) {
-  int before = 0;                        // sequences that begin at or before the item
-  for (int i0 = 0; i0 < s.nseq; i0 += kThreads) {
-    const int i = i0 + (int)threadIdx.x;
-    const int n = __syncthreads_count(i < s.nseq && s.at(i) / s.run + i <= item);
-    before += n;
-    if (n < kThreads) break;
+  int before = 0, left = s.nseq;
+  while (left > 0) {
+    const int share = (left + kThreads - 1) / kThreads, end = before + left;
+    const int i = before + ((int)threadIdx.x + 1) * share - 1;
+    before += share * __syncthreads_count(i < end && s.at(i) / s.run + i <= item);
+    left = share - 1 < end - before ? share - 1 : end - before;
   }
   Run out{before - 1, 0, 0, 0, 0, 0, 0};
   if (out.seq < 0) return out;
@@ -882,7 +885,9 @@ int launch_walks(const Walks& w, const Walks& states, const Seqs& sq, const floa
                        block, 0, st, states, sq, ld, H);
     if (longest > (int64_t)kFold * sq.run) {
       const unsigned parts = (unsigned)(K * V / 4 / kThreads * H * NW);
-      hipLaunchKernelGGL(run_starts_kernel, dim3(parts, (unsigned)(s.nseq < 8 ? s.nseq : 8)),
+      // (workgroups pass sequences of few runs by; of many, most must be)
+      const int64_t most = s.nseq < 512 ? 8 : s.nseq < 65536 ? s.nseq / 64 : 1024;
+      hipLaunchKernelGGL(run_starts_kernel, dim3(parts, (unsigned)(s.nseq < most ? s.nseq : most)),
                          block, 0, st, w, sq, ld, H, K * V);
     }
   }

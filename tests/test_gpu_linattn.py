@@ -412,6 +412,45 @@ def test_many_sequences_and_heads(ssd):
     check(backward(ssd, d), ref, "bf16")
 
 
+@pytest.mark.parametrize("nseq", [256, 257, 70000])
+def test_one_long_sequence_among_many_of_one_token(ssd, nseq):
+    """More sequences than a workgroup has threads, and than their square; every
+    third is empty, the others have a token, o = scale (q.k) v and k v^T as their
+    state, but for one of many runs."""
+    at, long, H, K = nseq // 2 // 3 * 3 + 1, 20000, 2, 64
+    lens = torch.tensor([i % 3 and 1 for i in range(nseq)])
+    lens[at] = long
+    cu = torch.zeros(nseq + 1, dtype=torch.int64)
+    cu[1:] = lens.cumsum(0)
+    T, t0 = int(cu[-1]), int(cu[at])
+    g = torch.Generator(device=DEV).manual_seed(nseq)
+    q, k, v = (torch.randn(1, T, H, K, generator=g, device=DEV) for _ in range(3))
+    ld = torch.tensor([-0.01, -0.3], device=DEV)
+    o, final = ssd.linattn(q, k, v, ld, None, cu.to(torch.int32).to(DEV))
+    dq, dk, dv, _ = ssd.linattn_backward(q, k, v, ld, v, None, None, cu.to(torch.int32).to(DEV))
+    alone = [t[:, t0:t0 + long].contiguous() for t in (q, k, v)]
+    lo, lfinal = ssd.linattn(*alone, ld)
+    ldq, ldk, ldv, _ = ssd.linattn_backward(*alone, ld, alone[2])
+    tol = 2 * TOL[torch.float32]          # (two results with an error each)
+    q, k, v = (t[0].double() for t in (q, k, v))
+    qk = K ** -0.5 * (q * k).sum(-1, keepdim=True)
+    vv = K ** -0.5 * (v * v).sum(-1, keepdim=True)
+    for got, one, part in ((o, qk * v, lo), (dq, vv * k, ldq), (dk, vv * q, ldk),
+                           (dv, qk * v, ldv)):
+        one[t0:t0 + long] = part[0].double()
+        err = float((got[0].double() - one).norm() / one.norm())
+        assert err <= tol, err
+        rest = torch.cat([got[0, :t0], got[0, t0 + long:]]).double()
+        one = torch.cat([one[:t0], one[t0 + long:]])
+        assert float((rest - one).norm() / one.norm()) <= tol
+    idx = torch.nonzero(lens == 1)[:, 0].to(DEV)
+    tok = cu.to(DEV)[idx]
+    kv = (k[tok, :, :, None] * v[tok, :, None, :]).float()
+    assert float((final[idx] - kv).norm() / kv.norm()) <= tol
+    assert float((final[at] - lfinal[0]).norm() / lfinal.norm()) <= tol
+    assert not final[(lens == 0).nonzero()[:, 0].to(DEV)].any()
+
+
 def test_bad_offsets_stay_in_range(ssd):
     """Offsets below zero, past the tokens, or descending are taken as the
     nearer end or as empty sequences; sequences that are sound keep their
