@@ -65,9 +65,9 @@ size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims *dims, ssd_dtype d
  * final_state [nseq, H, K, V] fp32 (written; an empty sequence's is its
  * initial state) or NULL.  They may be the same buffer (sequences continued
  * in place).  Sums and states are fp32; for bf16 tensors the state is rounded to
- * bf16 as an operand of q_t^T S.  A value of v that is not finite also reaches
- * the outputs of up to 63 tokens of its sequence and head before it (in the
- * gradients: one of k, q or dout those of dq, dk or dv that it is a part of).
+ * bf16 as an operand of q_t^T S.  A value of v that is not finite
+ * makes its column of o NaN from its token on, and those before it are as they
+ * would be without (and so for k, q and dout in the gradients' walks).
  */
 ssd_status ssd_linattn_fwd(const void *q, const void *k, const void *v,
                            const float *log_decay, const float *init_state,

@@ -66,6 +66,7 @@
 #include "ssd_device.h"
 #include "ssd_host.h"
 
+#include <climits>
 #include <type_traits>
 
 namespace ssd {
@@ -78,6 +79,7 @@ constexpr int kWaves = kThreads / kWave;
 // reads and writes each once and costs a launch (some 10 us at 4 runs of 16 heads
 // and 8 sequences; the walks get 3 us longer).
 constexpr int kFold = 4;
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 constexpr uint32_t kPastRange = 0x7FFF0000u;
 
 // One walk.  Head h of an operand is its head h / share.
@@ -201,7 +203,9 @@ struct Shape2 {
   static constexpr int WBYTES = C * 4;                          // the weights of Z
   static constexpr int XPBYTES =
       ROOMY ? XBYTES + PBYTES : XBYTES > PBYTES ? XBYTES : PBYTES;   // X and the scores
-  static constexpr int BYTES = WBYTES + XBYTES + ZBYTES + XPBYTES + (ROOMY ? 0 : DBYTES);
+  static constexpr int BADBYTES = 16 + ZD * 4;                  // values that are not finite
+  static constexpr int BYTES =
+      WBYTES + XBYTES + ZBYTES + XPBYTES + (ROOMY ? 0 : DBYTES) + BADBYTES;
   static constexpr int STATE_BYTES = XBYTES + ZBYTES + WBYTES;
   static constexpr int YU = C * YD * ES / 16 / kThreads;   // 16-byte units per thread
   static constexpr int ZU = C * ZD * ES / 16 / kThreads;
@@ -303,6 +307,62 @@ __device__ __forceinline__ void store_rows(const Walk& w, const f32x4 (&o)[NB][N
   }
 }
 
+// Values of Z that are not finite.  In the scores' product a value stands beside
+// scores of 0 for the tokens before it, and 0 times it would reach them.  So a
+// thread that brings one takes it out of the tile and notes its token for its
+// column; the outputs of the column are NaN from that token on, and so is M's column at
+// the end.
+template <bool BF16, int U>
+__device__ __forceinline__ bool holds_bad(const u32x4 (&v)[U]) {
+  if constexpr (BF16) {
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i)
+      top = __builtin_elementwise_max(top,
+                                      __builtin_bit_cast(u16x2, v[i / 4][i % 4] & 0x7FFF7FFFu));
+    return top[0] >= 0x7F80 || top[1] >= 0x7F80;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4 * U; ++i) top = max(top, v[i / 4][i % 4] & 0x7FFFFFFFu);
+  return top >= 0x7F800000u;
+}
+// The thread's own values of the tile, whose first token is the walk's p-th.
+template <int ZD, int ZS, int U, typename T>
+__device__ __forceinline__ void take_out_bad(T* zs, int* first, int* bad, int p, int tid) {
+  constexpr int PER = ZD * sizeof(T) / 16, STEP = kThreads / PER, E = 16 / sizeof(T);
+  constexpr T INF = (T)(sizeof(T) == 2 ? 0x7F80u : 0x7F800000u);
+#pragma nounroll
+  for (int u = 0; u < U * E; ++u) {
+    const int i = tid / PER + u / E * STEP, c = tid % PER * E + u % E;
+    if ((zs[i * ZS + c] & INF) == INF) {
+      zs[i * ZS + c] = 0;
+      atomicMin(first + c, p + i);
+      *bad = 1;
+    }
+  }
+}
+template <int YD, int ZD, bool BF16>
+__device__ __forceinline__ void store_bad(const Walk& w, const int* first, int p, int64_t lowest,
+                                          int n, int h, int H, int wave, int lr, int lq) {
+  using S = Shape2<YD, ZD, BF16>;
+  const int64_t oheads = H / w.oshare;
+#pragma nounroll
+  for (int c = 0; c < 4 * S::NZ; ++c) {
+    const int col = S::zcol(wave, c / 4, 4 * lq + c % 4);
+#pragma nounroll
+    for (int i = lr; i < n; i += 16) {
+      if (p + i < first[col]) continue;
+      const int64_t at =
+          ((lowest + (w.down ? n - 1 - i : i)) * oheads + h / w.oshare) * ZD + col;
+      if (!BF16 || w.f32out)
+        ((uint32_t*)w.out)[at] = 0x7FC00000u;
+      else
+        ((uint16_t*)w.out)[at] = 0x7FC0;
+    }
+  }
+}
+
 // lam^C from chunk to chunk: the factor that brings the product of all factors
 // so far nearest to the exact power, so the roundings do not add up.
 struct Factor {
@@ -344,6 +404,8 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   char* xs = zs + S::ZBYTES;
   char* ps = S::ROOMY ? xs + S::XBYTES : xs;
   f32x4* dtab = (f32x4*)(xs + S::XPBYTES);
+  int* bad = (int*)(lds + S::BYTES - S::BADBYTES);   // whether there was one
+  int* first = bad + 4;                              // its token, per column
 
   // Whether M goes on to a state in memory, where fp32 is asked for, or only
   // into outputs of the tensors' type.
@@ -430,6 +492,10 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     }
   }
   Factor lam{power(log_decay, h, C), 0.0f};
+  if (OUT && tid < ZD) {
+    *bad = 0;
+    first[tid] = INT_MAX;
+  }
 
   Tile<YD, C, ES, S::YU> tx, ty;
   Tile<ZD, C, ES, S::ZU> tz;
@@ -455,8 +521,13 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
     if constexpr (OUT) tx.template commit<BF16>(xs, YS, fresh);
     ty.template commit<BF16>(ys, YS, fresh);
     tz.template commit<false>(zs, ZS, fresh);
+    if (OUT && __builtin_expect(holds_bad<BF16>(tz.v), 0)) {
+      using T = std::conditional_t<BF16, uint16_t, uint32_t>;
+      take_out_bad<ZD, ZS, S::ZU, T>((T*)zs, first, bad, p, fresh);
+    }
     if (tid < C) wtab[tid] = tid < n ? w.cz * exp2_hw(l2 * (float)(n - a - tid)) : 0.0f;
     __syncthreads();
+    const bool any_bad = OUT && __builtin_amdgcn_readfirstlane(*bad) != 0;
     if constexpr (!BF16) {
       if (p + C < len) issue(p + C, fresh);
     }
@@ -572,6 +643,8 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           }
         }
         store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave, lr, lq);
+        if (__builtin_expect(any_bad, 0))
+          store_bad<YD, ZD, BF16>(w, first, p, lowest_of(p, n), n, h, H, wave, lr, lq);
         __builtin_amdgcn_sched_barrier(0);   // o's registers are free from here on
       }
       if (p + C < len) issue(p + C, fresh);
@@ -718,12 +791,24 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           }
         }
       }
-      if constexpr (OUT) store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave, lr, lq);
+      if constexpr (OUT) {
+        store_rows<YD, ZD, BF16>(w, o, lowest_of(p, n), n, h, H, wave, lr, lq);
+        if (__builtin_expect(any_bad, 0))
+          store_bad<YD, ZD, BF16>(w, first, p, lowest_of(p, n), n, h, H, wave, lr, lq);
+      }
     }
   }
 
   if constexpr (OUT) {
     if (w.end != nullptr && run.r == run.nruns - 1) {
+      if (len > 0 && *bad != 0) {
+#pragma unroll
+        for (int nz = 0; nz < NZ; ++nz) {
+          if (first[S::zcol(wave, nz, lr)] == INT_MAX) continue;
+#pragma unroll
+          for (int yb = 0; yb < NY; ++yb) m[yb][nz] += __builtin_nanf("");
+        }
+      }
 #pragma unroll
       for (int yb = 0; yb < NY; ++yb) {
 #pragma unroll

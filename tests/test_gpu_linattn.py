@@ -412,6 +412,55 @@ def test_many_sequences_and_heads(ssd):
     check(backward(ssd, d), ref, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at,K,V", [(0, 64, 64), (17, 64, 128), (37, 128, 128), (126, 128, 64),
+                                    (299, 128, 128)])
+def test_a_bad_value_stays_behind_its_token(ssd, dtype, bad, at, K, V):
+    """NaN or infinity at one token: every result that has no part of it is as it
+    would be without, those of its neighbours in a chunk too."""
+    s = make((300,), 4, 2, K, V, dtype, seed=at)
+    ref = reference(s)
+
+    def same(got, cut, heads=slice(None), cols=slice(None)):
+        for n, g in got.items():
+            g, r = g[cut][:, heads, cols].double().cpu(), ref[n][cut][:, heads, cols]
+            if r.numel():
+                err = float((g - r).norm() / r.norm())
+                assert err <= TOL[DTYPES[dtype]], (n, err)
+
+    before, after = slice(0, at), slice(at + 1, 300)
+    for name in ("q", "k", "v", "do"):
+        x = s[name].clone()
+        x[at, 1, 5] = bad
+        d = on_gpu(dict(s, **{name: x}))
+        fwd, grads = forward(ssd, d), backward(ssd, d)
+        o = fwd["o"]
+        if name == "v":             # one column of a head's state from that token on
+            same({"o": o}, before)
+            same({"o": o}, slice(None), slice(2, None))
+            same({"o": o}, slice(None), slice(1, 2), slice(6, None))
+            assert not torch.isfinite(o[at:, 1, 5]).any()
+            final = fwd["final"][0].double().cpu()
+            assert not torch.isfinite(final[1, :, 5]).any()
+            final[1, :, 5] = ref["final"][0, 1, :, 5]
+            err = float((final - ref["final"][0]).norm() / ref["final"].norm())
+            assert err <= STATE_TOL[DTYPES[dtype]], err
+            same({"dq": grads["dq"]}, before)
+            same({"dk": grads["dk"]}, after)
+        if name == "k":
+            same({"o": o, "dq": grads["dq"]}, before)
+            same({"dv": grads["dv"]}, after)
+        if name == "q":
+            same({"o": o}, before)
+            same({"o": o}, after)
+            same({"dk": grads["dk"], "dv": grads["dv"]}, after)
+        if name == "do":
+            same({"dk": grads["dk"], "dv": grads["dv"]}, after)
+            same({"dq": grads["dq"]}, before)
+            same({"dv": grads["dv"]}, slice(None), slice(1, 2), slice(6, None))
+
+
 @pytest.mark.parametrize("nseq", [256, 257, 70000])
 def test_one_long_sequence_among_many_of_one_token(ssd, nseq):
     """More sequences than a workgroup has threads, and than their square; every
