@@ -56,10 +56,10 @@
 // factor would otherwise grow with the number of chunks.
 //
 // Measured on MI355X (bf16; a device copy moves 5.1 TB/s).  8 x 2048 tokens, 16
-// heads of 128 x 128: run_states 36 us, walks 75 us (300 MB: 4.0 TB/s).  Gradients
-// of 16384 tokens, 32 heads of 128 x 128: run_states 187 us, the three walks 460 us
-// (1.5 GB: 3.2 TB/s; matrix pipe 24% busy, vector unit 30%, LDS 31%).  65536
-// tokens, 32 heads of 128 x 64 on one group: run_states 146 us, walks 325 us;
+// heads of 128 x 128: run_states 35 us, walks 77 us (300 MB: 3.9 TB/s).  Gradients
+// of 16384 tokens, 32 heads of 128 x 128: run_states 177 us, the three walks 445 us
+// (1.5 GB: 3.4 TB/s; matrix pipe 24% busy, vector unit 30%, LDS 31%).  65536
+// tokens, 32 heads of 128 x 64 on one group: run_states 152 us, walks 332 us;
 // there q and k come from the caches and the LDS (54% busy), the vector unit (39%)
 // and the matrix pipe (24%) bound it together.
 #include "ssd_block_launch.h"
@@ -311,7 +311,8 @@ __device__ __forceinline__ void store_rows(const Walk& w, const f32x4 (&o)[NB][N
 // scores of 0 for the tokens before it, and 0 times it would reach them.  So a
 // thread that brings one takes it out of the tile and notes its token for its
 // column; the outputs of the column are NaN from that token on, and so is M's column at
-// the end.
+// the end.  (Looking for them costs 1 to 2% of a walk; done on the operand as a wave
+// reads it, whose registers it lengthens, up to 10%.)
 template <bool BF16, int U>
 __device__ __forceinline__ bool holds_bad(const u32x4 (&v)[U]) {
   if constexpr (BF16) {
