@@ -64,8 +64,9 @@ size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims *dims, ssd_dtype d
  * Whole sequences.  init_state [nseq, H, K, V] fp32 or NULL (zeros);
  * final_state [nseq, H, K, V] fp32 (written; an empty sequence's is its
  * initial state) or NULL.  They may be the same buffer (sequences continued
- * in place).  Sums and states are fp32; for bf16 tensors the state is rounded to
- * bf16 as an operand of q_t^T S.  A value of v that is not finite
+ * in place).  Sums and states are fp32; for bf16 tensors the
+ * states, scores and decayed values enter products as two bf16 terms, which leave at
+ * most 2^-16 of each.  A value of v that is not finite
  * makes its column of o NaN from its token on, and those before it are as they
  * would be without (and so for k, q and dout in the gradients' walks).
  */

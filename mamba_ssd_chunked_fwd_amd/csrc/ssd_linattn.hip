@@ -33,11 +33,12 @@
 //     again, to every wave; Z comes from the LDS transpose read;
 //   - the output comes out transposed too, one token and 8 (fp32, or 64 columns: 4)
 //     consecutive columns per lane: 16- or 8-byte stores.
-// bf16 tensors: 16x16x32 bf16 products, chunks of 64.  M is rounded to bf16 as the
-// operand of X^T M: that part of the output gets an error as large as the
-// output's own rounding.  The scores are split into two bf16 terms, and so is the
-// decayed Z in M's update (three where M goes on to an fp32 state in memory: the
-// product is then as exact as an fp32 one).  fp32 tensors: 16x16x4 fp32
+// bf16 tensors: 16x16x32 bf16 products, chunks of 64.  Every operand that is not a
+// tensor itself is split into two bf16 terms, which leave 2^-16 of it at most: the
+// scores, M in X^T M (one term would leave 2^-8 |X|^T |M|, which is not small beside
+// an output whose products cancel: keys of one mean and queries that sum to zero gave
+// outputs off by a tenth) and the decayed Z in M's update (three where M goes on to
+// an fp32 state in memory: the product is then as exact as an fp32 one).  fp32 tensors: 16x16x4 fp32
 // products, chunks of 32 (the scores' share grows with the chunk, and these
 // calls are bound by the matrix pipe).
 //
@@ -590,22 +591,23 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
           }
         };
         if constexpr (S::ROOMY) write_scores();
-        // (2) X^T M, transposed, for all tokens
+        // (2) X^T M, transposed, for all tokens; M as two bf16 terms
 #pragma unroll
         for (int kk = 0; kk < NY / 2; ++kk) {
-          u32x4 mb[NZ], xf[NB];
-#pragma unroll
-          for (int nz = 0; nz < NZ; ++nz) {
-            const f32x4 m0 = m[2 * kk][nz], m1 = m[2 * kk + 1][nz];
-            mb[nz] = (u32x4){pack_bf16(m0[0], m0[1]), pack_bf16(m0[2], m0[3]),
-                             pack_bf16(m1[0], m1[1]), pack_bf16(m1[2], m1[3])};
-          }
+          u32x4 xf[NB];
 #pragma unroll
           for (int tb = 0; tb < NB; ++tb) xf[tb] = row_frag(xl, YS, 16 * tb + lr, kk);
 #pragma unroll
-          for (int tb = 0; tb < NB; ++tb) {
+          for (int nz = 0; nz < NZ; ++nz) {
+            u32x2 h0, l0, h1, l1;
+            split4(m[2 * kk][nz], h0, l0);
+            split4(m[2 * kk + 1][nz], h1, l1);
+            const u32x4 mt[2] = {join(h0, h1), join(l0, l1)};
 #pragma unroll
-            for (int nz = 0; nz < NZ; ++nz) o[tb][nz] = mfma_bf16(mb[nz], xf[tb], o[tb][nz]);
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int tb = 0; tb < NB; ++tb) o[tb][nz] = mfma_bf16(mt[e], xf[tb], o[tb][nz]);
+            }
           }
         }
 #pragma unroll
