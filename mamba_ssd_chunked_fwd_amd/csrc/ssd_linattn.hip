@@ -197,8 +197,9 @@ struct Shape2 {
   static constexpr int PBYTES = (BF16 ? 2 : 1) * C * PS * ES;   // the scores, bf16 as two terms
   // A 128 x 128 M leaves registers for two workgroups of a CU only, whose LDS has
   // room for the scores beside X (a barrier less per chunk) and whose registers
-  // have some left for the decays: 1 to 2% of such a walk.  The others keep three
-  // workgroups by letting the scores take X's place and the decays wait in LDS.
+  // have some left for the decays: 1 to 2% of such a walk.  The others have room for three
+  // (resident() says which take them) by letting the scores take X's place and the
+  // decays wait in LDS.
   static constexpr bool ROOMY = YD == 128 && ZD == 128;
   static constexpr int DBYTES = 3 * kWave * 16;                 // decays, four per lane
   static constexpr int WBYTES = C * 4;                          // the weights of Z
@@ -842,17 +843,24 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
   }
 }
 
-// Workgroups of a CU: what the registers of M leave room for (a workgroup has one
-// wave on each SIMD), and the LDS.
-template <int K, int V>
-constexpr int resident() { return K == 128 && V == 128 ? 2 : 3; }
+// Workgroups of a CU: what the registers leave room for (a workgroup has one wave on
+// each SIMD), and the LDS.  Two for a 128 x 128 M, and for outputs of bf16 tensors by a
+// 64 x 128 one, whose two column blocks for each wave spill with three (two against three,
+// 8 x 2048 tokens, 16 heads: 84 and 110 us; 9000, 5461 and 1923 tokens: 89 and 114).  The
+// gradients of 64 x 128 and 128 x 64 states, which have such a walk too, spill some 25
+// with three and keep them all the same: runs of whole chunks fill two places less evenly (24 heads
+// on 8 groups, 4 x 2048 tokens 284 and 300 us, but seven documents of 41 to 5000 tokens 424
+// and 347).  fp32 tensors and an M of 64 columns do not spill with three (128 x 64, 65536
+// tokens, 32 heads: 484 and 439 us).
+template <int K, int V, bool BF16, int NW>
+constexpr int resident() { return V == 128 && (K == 128 || (BF16 && NW == 1)) ? 2 : 3; }
 
 // Workgroup (item, walk, head), the head fastest.  Blocks are dealt to the 8 XCDs
 // in turn, so with H a multiple of 8 every XCD gets the walks of H/8 consecutive
 // heads, which share operands.  Items without a run (up to nseq of them) come
 // last: in between they would leave CUs with one workgroup and others with three.
 template <int K, int V, bool BF16, int NW, bool OUT>
-__global__ __launch_bounds__(kThreads, (resident<K, V>())) void walk_kernel(Walks ws, Seqs sq,
+__global__ __launch_bounds__(kThreads, (resident<K, V, BF16, NW>())) void walk_kernel(Walks ws, Seqs sq,
                                                         const float* __restrict__ log_decay,
                                                         int H) {
   using SA = Shape2<K, V, BF16>;
@@ -944,8 +952,8 @@ constexpr int64_t kMinChunks = 2;
 
 int run_tokens(const LinattnShape& s, bool bf16, int walks) {
   const int64_t C = bf16 ? 64 : 32;
-  const int64_t wgs =
-      kCus * (s.dk == 128 && s.dv == 128 ? resident<128, 128>() : resident<64, 64>());
+  const bool two = s.dv == 128 && (s.dk == 128 || (bf16 && walks == 1));
+  const int64_t wgs = kCus * (two ? resident<128, 128, true, 1>() : resident<64, 64, true, 1>());
   const int64_t each = 3 * wgs / (s.nheads * walks);           // thirds of runs for a head
   const int64_t ends = 2 * s.nseq < each / 2 ? 2 * s.nseq : each / 2;
   int64_t chunks = each > ends ? (3 * s.tokens + (each - ends) * C - 1) / ((each - ends) * C)
