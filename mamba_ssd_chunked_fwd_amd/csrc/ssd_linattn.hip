@@ -610,6 +610,9 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
               for (int tb = 0; tb < NB; ++tb) o[tb][nz] = mfma_bf16(mt[e], xf[tb], o[tb][nz]);
             }
           }
+          // (one slice of M at a time: its terms formed ahead would be spilled by the
+          // gradients of 64 x 128 and 128 x 64 states, 2 to 7% of them)
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int tb = 0; tb < NB; ++tb) {
