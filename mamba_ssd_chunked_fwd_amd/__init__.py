@@ -841,12 +841,25 @@ def _scratch(n: int, dev: torch.device):
     return t, (t.data_ptr(), n)
 
 
+def _no_graph(where: str, **tensors) -> None:
+    """Refuse tensors whose gradient a call would lose: the outputs carry no graph."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{where} records no graph, and {name} requires a gradient: call "
+                                 f"it under torch.no_grad() and take gradients from "
+                                 f"{where}_backward")
+
+
 def linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
             init_state: Optional[torch.Tensor] = None,
             cu_seqlens: Optional[torch.Tensor] = None,
             scale: Optional[float] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Allocate and run ``ssd_linattn_fwd``: (o, final_state).  Rows of o outside
-    every packed sequence are not written."""
+    every packed sequence are not written.  No graph is recorded (gradients come
+    from ``linattn_backward``): tensors that require one are refused outside
+    torch.no_grad()."""
+    _no_graph("linattn", q=q, k=k, v=v, log_decay=log_decay, init_state=init_state)
     d, ins = _linattn_args(q, k, v, log_decay, init_state, cu_seqlens)
     o = torch.empty_like(v)
     final = torch.empty((d.nseq, d.nheads, d.dk, d.dv), dtype=torch.float32, device=q.device)
@@ -875,7 +888,10 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
              res_scale: Optional[torch.Tensor] = None,
              weight: Optional[torch.Tensor] = None,
              eps: float = 1e-5) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Allocate and run ``ssd_add_norm_fwd``: (y, residual_out)."""
+    """Allocate and run ``ssd_add_norm_fwd``: (y, residual_out).  No graph is recorded
+    (gradients come from ``add_norm_backward``): tensors that require one are
+    refused outside torch.no_grad()."""
+    _no_graph("add_norm", x=x, residual=residual, res_scale=res_scale, weight=weight)
     y = torch.empty_like(x)
     out = torch.empty_like(x if residual is None else residual)
     ssd_add_norm_fwd(x, residual, res_scale, weight, y, out, eps)
@@ -903,7 +919,9 @@ def gated_norm(x: torch.Tensor, z: Optional[torch.Tensor] = None,
                group: Optional[int] = None, gate: str = "silu",
                gate_first: bool = False) -> torch.Tensor:
     """Allocate and run ``ssd_gated_norm_fwd``: y, in z's type (x's without a
-    gate)."""
+    gate).  No graph is recorded (gradients come from ``gated_norm_backward``):
+    tensors that require one are refused outside torch.no_grad()."""
+    _no_graph("gated_norm", x=x, z=z, weight=weight)
     y = torch.empty_like(x if z is None else z)
     ssd_gated_norm_fwd(x, z, weight, y, eps, group, gate, gate_first)
     return y
