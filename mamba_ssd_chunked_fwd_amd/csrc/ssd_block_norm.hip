@@ -11,7 +11,7 @@
 // nothing is kept from the forward call.
 //
 // MI355X design.  Each call reads its inputs once and writes its outputs
-// once: HBM-bound.  A team of TS lanes owns a segment: NV vectors of eight
+// once: HBM-bound (gradients: up to 8192 channels, see below).  A team of TS lanes owns a segment: NV vectors of eight
 // elements per lane stay in registers between the sums and the outputs (where the
 // segment length is no multiple of 8 the vectors start at any element, and the
 // last one overlaps the one before).  The sums of a team
@@ -26,6 +26,12 @@
 // 8 us for the row sums; gated norm of 16384 x 5120 by 64 channels 96 us (5.2);
 // its gradients at 8192 x 1536 by rows, fp32 and bf16 mixed, 31 us (176 MB: 5.7) and
 // 5 us for the row sums.
+// Gradients of segments of more than 8192 channels are not HBM-bound: up to 16 waves of
+// two vectors per lane leave 128 registers for eight (add norm) or seven (gated) arrays of
+// 16 values, and 110 to 230 bytes per lane of them go through scratch for every row.  4096
+// rows of bf16, with the row sums: add norm 8192 channels 96 us (4.2 TB/s of what it
+// must move), 12287 398 (1.5), 12288 373 (1.6), 16384 355 (2.3); gated by whole rows 80
+// (4.2), 282 (1.8), 263 (1.9) and 252 (2.7).
 #include "ssd_block_launch.h"
 #include "ssd_device.h"
 #include "ssd_host.h"
@@ -42,14 +48,18 @@ constexpr int kVec = 8;                // elements of a lane's vector
 constexpr int kNormWaves = 4096;
 
 // The eight elements at element offset `i`, as floats, and back (rounded once).
-// RAGGED: the segment length is no multiple of 8, so a vector may start at any
-// element, and a segment may have fewer than eight (zeros stand for the rest).
+// ENDS: kWhole: the segment length is a multiple of 8, and so is every offset;
+// kRagged: it is not, so a vector may start at any element; kShort: a segment may also
+// have fewer than eight (zeros stand for the rest).  That form goes to the smallest
+// teams alone: its branches for each element cost the widest ones, which have the
+// fewest registers to spare, up to 1650 bytes of scratch per lane.
+constexpr int kWhole = 0, kRagged = 1, kShort = 2;
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
-template <bool BF16, bool RAGGED>
+template <bool BF16, int ENDS>
 __device__ __forceinline__ void load_n(const void* p, int64_t i, int left, float* v) {
-  if (RAGGED && left < kVec) {
+  if (ENDS == kShort && left < kVec) {
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       v[e] = 0.0f;
@@ -59,7 +69,7 @@ __device__ __forceinline__ void load_n(const void* p, int64_t i, int left, float
     }
   } else if constexpr (BF16) {
     const uint16_t* q = (const uint16_t*)p + i;
-    const u32x4 u = RAGGED ? (u32x4) * (const u32x4_any*)q : *(const u32x4*)q;
+    const u32x4 u = ENDS ? (u32x4) * (const u32x4_any*)q : *(const u32x4*)q;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[2 * k] = bf16_lo(u[k]);
@@ -67,8 +77,8 @@ __device__ __forceinline__ void load_n(const void* p, int64_t i, int left, float
     }
   } else {
     const float* q = (const float*)p + i;
-    const f32x4 a = RAGGED ? (f32x4) * (const f32x4_any*)q : *(const f32x4*)q;
-    const f32x4 b = RAGGED ? (f32x4) * (const f32x4_any*)(q + 4) : *(const f32x4*)(q + 4);
+    const f32x4 a = ENDS ? (f32x4) * (const f32x4_any*)q : *(const f32x4*)q;
+    const f32x4 b = ENDS ? (f32x4) * (const f32x4_any*)(q + 4) : *(const f32x4*)(q + 4);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[k] = a[k];
@@ -76,9 +86,9 @@ __device__ __forceinline__ void load_n(const void* p, int64_t i, int left, float
     }
   }
 }
-template <bool BF16, bool RAGGED>
+template <bool BF16, int ENDS>
 __device__ __forceinline__ void store_n(void* p, int64_t i, int left, const float* v) {
-  if (RAGGED && left < kVec) {
+  if (ENDS == kShort && left < kVec) {
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       if (e < left) {
@@ -92,14 +102,14 @@ __device__ __forceinline__ void store_n(void* p, int64_t i, int left, const floa
     const u32x4 u = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                      pack_bf16(v[6], v[7])};
     uint16_t* q = (uint16_t*)p + i;
-    if constexpr (RAGGED)
+    if constexpr (ENDS != kWhole)
       *(u32x4_any*)q = u;
     else
       *(u32x4*)q = u;
   } else {
     const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
     float* q = (float*)p + i;
-    if constexpr (RAGGED) {
+    if constexpr (ENDS != kWhole) {
       *(f32x4_any*)q = a;
       *(f32x4_any*)(q + 4) = b;
     } else {
@@ -172,40 +182,40 @@ struct Team {
   }
 };
 
-// A lane's vector of a segment of n elements.  In a RAGGED segment the last vector
+// A lane's vector of a segment of n elements.  In a ragged segment the last vector
 // ends with the segment and shares its first `skip` elements with the one before:
 // both lanes form and store the same values there, and only one adds them to the
 // segment's sums.  (A segment of less than eight elements is one short vector.)
-template <bool RAGGED>
+template <int ENDS>
 struct Span {
   int c, skip;
   bool on;
   __device__ __forceinline__ Span(int vec, int n) : c(vec * kVec), skip(0), on(vec * kVec < n) {
-    if (RAGGED && n >= kVec && c + kVec > n) {
+    if (ENDS != kWhole && n >= kVec && c + kVec > n) {
       skip = c - (n - kVec);
       c = n - kVec;
     }
   }
-  __device__ __forceinline__ bool counts(int e) const { return !RAGGED || e >= skip; }
+  __device__ __forceinline__ bool counts(int e) const { return ENDS == kWhole || e >= skip; }
 };
 
-template <int NV, bool RAGGED, int TS>
+template <int NV, int ENDS, int TS>
 __device__ __forceinline__ void load_weights(const float* p, const NormGrid& g, const Team<TS>& t,
                                              bool shared, float other, float* w) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+    const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
     const int c = sp.c;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) w[j * kVec + e] = other;
     if (p != nullptr && t.on && sp.on)
-      load_n<false, RAGGED>(p, (shared ? 0 : (int64_t)t.group * g.n) + c, g.n - c, w + j * kVec);
+      load_n<false, ENDS>(p, (shared ? 0 : (int64_t)t.group * g.n) + c, g.n - c, w + j * kVec);
   }
 }
 
 // One row of partial sums of this workgroup: over its teams of one group, or
 // of every group where the weights are shared.
-template <int TS, int NV, bool RAGGED>
+template <int TS, int NV, int ENDS>
 __device__ __forceinline__ void store_partial(const float* acc, float* part, const NormGrid& g,
                                               const Team<TS>& t, float* buf) {
   constexpr int kTeams = Team<TS>::kTeams;
@@ -233,14 +243,14 @@ __device__ __forceinline__ void store_partial(const float* acc, float* part, con
         }
       }
     }
-    const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
-      const int c = sp.c;
-    if (writes && sp.on) store_n<false, RAGGED>(row, c, g.n - c, v);
+    const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
+    const int c = sp.c;
+    if (writes && sp.on) store_n<false, ENDS>(row, c, g.n - c, v);
   }
 }
 
 // ---------------------------------------------------------------- add norm
-template <int TS, int NV, bool RAGGED, bool XB, bool RB>
+template <int TS, int NV, int ENDS, bool XB, bool RB>
 __global__ __launch_bounds__(max_threads<TS>()) void add_norm_fwd_kernel(
     const void* x, const void* res, const float* __restrict__ scale,
     const float* __restrict__ weight, void* y, void* res_out, NormGrid g) {
@@ -248,19 +258,19 @@ __global__ __launch_bounds__(max_threads<TS>()) void add_norm_fwd_kernel(
   int turn = 0;
   Team<TS> t(g);
   float w[NV * kVec], s[NV * kVec];
-  load_weights<NV, RAGGED, TS>(weight, g, t, false, 1.0f, w);
-  load_weights<NV, RAGGED, TS>(scale, g, t, false, 1.0f, s);
+  load_weights<NV, ENDS, TS>(weight, g, t, false, 1.0f, w);
+  load_weights<NV, ENDS, TS>(scale, g, t, false, 1.0f, s);
   for (int64_t row = t.row; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim;
     float h[NV * kVec], sum[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float xv[kVec] = {}, rv[kVec] = {};
       if (sp.on) {
-        load_n<XB, RAGGED>(x, base + c, g.n - c, xv);
-        if (res) load_n<RB, RAGGED>(res, base + c, g.n - c, rv);
+        load_n<XB, ENDS>(x, base + c, g.n - c, xv);
+        if (res) load_n<RB, ENDS>(res, base + c, g.n - c, rv);
       }
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
@@ -272,20 +282,20 @@ __global__ __launch_bounds__(max_threads<TS>()) void add_norm_fwd_kernel(
     const float r = rsqrtf(__builtin_fmaf(sum[0], g.inv_n, g.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       if (sp.on) {
         float v[kVec];
-        if (res_out) store_n<RB, RAGGED>(res_out, base + c, g.n - c, h + j * kVec);
+        if (res_out) store_n<RB, ENDS>(res_out, base + c, g.n - c, h + j * kVec);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) v[e] = h[j * kVec + e] * r * w[j * kVec + e];
-        store_n<XB, RAGGED>(y, base + c, g.n - c, v);
+        store_n<XB, ENDS>(y, base + c, g.n - c, v);
       }
     }
   }
 }
 
-template <int TS, int NV, bool RAGGED, bool XB, bool RB>
+template <int TS, int NV, int ENDS, bool XB, bool RB>
 __global__ __launch_bounds__(max_threads<TS>()) void add_norm_bwd_kernel(
     const void* x, const void* res, const float* __restrict__ scale,
     const float* __restrict__ weight, const void* dy, const void* dres_out, void* dx, void* dres,
@@ -295,23 +305,23 @@ __global__ __launch_bounds__(max_threads<TS>()) void add_norm_bwd_kernel(
   int turn = 0;
   Team<TS> t(g);
   float w[NV * kVec], s[NV * kVec], dw[NV * kVec] = {}, ds[NV * kVec] = {};
-  load_weights<NV, RAGGED, TS>(weight, g, t, false, 1.0f, w);
-  load_weights<NV, RAGGED, TS>(scale, g, t, false, 1.0f, s);
+  load_weights<NV, ENDS, TS>(weight, g, t, false, 1.0f, w);
+  load_weights<NV, ENDS, TS>(scale, g, t, false, 1.0f, s);
   for (int64_t row = t.row; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim;
     float h[NV * kVec], xs[NV * kVec], dv[NV * kVec], gv[NV * kVec], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float rv[kVec] = {};
 #pragma unroll
       for (int e = 0; e < kVec; ++e) xs[j * kVec + e] = dv[j * kVec + e] = gv[j * kVec + e] = 0.0f;
       if (sp.on) {
-        load_n<XB, RAGGED>(x, base + c, g.n - c, xs + j * kVec);
-        load_n<XB, RAGGED>(dy, base + c, g.n - c, dv + j * kVec);
-        if (res) load_n<RB, RAGGED>(res, base + c, g.n - c, rv);
-        if (dres_out) load_n<RB, RAGGED>(dres_out, base + c, g.n - c, gv + j * kVec);
+        load_n<XB, ENDS>(x, base + c, g.n - c, xs + j * kVec);
+        load_n<XB, ENDS>(dy, base + c, g.n - c, dv + j * kVec);
+        if (res) load_n<RB, ENDS>(res, base + c, g.n - c, rv);
+        if (dres_out) load_n<RB, ENDS>(dres_out, base + c, g.n - c, gv + j * kVec);
       }
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
@@ -328,7 +338,7 @@ __global__ __launch_bounds__(max_threads<TS>()) void add_norm_bwd_kernel(
     const float m = sum[1] * g.inv_n * r;              // mean(w dy n)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float dxv[kVec];
 #pragma unroll
@@ -341,13 +351,13 @@ __global__ __launch_bounds__(max_threads<TS>()) void add_norm_bwd_kernel(
         ds[i] = __builtin_fmaf(gv[i], xs[i], ds[i]);
       }
       if (sp.on) {
-        if (dres) store_n<RB, RAGGED>(dres, base + c, g.n - c, gv + j * kVec);
-        store_n<XB, RAGGED>(dx, base + c, g.n - c, dxv);
+        if (dres) store_n<RB, ENDS>(dres, base + c, g.n - c, gv + j * kVec);
+        store_n<XB, ENDS>(dx, base + c, g.n - c, dxv);
       }
     }
   }
-  if (dweight) store_partial<TS, NV, RAGGED>(dw, dweight, g, t, buf);
-  if (dscale) store_partial<TS, NV, RAGGED>(ds, dscale, g, t, buf);
+  if (dweight) store_partial<TS, NV, ENDS>(dw, dweight, g, t, buf);
+  if (dscale) store_partial<TS, NV, ENDS>(ds, dscale, g, t, buf);
 }
 
 // -------------------------------------------------------------- gated norm
@@ -362,27 +372,32 @@ __device__ __forceinline__ float gate_act(float z, bool silu, float& d) {
   return silu ? z * sig : sig;
 }
 
-template <int TS, int NV, bool RAGGED, bool XB, bool ZB>
-__global__ __launch_bounds__(max_threads<TS>()) void gated_norm_fwd_kernel(
+// Waves per SIMD asked for: with five, rows of up to 12288 channels, 12 waves to a row, have
+// one workgroup to a CU in place of two (12287 channels of bf16: 96 us in place of 81).
+template <int TS, int NV>
+constexpr int gate_waves() { return TS == kBlockTeam && NV == 2 ? 6 : 1; }
+
+template <int TS, int NV, int ENDS, bool XB, bool ZB>
+__global__ __launch_bounds__(max_threads<TS>(), (gate_waves<TS, NV>())) void gated_norm_fwd_kernel(
     const void* x, const void* z, const float* __restrict__ weight, void* y, bool silu,
     bool first, NormGrid g) {
   __shared__ float red[2][kMaxWaves][2];
   int turn = 0;
   Team<TS> t(g);
   float w[NV * kVec];
-  load_weights<NV, RAGGED, TS>(weight, g, t, g.shared, 1.0f, w);
+  load_weights<NV, ENDS, TS>(weight, g, t, g.shared, 1.0f, w);
   if (!t.on) return;            // whole teams; one of a workgroup is always on
   for (int64_t row = t.row; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim + (int64_t)t.group * g.n;
     float u[NV * kVec], a[NV * kVec], sum[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float xv[kVec] = {}, zv[kVec] = {}, d;
       if (sp.on) {
-        load_n<XB, RAGGED>(x, base + c, g.n - c, xv);
-        if (z) load_n<ZB, RAGGED>(z, base + c, g.n - c, zv);
+        load_n<XB, ENDS>(x, base + c, g.n - c, xv);
+        if (z) load_n<ZB, ENDS>(z, base + c, g.n - c, zv);
       }
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
@@ -397,20 +412,20 @@ __global__ __launch_bounds__(max_threads<TS>()) void gated_norm_fwd_kernel(
     const float r = rsqrtf(__builtin_fmaf(sum[0], g.inv_n, g.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       if (sp.on) {
         float v[kVec];
 #pragma unroll
         for (int e = 0; e < kVec; ++e)
           v[e] = u[j * kVec + e] * r * w[j * kVec + e] * a[j * kVec + e];
-        store_n<ZB, RAGGED>(y, base + c, g.n - c, v);
+        store_n<ZB, ENDS>(y, base + c, g.n - c, v);
       }
     }
   }
 }
 
-template <int TS, int NV, bool RAGGED, bool XB, bool ZB>
+template <int TS, int NV, int ENDS, bool XB, bool ZB>
 __global__ __launch_bounds__(max_threads<TS>()) void gated_norm_bwd_kernel(
     const void* x, const void* z, const float* __restrict__ weight, const void* dy, void* dx,
     void* dz, float* __restrict__ dweight, bool silu, bool first, NormGrid g) {
@@ -419,21 +434,21 @@ __global__ __launch_bounds__(max_threads<TS>()) void gated_norm_bwd_kernel(
   int turn = 0;
   Team<TS> t(g);
   float w[NV * kVec], dw[NV * kVec] = {};
-  load_weights<NV, RAGGED, TS>(weight, g, t, g.shared, 1.0f, w);
+  load_weights<NV, ENDS, TS>(weight, g, t, g.shared, 1.0f, w);
   for (int64_t row = t.on ? t.row : g.rows; row < g.rows; row += t.step) {
     const int64_t base = row * g.dim + (int64_t)t.group * g.n;
     float xs[NV * kVec], act[NV * kVec], der[NV * kVec], dv[NV * kVec], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float zv[kVec] = {};
 #pragma unroll
       for (int e = 0; e < kVec; ++e) xs[j * kVec + e] = dv[j * kVec + e] = 0.0f;
       if (sp.on) {
-        load_n<XB, RAGGED>(x, base + c, g.n - c, xs + j * kVec);
-        load_n<ZB, RAGGED>(dy, base + c, g.n - c, dv + j * kVec);
-        if (z) load_n<ZB, RAGGED>(z, base + c, g.n - c, zv);
+        load_n<XB, ENDS>(x, base + c, g.n - c, xs + j * kVec);
+        load_n<ZB, ENDS>(dy, base + c, g.n - c, dv + j * kVec);
+        if (z) load_n<ZB, ENDS>(z, base + c, g.n - c, zv);
       }
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
@@ -453,7 +468,7 @@ __global__ __launch_bounds__(max_threads<TS>()) void gated_norm_bwd_kernel(
     const float m = sum[1] * g.inv_n * r;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Span<RAGGED> sp(t.lane + team_lanes<TS>() * j, g.n);
+      const Span<ENDS> sp(t.lane + team_lanes<TS>() * j, g.n);
       const int c = sp.c;
       float dxv[kVec], dzv[kVec];
 #pragma unroll
@@ -467,12 +482,12 @@ __global__ __launch_bounds__(max_threads<TS>()) void gated_norm_bwd_kernel(
         dw[i] = __builtin_fmaf(dn, n, dw[i]);
       }
       if (sp.on) {
-        store_n<XB, RAGGED>(dx, base + c, g.n - c, dxv);
-        if (z) store_n<ZB, RAGGED>(dz, base + c, g.n - c, dzv);
+        store_n<XB, ENDS>(dx, base + c, g.n - c, dxv);
+        if (z) store_n<ZB, ENDS>(dz, base + c, g.n - c, dzv);
       }
     }
   }
-  if (dweight) store_partial<TS, NV, RAGGED>(dw, dweight, g, t, buf);
+  if (dweight) store_partial<TS, NV, ENDS>(dw, dweight, g, t, buf);
 }
 
 // Adds `parts` rows of `cols` partial sums in a fixed order: 16 slices of the
@@ -554,7 +569,7 @@ NormLaunch norm_launch(const NormShape& s, float eps) {
   return l;
 }
 
-// f(TeamPlan constants, ragged) for the plan of a segment of n channels.
+// f(TeamPlan constants, ends) for the plan of a segment of n channels.
 template <class F>
 void with_plan(int64_t n, F f) {
   const TeamPlan p = team_plan(n);
@@ -562,9 +577,9 @@ void with_plan(int64_t n, F f) {
   if (p.ts == TS && p.nv == NV) {                                                      \
     if (n % kVec)                                                                      \
       return f(std::integral_constant<int, TS>{}, std::integral_constant<int, NV>{},   \
-               std::true_type{});                                                      \
+               std::integral_constant<int, TS == 8 ? kShort : kRagged>{});             \
     return f(std::integral_constant<int, TS>{}, std::integral_constant<int, NV>{},     \
-             std::false_type{});                                                       \
+             std::integral_constant<int, kWhole>{});                                   \
   }
   SSD_NORM_PLAN(8, 1)
   SSD_NORM_PLAN(16, 1)
@@ -610,10 +625,10 @@ int launch_add_norm_fwd(const void* x, const void* res, const float* scale, cons
                         const NormShape& s, void* stream) {
   clear_launch_error();
   const NormLaunch l = norm_launch(s, eps);
-  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
+  with_plan(s.group, [&](auto ts, auto nv, auto ends) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
-        hipLaunchKernelGGL((add_norm_fwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
+        hipLaunchKernelGGL((add_norm_fwd_kernel<ts(), nv(), ends(), xb(), rb()>), l.grid,
                            dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale,
                            weight, y, res_out, l.g);
       });
@@ -630,10 +645,10 @@ int launch_add_norm_bwd(const void* x, const void* res, const float* scale, cons
   const NormLaunch l = norm_launch(s, eps);
   float* pw = dweight ? (float*)ws : nullptr;
   float* ps = dscale ? (float*)((char*)ws + norm_bwd_workspace(s, 1)) : nullptr;
-  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
+  with_plan(s.group, [&](auto ts, auto nv, auto ends) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(rbf16, [&](auto rb) {
-        hipLaunchKernelGGL((add_norm_bwd_kernel<ts(), nv(), rag(), xb(), rb()>), l.grid,
+        hipLaunchKernelGGL((add_norm_bwd_kernel<ts(), nv(), ends(), xb(), rb()>), l.grid,
                            dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, res, scale,
                            weight, dy, dres_out, dx, dres, ps, pw, l.g);
       });
@@ -648,10 +663,10 @@ int launch_gated_norm_fwd(const void* x, const void* z, const float* weight, voi
                           void* stream) {
   clear_launch_error();
   const NormLaunch l = norm_launch(s, eps);
-  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
+  with_plan(s.group, [&](auto ts, auto nv, auto ends) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(zbf16, [&](auto zb) {
-        hipLaunchKernelGGL((gated_norm_fwd_kernel<ts(), nv(), rag(), xb(), zb()>), l.grid,
+        hipLaunchKernelGGL((gated_norm_fwd_kernel<ts(), nv(), ends(), xb(), zb()>), l.grid,
                            dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, z, weight, y, silu,
                            first, l.g);
       });
@@ -666,10 +681,10 @@ int launch_gated_norm_bwd(const void* x, const void* z, const float* weight, con
   clear_launch_error();
   const NormLaunch l = norm_launch(s, eps);
   float* pw = dweight ? (float*)ws : nullptr;
-  with_plan(s.group, [&](auto ts, auto nv, auto rag) {
+  with_plan(s.group, [&](auto ts, auto nv, auto ends) {
     with_bool(xbf16, [&](auto xb) {
       with_bool(zbf16, [&](auto zb) {
-        hipLaunchKernelGGL((gated_norm_bwd_kernel<ts(), nv(), rag(), xb(), zb()>), l.grid,
+        hipLaunchKernelGGL((gated_norm_bwd_kernel<ts(), nv(), ends(), xb(), zb()>), l.grid,
                            dim3((unsigned)l.threads), 0, (hipStream_t)stream, x, z, weight, dy,
                            dx, dz, pw, silu, first, l.g);
       });
