@@ -42,6 +42,12 @@ extern "C" {
  * nearer end; where entries descend a call still reads and writes nothing out
  * of range, but its results are undefined.
  *
+ * For sequences of equal length with V = 64 these are ssd_forward's results for
+ * x = v, B = k, C = scale q, dt = 1, A = log_decay and D = 0 (there with every chunk's
+ * state in memory), and the single token's call ssd_decode_step's with the state
+ * transposed.  Here are packed sequences, values of 128, K and V in any pairing,
+ * gradients, and outputs without the states.
+ *
  * Supported: K and V in {64, 128}, up to 32768 heads, tokens * nheads below 2^27,
  * nseq * nheads below 2^22 (of the recurrent form: tokens * nheads below 2^24);
  * anything else valid returns SSD_ERR_UNSUPPORTED.
@@ -66,9 +72,10 @@ size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims *dims, ssd_dtype d
  * initial state) or NULL.  They may be the same buffer (sequences continued
  * in place).  Sums and states are fp32; for bf16 tensors the
  * states, scores and decayed values enter products as two bf16 terms, which leave at
- * most 2^-16 of each.  A value of v that is not finite
- * makes its column of o NaN from its token on, and those before it are as they
- * would be without (and so for k, q and dout in the gradients' walks).
+ * most 2^-16 of each.  A value of v that is not
+ * finite leaves its column of o, from its token on, and of the final state NaN or
+ * infinite, and the tokens before it as they would be without (and so for k, q and
+ * dout in the gradients' walks).
  */
 ssd_status ssd_linattn_fwd(const void *q, const void *k, const void *v,
                            const float *log_decay, const float *init_state,
@@ -115,7 +122,8 @@ ssd_status ssd_linattn_step(const void *q, const void *k, const void *v,
  * res_dtype; res_scale, weight [dim] fp32.  residual NULL: zeros (the first
  * block); res_scale or weight NULL: ones; residual_out NULL: h is not stored.
  * y is formed from h before h is rounded to res_dtype.  residual_out may be
- * the same buffer as residual, and y the same as x.  eps > 0.
+ * the same buffer as residual, and y the same as x.  eps > 0.  The squares are summed
+ * in fp32: rows of values beyond some 1e17 overflow to y = 0 (here and below).
  * Supported: dim up to 16384.
  */
 ssd_status ssd_add_norm_fwd(const void *x, const void *residual, const float *res_scale,

@@ -38,8 +38,8 @@
 // scores, M in X^T M (one term would leave 2^-8 |X|^T |M|, which is not small beside
 // an output whose products cancel: keys of one mean and queries that sum to zero gave
 // outputs off by a tenth) and the decayed Z in M's update (three where M goes on to
-// an fp32 state in memory: the product is then as exact as an fp32 one).  fp32 tensors: 16x16x4 fp32
-// products, chunks of 32 (the scores' share grows with the chunk, and these
+// an fp32 state in memory: the product is then as exact as an fp32 one).  fp32 tensors:
+// 16x16x4 fp32 products, chunks of 32 (the scores' share grows with the chunk, and these
 // calls are bound by the matrix pipe).
 //
 // The chains of a call are few (sequences x heads) and long, so each is cut
@@ -56,13 +56,13 @@
 // kept as two fp32 terms, or corrected from chunk to chunk: the rounding of one
 // factor would otherwise grow with the number of chunks.
 //
-// Measured on MI355X (bf16; a device copy moves 5.1 TB/s).  8 x 2048 tokens, 16
-// heads of 128 x 128: run_states 35 us, walks 77 us (300 MB: 3.9 TB/s).  Gradients
-// of 16384 tokens, 32 heads of 128 x 128: run_states 177 us, the three walks 445 us
-// (1.5 GB: 3.4 TB/s; matrix pipe 24% busy, vector unit 30%, LDS 31%).  65536
-// tokens, 32 heads of 128 x 64 on one group: run_states 152 us, walks 332 us;
-// there q and k come from the caches and the LDS (54% busy), the vector unit (39%)
-// and the matrix pipe (24%) bound it together.
+// Measured on MI355X (bf16; a device copy moves 5.1 TB/s; kernels under the profiler).
+// 8 x 2048 tokens, 16 heads of 128 x 128: run_states 40 us, walks 92 us (300 MB: 3.3
+// TB/s).  Gradients of 16384 tokens, 32 heads of 128 x 128: run_states 153 us, the three
+// walks 435 us (1.5 GB: 3.4 TB/s; matrix pipe 26% busy, vector unit 35%, LDS 27%).
+// 65536 tokens, 32 heads of 128 x 64 on one group: run_states 141 us, walks 328 us; there q
+// and k come from the caches, and the LDS (49% busy), the vector unit (44%) and
+// the matrix pipe (27%) bound it together.
 #include "ssd_block_launch.h"
 #include "ssd_device.h"
 #include "ssd_host.h"
@@ -76,9 +76,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 // A walk goes through the slots before its own itself in sequences of up to this
-// many runs: up to kFold - 1 slots are then read by each run, where run_starts
-// reads and writes each once and costs a launch (some 10 us at 4 runs of 16 heads
-// and 8 sequences; the walks get 3 us longer).
+// many runs: up to kFold - 1 slots are then read by each run, where run_starts reads
+// and writes each once and costs a launch.  8 sequences of 2048 tokens, 16 heads of 128 x
+// 128, which are 4 runs each: 110 us against 118 with run_starts for all.  Where the host
+// does not know the lengths (cu_seqlens) the launch is made whenever the tokens would
+// be enough for more runs in one sequence, and passes the shorter ones by, some 5 us: 115
+// us there, against 120.
 constexpr int kFold = 4;
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 constexpr uint32_t kPastRange = 0x7FFF0000u;
@@ -850,11 +853,11 @@ __device__ __forceinline__ void walk_run(const Walk& w, const Seqs& sq, const Ru
 // each SIMD), and the LDS.  Two for a 128 x 128 M, and for outputs of bf16 tensors by a
 // 64 x 128 one, whose two column blocks for each wave spill with three (two against three,
 // 8 x 2048 tokens, 16 heads: 84 and 110 us; 9000, 5461 and 1923 tokens: 89 and 114).  The
-// gradients of 64 x 128 and 128 x 64 states, which have such a walk too, spill some 25
-// with three and keep them all the same: runs of whole chunks fill two places less evenly (24 heads
-// on 8 groups, 4 x 2048 tokens 284 and 300 us, but seven documents of 41 to 5000 tokens 424
-// and 347).  fp32 tensors and an M of 64 columns do not spill with three (128 x 64, 65536
-// tokens, 32 heads: 484 and 439 us).
+// gradients of 64 x 128 and 128 x 64 states have such a walk too and spill some 25
+// registers with three, but keep them: with two the runs, which are whole chunks, can fill
+// the CUs less evenly (24 heads on 8 groups, 4 x 2048 tokens: 284 and 300 us; seven
+// documents of 41 to 5000 tokens: 424 and 347).  fp32 tensors and an M of 64 columns do
+// not spill with three (128 x 64, 65536 tokens, 32 heads: 484 and 439 us).
 template <int K, int V, bool BF16, int NW>
 constexpr int resident() { return V == 128 && (K == 128 || (BF16 && NW == 1)) ? 2 : 3; }
 

@@ -42,3 +42,30 @@ def test_each_decay_by_itself(ssd, decays, K, V, dtype):  # noqa: F811
 def test_each_head_by_itself(ssd, lens, H, G, K, V, init, dtype):  # noqa: F811
     s = make(lens, H, G, K, V, dtype, seed=sum(lens) + 2 * H, init=init)
     run(ssd, s, f"{dtype} {lens}")
+
+
+@pytest.mark.parametrize("G,H", [(2, 4), (3, 3)])
+def test_equal_lengths_are_the_ssd_with_constant_steps(ssd, G, H):  # noqa: F811
+    """x = v, B = k, C = scale q, dt = 1, A = log_decay, D = 0; and a further token on the
+    transposed state.  fp32: each side as far from exact as the parity tests allow, 1e-4
+    of the largest of a value and the root mean square."""
+    b, L, K, V = 2, 150, 128, 64
+    g = torch.Generator().manual_seed(G)
+    q, k = (torch.randn(b, L, G, K, generator=g).to("cuda:0") for _ in range(2))
+    v = torch.randn(b, L, H, V, generator=g).to("cuda:0")
+    ld = -torch.rand(H, generator=g).to("cuda:0")
+    scale, ones, none = K ** -0.5, torch.ones(b, L, H, device="cuda:0"), torch.zeros_like(ld)
+    o, final = ssd.linattn(q, k, v, ld)
+    y, _, last = ssd.forward(v, ones, ld, k, q * scale, none)
+
+    def close(a, r):
+        assert float((a - r).abs().max() / r.square().mean().sqrt()) <= 2e-4
+
+    close(o, y)
+    close(final.transpose(-1, -2), last)
+    q1, k1, v1 = (t[:, 0].contiguous() for t in (q, k, v))
+    o1, y1 = torch.empty_like(v1), torch.empty_like(v1)
+    ssd.ssd_linattn_step(q1, k1, v1, ld, final, o1)
+    ssd.ssd_decode_step(v1, ones[:, 0].contiguous(), ld, k1, q1 * scale, none, last, y1)
+    close(o1, y1)
+    close(final.transpose(-1, -2), last)
