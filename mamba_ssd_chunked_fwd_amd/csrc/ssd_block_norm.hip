@@ -13,8 +13,8 @@
 // MI355X design.  Each call reads its inputs once and writes its outputs
 // once: HBM-bound (gradients: up to 8192 channels, see below).  A team of TS lanes owns a
 // segment: NV vectors of eight elements per lane stay in registers between the sums and
-// the outputs (where the segment length is no multiple of 8 the vectors start at any element, and the
-// last one overlaps the one before).  The sums of a team
+// the outputs (where the segment length is no multiple of 8 the vectors start at any
+// element, and the last one overlaps the one before).  The sums of a team
 // within a wave are lane exchanges; teams of several waves meet once in LDS.
 // Teams are tied to a group of channels and walk the rows with the stride of
 // the grid, so weights are loaded once per team, and the gradients of weights

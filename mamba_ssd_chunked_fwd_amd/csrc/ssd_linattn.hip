@@ -866,9 +866,8 @@ constexpr int resident() { return V == 128 && (K == 128 || (BF16 && NW == 1)) ? 
 // heads, which share operands.  Items without a run (up to nseq of them) come
 // last: in between they would leave CUs with one workgroup and others with three.
 template <int K, int V, bool BF16, int NW, bool OUT>
-__global__ __launch_bounds__(kThreads, (resident<K, V, BF16, NW>())) void walk_kernel(Walks ws, Seqs sq,
-                                                        const float* __restrict__ log_decay,
-                                                        int H) {
+__global__ __launch_bounds__(kThreads, (resident<K, V, BF16, NW>())) void walk_kernel(
+    Walks ws, Seqs sq, const float* __restrict__ log_decay, int H) {
   using SA = Shape2<K, V, BF16>;
   using SB = Shape2<V, K, BF16>;
   constexpr int XA = OUT ? SA::BYTES : SA::STATE_BYTES;
