@@ -1,7 +1,7 @@
 """Mamba-2 SSD chunked forward on AMD Instinct MI355X (gfx950).
 
-A thin Python binding over libssd's C ABI (``include/ssd.h`` and
-``include/ssd_block.h``).  Every step of
+A thin Python binding over libssd's C ABI (``include/ssd.h``,
+``include/ssd_block.h`` and ``include/ssd_selective.h``).  Every step of
 the computation runs in the library's HIP kernels; this module only checks
 tensor shapes/dtypes, builds the dims struct and passes device pointers and
 the current HIP stream.  PyTorch supplies device memory and streams.
@@ -11,10 +11,14 @@ Entry points (same names as the C ABI):
   ssd_compute_out, ssd_state_and_out, ssd_forward, ssd_forward_noalloc,
   ssd_decode_step, ssd_causal_conv1d, ssd_gdn_chunk_fwd_h, ssd_gdn_chunk_fwd_o,
   ssd_linattn_fwd, ssd_linattn_bwd, ssd_linattn_step, ssd_add_norm_fwd,
-  ssd_add_norm_bwd, ssd_gated_norm_fwd, ssd_gated_norm_bwd
+  ssd_add_norm_bwd, ssd_gated_norm_fwd, ssd_gated_norm_bwd,
+  ssd_short_conv_fwd, ssd_short_conv_bwd, ssd_short_conv_step,
+  ssd_selective_scan_fwd, ssd_selective_scan_bwd, ssd_selective_scan_step,
+  ssd_add_norm_quant_fwd
 and the allocating convenience wrappers ``forward``, ``linattn``,
-``linattn_backward``, ``add_norm``, ``add_norm_backward``, ``gated_norm`` and
-``gated_norm_backward``.
+``linattn_backward``, ``add_norm``, ``add_norm_backward``, ``gated_norm``,
+``gated_norm_backward``, ``short_conv``, ``short_conv_backward``,
+``selective_scan``, ``selective_scan_backward`` and ``add_norm_quant``.
 
 Importing fails loudly (ImportError) when libssd.so has not been built:
 there is no fallback implementation.
@@ -32,6 +36,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssd.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ssd.h")
 BLOCK_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ssd_block.h")
+SELECTIVE_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ssd_selective.h")
 
 SSD_OK = 0
 SSD_ERR_INVALID_ARGUMENT = 1
@@ -41,6 +46,8 @@ SSD_ERR_HIP = 4
 SSD_F32 = 0
 SSD_BF16 = 1
 SSD_GATES = {"silu": 0, "sigmoid": 1}
+SSD_CONV_ACTS = {None: 0, "silu": 1}
+SSD_CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}
 
 
 class SsdDims(ctypes.Structure):
@@ -65,6 +72,20 @@ class LinattnDims(ctypes.Structure):
 class GatedNormDims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("group", ctypes.c_int64), ("weight_dim", ctypes.c_int64)]
+
+
+class ShortConvDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("nseq", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64)]
+
+
+class SelectiveScanDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("nseq", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64)]
 
 
 class SsdError(RuntimeError):
@@ -135,6 +156,27 @@ def _load() -> ctypes.CDLL:
     lib.ssd_gated_norm_bwd_workspace_bytes.restype = sz
     lib.ssd_gated_norm_bwd.argtypes = [vp] * 8 + [sz, f, i, i, i, i, ndims, vp]
     lib.ssd_gated_norm_bwd.restype = i
+    cdims, sdims = ctypes.POINTER(ShortConvDims), ctypes.POINTER(SelectiveScanDims)
+    lib.ssd_short_conv_fwd.argtypes = [vp] * 7 + [i, i, cdims, vp]
+    lib.ssd_short_conv_fwd.restype = i
+    lib.ssd_short_conv_bwd_workspace_bytes.argtypes = [cdims]
+    lib.ssd_short_conv_bwd_workspace_bytes.restype = sz
+    lib.ssd_short_conv_bwd.argtypes = [vp] * 12 + [sz, i, i, cdims, vp]
+    lib.ssd_short_conv_bwd.restype = i
+    lib.ssd_short_conv_step.argtypes = [vp] * 5 + [i, i, cdims, vp]
+    lib.ssd_short_conv_step.restype = i
+    for name in ("ssd_selective_scan_fwd_workspace_bytes",
+                 "ssd_selective_scan_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [sdims, i]
+        getattr(lib, name).restype = sz
+    lib.ssd_selective_scan_fwd.argtypes = [vp] * 13 + [sz, i, i, sdims, vp]
+    lib.ssd_selective_scan_fwd.restype = i
+    lib.ssd_selective_scan_bwd.argtypes = [vp] * 22 + [sz, i, i, sdims, vp]
+    lib.ssd_selective_scan_bwd.restype = i
+    lib.ssd_selective_scan_step.argtypes = [vp] * 10 + [i, i, sdims, vp]
+    lib.ssd_selective_scan_step.restype = i
+    lib.ssd_add_norm_quant_fwd.argtypes = [vp] * 7 + [i64, i64, i64, f, i, i, i, vp]
+    lib.ssd_add_norm_quant_fwd.restype = i
     return lib
 
 
@@ -805,6 +847,298 @@ def _run_gated_norm_bwd(d, ins, x, z, dy, dx, dz, dweight, workspace, eps, gate,
           _gate(gate), int(gate_first), _dtype_code(x.dtype), _dtype_code(dy.dtype), d)
 
 
+# ------------------------------------------- operators of a selective state space
+def _rows_arg(t, name: str, shape, dtypes, device, size: int):
+    """The address and the row stride (in elements) of a tensor whose rows (its last
+    dimensions, ``shape`` being all of them) may be columns of a wider tensor.  It
+    starts on a multiple of ``size`` bytes, and so does every row."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    p, el = t.data_ptr(), t.element_size()
+    if t.is_contiguous():
+        stride = 0
+    else:
+        stride = _row_stride(t, name)
+        if stride * el % size:
+            raise ValueError(f"rows of {name} must be a multiple of {size} bytes apart (pass a "
+                             f"copy)")
+    if p % size:
+        raise ValueError(f"{name} must start on a {size}-byte boundary (pass a copy)")
+    return p, stride
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of x [b, L, dim] or [b, dim], or of B [b, L, G, N] or
+    [b, G, N]: rows contiguous, one distance between all of them."""
+    lead = 2 if t.dim() == 4 or (t.dim() == 3 and name not in ("B", "C")) else 1
+    inner = 1
+    for n, s in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if n > 1 and s != inner:
+            raise ValueError(f"{name}: the elements of a row must be contiguous (pass a copy)")
+        inner *= n
+    b, L = (1, t.shape[0]) if lead == 1 else t.shape[:2]
+    if b * L == 1:
+        return inner
+    stride = t.stride(lead - 1) if L > 1 else t.stride(0)
+    if stride < inner or (lead == 2 and b > 1 and L > 1 and t.stride(0) != L * stride):
+        raise ValueError(f"{name}: rows must be one distance apart (pass a copy)")
+    return stride
+
+
+def _sequences(b: int, cu_seqlens, device):
+    """The number of sequences and the address of cu_seqlens (None: each batch row is
+    one sequence)."""
+    if cu_seqlens is None:
+        return b, None
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 \
+            or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a tensor [sequences + 1]")
+    if b != 1:
+        raise ValueError(f"packed sequences need a batch of 1, not {b}")
+    return cu_seqlens.numel() - 1, _arg(cu_seqlens, "cu_seqlens", None, (torch.int32,), device)
+
+
+def _conv_act(activation: Optional[str]) -> int:
+    if activation not in SSD_CONV_ACTS:
+        raise ValueError(f"activation must be None or 'silu', not {activation!r}")
+    return SSD_CONV_ACTS[activation]
+
+
+def _conv_args(x, weight, bias, init_state, cu_seqlens):
+    """The dims of a short convolution and the addresses of its inputs."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a tensor [batch, seqlen, dim]")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor [dim, width]")
+    b, L, D = x.shape
+    W, dev = weight.shape[1], x.device
+    px, stride = _rows_arg(x, "x", x.shape, _FLOATS, dev, x.element_size())
+    nseq, cu = _sequences(b, cu_seqlens, dev)
+    return ShortConvDims(b * L, nseq, D, W, stride), [
+        px, _arg(weight, "weight", (D, W), _F32, dev), _arg(bias, "bias", (D,), _F32, dev, True),
+        _arg(init_state, "init_state", (nseq, W - 1, D), (x.dtype,), dev, True), cu]
+
+
+def short_conv_workspace_bytes(d: ShortConvDims) -> int:
+    return int(_lib.ssd_short_conv_bwd_workspace_bytes(ctypes.byref(d)))
+
+
+def _run_conv_fwd(d, ins, x, y, final_state, activation) -> None:
+    dev, own = x.device, (x.dtype,)
+    _call("ssd_short_conv_fwd", dev, *ins, _arg(y, "y", x.shape, own, dev),
+          _arg(final_state, "final_state", (d.nseq, d.width - 1, d.dim), own, dev, True),
+          _conv_act(activation), _dtype_code(x.dtype), d)
+
+
+def _run_conv_bwd(d, ins, x, dy, dfinal, dx, dweight, dbias, dinit, workspace,
+                  activation) -> None:
+    dev, own = x.device, (x.dtype,)
+    state = (d.nseq, d.width - 1, d.dim)
+    _call("ssd_short_conv_bwd", dev, *ins, _arg(dy, "dy", x.shape, own, dev),
+          _arg(dfinal, "dfinal", state, own, dev, True), _arg(dx, "dx", x.shape, own, dev),
+          _arg(dweight, "dweight", (d.dim, d.width), _F32, dev, True),
+          _arg(dbias, "dbias", (d.dim,), _F32, dev, True),
+          _arg(dinit, "dinit", state, own, dev, True), *workspace, _conv_act(activation),
+          _dtype_code(x.dtype), d)
+
+
+def ssd_short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                       init_state: Optional[torch.Tensor], cu_seqlens: Optional[torch.Tensor],
+                       y: torch.Tensor, final_state: Optional[torch.Tensor],
+                       activation: Optional[str] = "silu") -> None:
+    """The short causal convolution: y_t = act(bias + sum_k weight[:, k] x_{t-W+1+k}), the
+    W - 1 rows before a sequence's first being init_state's (or zeros).  x, y [b, L, dim]
+    (fp32 or bf16; rows of x may be columns of a wider tensor), weight [dim, W] and bias
+    [dim] fp32 (bias may be None), states [sequences, W-1, dim] in x's type or None.
+    With cu_seqlens [sequences + 1] int32 the sequences are packed in a batch of
+    1; else each batch row is one.  activation "silu" or None."""
+    d, ins = _conv_args(x, weight, bias, init_state, cu_seqlens)
+    _run_conv_fwd(d, ins, x, y, final_state, activation)
+
+
+def ssd_short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                       init_state: Optional[torch.Tensor], cu_seqlens: Optional[torch.Tensor],
+                       dy: torch.Tensor, dfinal: Optional[torch.Tensor], dx: torch.Tensor,
+                       dweight: Optional[torch.Tensor], dbias: Optional[torch.Tensor],
+                       dinit: Optional[torch.Tensor], workspace: torch.Tensor,
+                       activation: Optional[str] = "silu") -> None:
+    """Gradients of ``ssd_short_conv_fwd`` from its inputs.  ``workspace`` has
+    short_conv_workspace_bytes(dims) bytes."""
+    d, ins = _conv_args(x, weight, bias, init_state, cu_seqlens)
+    _run_conv_bwd(d, ins, x, dy, dfinal, dx, dweight, dbias, dinit,
+                  _workspace(workspace, x.device), activation)
+
+
+def ssd_short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                        state: torch.Tensor, y: torch.Tensor,
+                        activation: Optional[str] = "silu") -> None:
+    """One token of the short convolution for every sequence: ``state`` [b, W-1, dim] is
+    updated in place and ``y`` [b, dim] written.  x [b, dim]."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [batch, dim]")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor [dim, width]")
+    b, D = x.shape
+    W, dev, own = weight.shape[1], x.device, (x.dtype,)
+    px, stride = _rows_arg(x, "x", x.shape, _FLOATS, dev, x.element_size())
+    _call("ssd_short_conv_step", dev, px, _arg(weight, "weight", (D, W), _F32, dev),
+          _arg(bias, "bias", (D,), _F32, dev, True),
+          _arg(state, "state", (b, W - 1, D), own, dev), _arg(y, "y", x.shape, own, dev),
+          _conv_act(activation), _dtype_code(x.dtype), ShortConvDims(b, b, D, W, stride))
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, step: bool):
+    """The dims of a selective scan but nseq, and the addresses of its inputs."""
+    lead = 1 if step else 2
+    if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
+        raise ValueError(f"x must be a tensor [batch, {'' if step else 'seqlen, '}dim]")
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a tensor [dim, dstate]")
+    if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
+        raise ValueError(f"B must be a tensor [batch, {'' if step else 'seqlen, '}groups, dstate]")
+    dim, N, G, dev, own = x.shape[-1], A.shape[1], B.shape[-2], x.device, (x.dtype,)
+    el, bc = x.element_size(), x.shape[:-1] + (G, N)
+    px, xs = _rows_arg(x, "x", x.shape, _FLOATS, dev, el)
+    pdt, dts = _rows_arg(dt, "dt", x.shape, own, dev, el)
+    pB, bs = _rows_arg(B, "B", bc, own, dev, 4)
+    pC, cs = _rows_arg(C, "C", bc, own, dev, 4)
+    pz, zs = (None, 0) if z is None else _rows_arg(z, "z", x.shape, own, dev, el)
+    return SelectiveScanDims(x.numel() // dim if dim else 0, 0, dim, N, G, xs, dts, zs, bs, cs), [
+        px, pdt, _arg(A, "A", (dim, N), _F32, dev), pB, pC,
+        _arg(D, "D", (dim,), _F32, dev, True), pz,
+        _arg(dt_bias, "dt_bias", (dim,), _F32, dev, True)]
+
+
+def _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens):
+    d, ins = _scan_args(x, dt, A, B, C, D, z, dt_bias, False)
+    d.nseq, cu = _sequences(x.shape[0], cu_seqlens, x.device)
+    ins += [_arg(init_state, "init_state", (d.nseq, d.dim, d.dstate), _F32, x.device, True), cu]
+    return d, ins
+
+
+def selective_scan_workspace_bytes(d: SelectiveScanDims, dtype: torch.dtype,
+                                   backward: bool = False) -> int:
+    f = (_lib.ssd_selective_scan_bwd_workspace_bytes if backward
+         else _lib.ssd_selective_scan_fwd_workspace_bytes)
+    return int(f(ctypes.byref(d), _dtype_code(dtype)))
+
+
+def _run_scan_fwd(d, ins, x, y, final_state, workspace, softplus) -> None:
+    dev = x.device
+    _call("ssd_selective_scan_fwd", dev, *ins, _arg(y, "y", x.shape, (x.dtype,), dev),
+          _arg(final_state, "final_state", (d.nseq, d.dim, d.dstate), _F32, dev, True),
+          *workspace, int(softplus), _dtype_code(x.dtype), d)
+
+
+def _run_scan_bwd(d, ins, x, dy, dfinal, grads, workspace, softplus) -> None:
+    dev, own = x.device, (x.dtype,)
+    dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit = grads
+    if (ins[6] is None) != (dz is None):
+        raise ValueError("dz is given exactly when z is")
+    state, bc = (d.nseq, d.dim, d.dstate), x.shape[:-1] + (d.ngroups, d.dstate)
+    _call("ssd_selective_scan_bwd", dev, *ins, _arg(dy, "dy", x.shape, own, dev),
+          _arg(dfinal, "dfinal", state, _F32, dev, True), _arg(dx, "dx", x.shape, own, dev),
+          _arg(ddt, "ddt", x.shape, own, dev), _arg(dA, "dA", (d.dim, d.dstate), _F32, dev),
+          _arg(dB, "dB", bc, own, dev), _arg(dC, "dC", bc, own, dev),
+          _arg(dD, "dD", (d.dim,), _F32, dev, True), _arg(dz, "dz", x.shape, own, dev, True),
+          _arg(ddt_bias, "ddt_bias", (d.dim,), _F32, dev, True),
+          _arg(dinit, "dinit", state, _F32, dev, True), *workspace, int(softplus),
+          _dtype_code(x.dtype), d)
+
+
+def ssd_selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                           C: torch.Tensor, D: Optional[torch.Tensor],
+                           z: Optional[torch.Tensor], dt_bias: Optional[torch.Tensor],
+                           init_state: Optional[torch.Tensor],
+                           cu_seqlens: Optional[torch.Tensor], y: torch.Tensor,
+                           final_state: Optional[torch.Tensor], workspace: torch.Tensor,
+                           softplus: bool = True) -> None:
+    """The selective scan: with delta = softplus(dt + dt_bias), per channel h_t =
+    exp(delta_t A) h_{t-1} + delta_t x_t B_t and y_t = (C_t . h_t + D x_t) silu(z_t).
+    x, dt, z, y [b, L, dim], B and C [b, L, G, N] (fp32 or bf16; rows of the inputs may be
+    columns of wider tensors), A [dim, N], D and dt_bias [dim] fp32, states
+    [sequences, dim, N] fp32; D, z, dt_bias and the states may be None.  With
+    cu_seqlens [sequences + 1] int32 the sequences are packed in a batch of 1; else each
+    batch row is one.  ``workspace`` has selective_scan_workspace_bytes(dims, dtype)
+    bytes."""
+    d, ins = _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens)
+    _run_scan_fwd(d, ins, x, y, final_state, _workspace(workspace, x.device), softplus)
+
+
+def ssd_selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                           C: torch.Tensor, D: Optional[torch.Tensor],
+                           z: Optional[torch.Tensor], dt_bias: Optional[torch.Tensor],
+                           init_state: Optional[torch.Tensor],
+                           cu_seqlens: Optional[torch.Tensor], dy: torch.Tensor,
+                           dfinal: Optional[torch.Tensor], dx: torch.Tensor, ddt: torch.Tensor,
+                           dA: torch.Tensor, dB: torch.Tensor, dC: torch.Tensor,
+                           dD: Optional[torch.Tensor], dz: Optional[torch.Tensor],
+                           ddt_bias: Optional[torch.Tensor], dinit: Optional[torch.Tensor],
+                           workspace: torch.Tensor, softplus: bool = True) -> None:
+    """Gradients of ``ssd_selective_scan_fwd`` from its inputs, into contiguous tensors.
+    ``workspace`` has selective_scan_workspace_bytes(dims, dtype, backward=True) bytes."""
+    d, ins = _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens)
+    _run_scan_bwd(d, ins, x, dy, dfinal, (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit),
+                  _workspace(workspace, x.device), softplus)
+
+
+def ssd_selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
+                            B: torch.Tensor, C: torch.Tensor, D: Optional[torch.Tensor],
+                            z: Optional[torch.Tensor], dt_bias: Optional[torch.Tensor],
+                            state: torch.Tensor, y: torch.Tensor,
+                            softplus: bool = True) -> None:
+    """One token of the selective scan for every sequence: ``state`` [b, dim, N] fp32 is
+    updated in place and ``y`` [b, dim] written.  x, dt, z [b, dim], B, C [b, G, N]."""
+    d, ins = _scan_args(x, dt, A, B, C, D, z, dt_bias, True)
+    dev = x.device
+    d.nseq = d.tokens
+    _call("ssd_selective_scan_step", dev, *ins,
+          _arg(state, "state", (d.tokens, d.dim, d.dstate), _F32, dev),
+          _arg(y, "y", x.shape, (x.dtype,), dev), int(softplus), _dtype_code(x.dtype), d)
+
+
+def _quant_code(dtype: torch.dtype) -> int:
+    if dtype not in SSD_CODES:
+        raise ValueError(f"codes are torch.float8_e4m3fn or torch.int8, not {dtype}")
+    return SSD_CODES[dtype]
+
+
+def ssd_add_norm_quant_fwd(x: torch.Tensor, residual: Optional[torch.Tensor],
+                           res_scale: Optional[torch.Tensor], weight: Optional[torch.Tensor],
+                           codes: torch.Tensor, scales: torch.Tensor,
+                           residual_out: Optional[torch.Tensor], eps: float = 1e-5) -> None:
+    """``ssd_add_norm_fwd`` with its output in 8 bits: ``codes`` [..., dim] (float8_e4m3fn
+    or int8) and ``scales`` [..., dim / group] fp32, of which codes o scales stands for the
+    normed row; the scales' last dimension gives the group (dim, or 16, 32, 64, 128 or
+    256 channels)."""
+    rows, D = _rows(x, "x")
+    dev, shape = x.device, x.shape
+    if not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor):
+        raise TypeError("codes and scales must be torch.Tensors")
+    groups = scales.shape[-1] if scales.dim() else 0
+    if not groups or D % groups:
+        raise ValueError(f"scales must be a tensor [..., groups], groups a divisor of {D}")
+    rdts = _FLOATS if residual is None else (residual.dtype,)
+    rdt = next((t.dtype for t in (residual, residual_out) if t is not None), x.dtype)
+    code = _quant_code(codes.dtype)
+    _call("ssd_add_norm_quant_fwd", dev, _arg(x, "x", None, _FLOATS, dev),
+          _arg(residual, "residual", shape, _FLOATS, dev, True),
+          _arg(res_scale, "res_scale", (D,), _F32, dev, True),
+          _arg(weight, "weight", (D,), _F32, dev, True),
+          _arg(codes, "codes", shape, (codes.dtype,), dev),
+          _arg(scales, "scales", shape[:-1] + (groups,), _F32, dev),
+          _arg(residual_out, "residual_out", shape, rdts, dev, True), rows, D, D // groups, eps,
+          code, _dtype_code(x.dtype), _dtype_code(rdt))
+
+
 # ------------------------------------------------------------ convenience
 def forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
             B: torch.Tensor, C: torch.Tensor, D: torch.Tensor,
@@ -939,3 +1273,101 @@ def gated_norm_backward(x: torch.Tensor, z: Optional[torch.Tensor],
     keep, ws = _scratch(gated_norm_workspace_bytes(d), x.device)
     _run_gated_norm_bwd(d, ins, x, z, dy, dx, dz, dw, ws, eps, gate, gate_first)
     return dx, dz, dw
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               init_state: Optional[torch.Tensor] = None,
+               cu_seqlens: Optional[torch.Tensor] = None,
+               activation: Optional[str] = "silu") -> Tuple[torch.Tensor, torch.Tensor]:
+    """Allocate and run ``ssd_short_conv_fwd``: (y, final_state).  Rows of y outside every
+    packed sequence are not written.  No graph is recorded (gradients come from
+    ``short_conv_backward``): tensors that require one are refused outside
+    torch.no_grad()."""
+    _no_graph("short_conv", x=x, weight=weight, bias=bias, init_state=init_state)
+    d, ins = _conv_args(x, weight, bias, init_state, cu_seqlens)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    final = torch.empty((d.nseq, d.width - 1, d.dim), dtype=x.dtype, device=x.device)
+    _run_conv_fwd(d, ins, x, y, final, activation)
+    return y, final
+
+
+def short_conv_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                        dy: torch.Tensor, dfinal: Optional[torch.Tensor] = None,
+                        init_state: Optional[torch.Tensor] = None,
+                        cu_seqlens: Optional[torch.Tensor] = None,
+                        activation: Optional[str] = "silu"
+                        ) -> Tuple[Optional[torch.Tensor], ...]:
+    """Allocate and run ``ssd_short_conv_bwd``: (dx, dweight, dbias, dinit), None for
+    each of the last two whose input is None."""
+    d, ins = _conv_args(x, weight, bias, init_state, cu_seqlens)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(weight)
+    db, dinit = (None if t is None else torch.empty_like(t) for t in (bias, init_state))
+    keep, ws = _scratch(short_conv_workspace_bytes(d), x.device)
+    _run_conv_bwd(d, ins, x, dy, dfinal, dx, dw, db, dinit, ws, activation)
+    return dx, dw, db, dinit
+
+
+def selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                   C: torch.Tensor, D: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                   init_state: Optional[torch.Tensor] = None,
+                   cu_seqlens: Optional[torch.Tensor] = None,
+                   softplus: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Allocate and run ``ssd_selective_scan_fwd``: (y, final_state).  Rows of y outside
+    every packed sequence are not written.  No graph is recorded (gradients come from
+    ``selective_scan_backward``): tensors that require one are refused outside
+    torch.no_grad()."""
+    _no_graph("selective_scan", x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
+              init_state=init_state)
+    d, ins = _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    final = torch.empty((d.nseq, d.dim, d.dstate), dtype=torch.float32, device=x.device)
+    keep, ws = _scratch(selective_scan_workspace_bytes(d, x.dtype), x.device)
+    _run_scan_fwd(d, ins, x, y, final, ws, softplus)
+    return y, final
+
+
+def selective_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
+                            B: torch.Tensor, C: torch.Tensor, D: Optional[torch.Tensor],
+                            z: Optional[torch.Tensor], dt_bias: Optional[torch.Tensor],
+                            dy: torch.Tensor, dfinal: Optional[torch.Tensor] = None,
+                            init_state: Optional[torch.Tensor] = None,
+                            cu_seqlens: Optional[torch.Tensor] = None, softplus: bool = True
+                            ) -> Tuple[Optional[torch.Tensor], ...]:
+    """Allocate and run ``ssd_selective_scan_bwd``: (dx, ddt, dA, dB, dC, dD, dz,
+    ddt_bias, dinit), None for each of the last four whose input is None."""
+    d, ins = _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens)
+
+    def like(t):
+        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+    grads = [like(t) for t in (x, dt, A, B, C, D, z, dt_bias, init_state)]
+    keep, ws = _scratch(selective_scan_workspace_bytes(d, x.dtype, backward=True), x.device)
+    _run_scan_bwd(d, ins, x, dy, dfinal, grads, ws, softplus)
+    return tuple(grads)
+
+
+def add_norm_quant(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                   res_scale: Optional[torch.Tensor] = None,
+                   weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   dtype: torch.dtype = torch.float8_e4m3fn, group: Optional[int] = None
+                   ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Allocate and run ``ssd_add_norm_quant_fwd``: (codes, scales, residual_out).  group
+    None: one scale for each row.  The codes have no gradient: tensors that require one are
+    refused outside torch.no_grad()."""
+    if torch.is_grad_enabled():
+        for name, t in (("x", x), ("residual", residual), ("res_scale", res_scale),
+                        ("weight", weight)):
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"add_norm_quant has no gradient, and {name} requires one: call "
+                                 f"it under torch.no_grad()")
+    rows, D = _rows(x, "x")
+    group = D if group is None else int(group)
+    if group < 1 or D % group:
+        raise ValueError(f"group must be a divisor of {D}, not {group}")
+    codes = torch.empty(x.shape, dtype=dtype, device=x.device)
+    scales = torch.empty(x.shape[:-1] + (D // group,), dtype=torch.float32, device=x.device)
+    out = torch.empty_like(x if residual is None else residual)
+    ssd_add_norm_quant_fwd(x, residual, res_scale, weight, codes, scales, out, eps)
+    return codes, scales, out

@@ -30,7 +30,10 @@ SOURCES = ["ssd_api.cpp", "ssd_chunk_cumsum.hip", "ssd_fwd_pass_state.hip",
            "ssd_state_two_level.hip", "ssd_forward_noalloc.hip",
            "ssd_fused_f32.hip", "ssd_fused_bf16.hip", "ssd_state_pair_f32.hip",
            "ssd_block_api.cpp", "ssd_block_norm.hip", "ssd_linattn.hip",
-           "ssd_linattn_step.hip"]
+           "ssd_linattn_step.hip",
+           "ssd_selective_api.cpp", "ssd_selective_scan.hip",
+           "ssd_selective_scan_bwd.hip", "ssd_selective_step.hip",
+           "ssd_short_conv.hip", "ssd_norm_quant.hip"]
 
 HIP_FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

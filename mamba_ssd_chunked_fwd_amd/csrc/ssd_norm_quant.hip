@@ -1,0 +1,270 @@
+// The residual add and RMS norm in front of a block whose projection takes 8 bits:
+//   h = residual + s o x,   y = h / sqrt(mean(h^2) + eps) o w,
+//   scale = max |y| / top and codes = nearest(y top / max |y|) per group of channels.
+//
+// MI355X design.  Read once, written once: HBM-bound.  A workgroup owns a row, a lane one or
+// two vectors of eight channels, which stay in registers from the read to the codes; groups
+// of up to 256 channels lie in up to 32 neighbouring lanes and find their largest value by
+// lane exchanges, longer ones meet in LDS.  A code's border may lie anywhere, and a
+// value that 32 bits put on its other side comes out a whole step (up to 12%) away, so
+// everything between the inputs and the codes is formed in 64 bits, which the
+// vector unit does at the rate of 32.
+#include "ssd_host.h"
+#include "ssd_selective_device.h"
+#include "ssd_selective_launch.h"
+
+#include <type_traits>
+
+namespace ssd {
+namespace {
+
+constexpr int kVec = 8;
+constexpr double kLeast = 1e-30;    // groups below it have codes of 0
+
+struct QuantArgs {
+  const void *x, *res;
+  const float *scale, *weight;
+  void *codes, *res_out;
+  float* scales;
+  int64_t rows;
+  int dim, group;
+  double eps, inv_dim;
+};
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void load_eight(const void* p, int64_t i, int left, float (&v)[kVec]) {
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v[e] = e < left ? load_one<BF16>(p, i + e) : 0.0f;
+  } else if constexpr (BF16) {
+    const u32x4 u = *(const u32x4*)((const uint16_t*)p + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16_lo(u[k]);
+      v[2 * k + 1] = bf16_hi(u[k]);
+    }
+  } else {
+    const f32x4 a = *(const f32x4*)((const float*)p + i);
+    const f32x4 b = *(const f32x4*)((const float*)p + i + 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = a[k];
+      v[4 + k] = b[k];
+    }
+  }
+}
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void store_eight(void* p, int64_t i, int left, const float (&v)[kVec]) {
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      if (e < left) store_one<BF16>(p, i + e, v[e]);
+  } else if constexpr (BF16) {
+    *(u32x4*)((uint16_t*)p + i) = (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                          pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+  } else {
+    *(f32x4*)((float*)p + i) = (f32x4){v[0], v[1], v[2], v[3]};
+    *(f32x4*)((float*)p + i + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+  }
+}
+
+// The larger of two values that are not negative; a NaN stays (its bits are the largest).
+__device__ __forceinline__ double larger(double a, double b) {
+  const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
+  return x > y ? a : b;
+}
+
+// To 32 bits so that rounding the result again, to fewer bits, rounds v once: cut off, and
+// the last bit set if anything was.
+__device__ __forceinline__ float to_odd(double v) {
+  uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t rest = u & 0x1FFFFFFFu;
+  u &= ~(uint64_t)0x1FFFFFFFu;
+  if (rest != 0) u |= 0x20000000u;
+  return (float)__builtin_bit_cast(double, u);
+}
+
+// Eight codes.
+template <bool E4M3>
+__device__ __forceinline__ u32x2 encode(const double (&v)[kVec]) {
+  u32x2 out;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if constexpr (E4M3) {
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(to_odd(v[4 * k]), to_odd(v[4 * k + 1]), 0, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(to_odd(v[4 * k + 2]), to_odd(v[4 * k + 3]), w, true);
+      out[k] = (uint32_t)w;
+    } else {
+      uint32_t w = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const double q = v[4 * k + e];
+        const int c = q == q ? (int)__builtin_rint(q) : 0;
+        w |= (uint32_t)(c & 0xFF) << (8 * e);
+      }
+      out[k] = w;
+    }
+  }
+  return out;
+}
+
+constexpr int kMaxWaves = 16;
+
+// GROUPED: groups of 16 to 256 channels; otherwise the row is one.
+template <int NV, bool XBF16, bool RBF16, bool E4M3, bool GROUPED, bool WHOLE>
+__global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const QuantArgs a) {
+  __shared__ double red[2][kMaxWaves];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int waves = (int)blockDim.x / kWave;
+  const double top = E4M3 ? 448.0 : 127.0;
+
+  float s[NV][kVec], w[NV][kVec];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * kVec;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) s[j][e] = w[j][e] = 1.0f;
+    if (c < a.dim) {
+      if (a.scale) load_eight<false, WHOLE>(a.scale, c, a.dim - c, s[j]);
+      if (a.weight) load_eight<false, WHOLE>(a.weight, c, a.dim - c, w[j]);
+    }
+  }
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    double h[NV][kVec], sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * kVec;
+      const int64_t i = row * a.dim + c;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) h[j][e] = 0.0;
+      if (c >= a.dim) continue;
+      float x[kVec], r[kVec];
+      load_eight<XBF16, WHOLE>(a.x, i, a.dim - c, x);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) r[e] = 0.0f;
+      if (a.res) load_eight<RBF16, WHOLE>(a.res, i, a.dim - c, r);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        h[j][e] = __builtin_fma((double)s[j][e], (double)x[e], (double)r[e]);
+        if (!WHOLE && c + e >= a.dim) h[j][e] = 0.0;
+        sum = __builtin_fma(h[j][e], h[j][e], sum);
+        r[e] = (float)h[j][e];
+      }
+      if (a.res_out) store_eight<RBF16, WHOLE>(a.res_out, i, a.dim - c, r);
+    }
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+    if (waves > 1) {
+      if (lane == 0) red[0][wave] = sum;
+      __syncthreads();
+      sum = 0.0;
+      for (int k = 0; k < waves; ++k) sum += red[0][k];
+    }
+    const double rstd = 1.0 / __builtin_sqrt(__builtin_fma(sum, a.inv_dim, a.eps));
+    double most[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      most[j] = 0.0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        h[j][e] = h[j][e] * rstd * (double)w[j][e];
+        most[j] = larger(most[j], __builtin_fabs(h[j][e]));
+      }
+    }
+    if constexpr (GROUPED) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        for (int off = 1; off < a.group / kVec; off <<= 1)
+          most[j] = larger(most[j], __shfl_xor(most[j], off, kWave));
+      }
+    } else {
+      double m = most[0];
+#pragma unroll
+      for (int j = 1; j < NV; ++j) m = larger(m, most[j]);
+#pragma unroll
+      for (int off = kWave / 2; off > 0; off >>= 1) m = larger(m, __shfl_xor(m, off, kWave));
+      if (waves > 1) {
+        if (lane == 0) red[1][wave] = m;
+        __syncthreads();
+        for (int k = 0; k < waves; ++k) m = larger(m, red[1][k]);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) most[j] = m;
+    }
+    const int64_t groups = a.dim / a.group;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * kVec;
+      if (c >= a.dim) continue;
+      const double inv = most[j] >= kLeast ? top / most[j] : 0.0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) h[j][e] *= inv;
+      const u32x2 codes = encode<E4M3>(h[j]);
+      uint8_t* out = (uint8_t*)a.codes + row * a.dim + c;
+      if constexpr (WHOLE) {
+        *(u32x2*)out = codes;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+          if (c + e < a.dim) out[e] = (uint8_t)(codes[e / 4] >> (8 * (e % 4)));
+      }
+      if (c % a.group == 0) a.scales[row * groups + c / a.group] = (float)(most[j] / top);
+    }
+    if (waves > 1 && GROUPED) __syncthreads();   // (red[0] is written again)
+  }
+}
+
+template <int NV, bool XBF16, bool RBF16, bool E4M3>
+void launch_t(const QuantArgs& a, bool grouped, bool whole, int blocks, int threads,
+              hipStream_t st) {
+#define SSD_QUANT(G, W)                                                                       \
+  hipLaunchKernelGGL((add_norm_quant_kernel<NV, XBF16, RBF16, E4M3, G, W>), dim3(blocks),     \
+                     dim3(threads), 0, st, a)
+  if (grouped)
+    SSD_QUANT(true, true);
+  else if (whole)
+    SSD_QUANT(false, true);
+  else
+    SSD_QUANT(false, false);
+#undef SSD_QUANT
+}
+
+}  // namespace
+
+int launch_add_norm_quant(const void* x, const void* res, const float* scale, const float* weight,
+                          void* codes, float* scales, void* res_out, int64_t rows, int64_t dim,
+                          int64_t group, float eps, bool e4m3, bool xbf16, bool rbf16,
+                          void* stream) {
+  clear_launch_error();
+  const QuantArgs a{x, res, scale, weight, codes, res_out, scales, rows, (int)dim, (int)group,
+                    (double)eps, 1.0 / (double)dim};
+  const int vectors = (int)((dim + kVec - 1) / kVec);
+  const int nv = vectors > kMaxWaves * kWave ? 2 : 1;
+  const int waves = (vectors + nv * kWave - 1) / (nv * kWave);
+  // 16 waves per CU
+  const int64_t most = 4096 / waves;
+  const int blocks = (int)(rows < most ? rows : most);
+  const bool grouped = group == 16 || group == 32 || group == 64 || group == 128 || group == 256;
+  const bool whole = dim % kVec == 0;
+  hipStream_t st = (hipStream_t)stream;
+  auto go = [&](auto n, auto xb, auto rb, auto q) {
+    launch_t<decltype(n)::value, decltype(xb)::value, decltype(rb)::value, decltype(q)::value>(
+        a, grouped, whole, blocks, waves * kWave, st);
+  };
+  auto code = [&](auto n, auto xb, auto rb) {
+    e4m3 ? go(n, xb, rb, std::true_type{}) : go(n, xb, rb, std::false_type{});
+  };
+  auto res_type = [&](auto n, auto xb) {
+    rbf16 ? code(n, xb, std::true_type{}) : code(n, xb, std::false_type{});
+  };
+  auto x_type = [&](auto n) {
+    xbf16 ? res_type(n, std::true_type{}) : res_type(n, std::false_type{});
+  };
+  if (nv == 1)
+    x_type(std::integral_constant<int, 1>{});
+  else
+    x_type(std::integral_constant<int, 2>{});
+  return (int)hipGetLastError();
+}
+
+}  // namespace ssd
