@@ -3,6 +3,8 @@
 
 #include "ssd_host.h"
 
+#include <type_traits>
+
 namespace ssd {
 namespace {
 
@@ -102,336 +104,414 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   for (int n = 0; n < N; ++n) b.back[(pl.slot * N + n) * a.dim + d] = back[n];
 }
 
-// ---- sums over a wave's lanes, several values at once
-// Two values' sums over pairs of lanes that differ in one bit of their number: the
-// lanes without that bit hold a's, those with it b's.
-__device__ __forceinline__ float merge32(float a, float b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
-                                                  false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-__device__ __forceinline__ float merge16(float a, float b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
-                                                  false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-constexpr int kRowRor8 = 0x128, kHalfMirror = 0x141, kQuadXor2 = 0x4E, kQuadXor1 = 0xB1;
+// ---- the second walk, down the tokens
+// A lane holds four states of two neighbouring channels, the N/4 lanes of a channel pair
+// lie side by side: sums over the states are lane exchanges within the group, sums
+// over the channels (dB, dC) start within the lane and go on through LDS.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kRowRor8 = 0x128;
 template <int CTRL>
 __device__ __forceinline__ float moved(float v) {
   return __uint_as_float(
       __builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xF, 0xF, false));
 }
-template <int CTRL>
-__device__ __forceinline__ float merge_dpp(float a, float b, bool upper) {
-  return (upper ? b : a) + moved<CTRL>(upper ? a : b);
-}
 
-// Sums of M (8 or 16) values, taken in one by one: in the end `sum` holds, in the lanes whose
-// bits 5, 4, 3 (and 2) are n's bits 0, 1, 2 (and 3), value n's sum over the lanes that
-// differ in those bits.
-template <int M>
-struct LaneSums {
-  float l0, l1, l2, l3, sum;
-  __device__ __forceinline__ void add(int n, float v) {
-    const int lane = threadIdx.x;
-    if ((n & 1) == 0) {
-      l0 = v;
-      return;
-    }
-    v = merge32(l0, v);
-    if ((n & 2) == 0) {
-      l1 = v;
-      return;
-    }
-    v = merge16(l1, v);
-    if ((n & 4) == 0) {
-      l2 = v;
-      return;
-    }
-    v = merge_dpp<kRowRor8>(l2, v, lane & 8);
-    if (M == 8) {
-      sum = v;
-      return;
-    }
-    if ((n & 8) == 0) {
-      l3 = v;
-      return;
-    }
-    sum = merge_dpp<kHalfMirror>(l3, v, lane & 4);
+template <int N>
+struct Lanes {
+  static constexpr int L = N / 4;                        // lanes of a channel pair
+  static constexpr int kPairs = kWave / L;               // pairs of a wave
+  static constexpr int kChannels = 2 * kPairs;
+  static constexpr int kTurns = L < kMark ? L : kMark;   // lanes that share a block's tokens
+  static constexpr int kOwn = kMark / kTurns;            // tokens of a lane, kTurns apart
+
+  // The sum over a pair's lanes, in each of them.
+  static __device__ __forceinline__ float sum(float v) {
+    v += moved<kXor1>(v);
+    if (L >= 4) v += moved<kXor2>(v);
+    if (L >= 8) v += moved<kHalfMirror>(v);
+    if (L >= 16) v += moved<kRowRor8>(v);
+    return v;
+  }
+  // The value of the pair's lane `from`.
+  template <int FROM>
+  static __device__ __forceinline__ float bcast(float v) {
+    if constexpr (L == 2) return moved<FROM * 0x55 + 0xA0>(v);          // (f, f, 2+f, 2+f)
+    if constexpr (L == 4) return moved<FROM * 0x55>(v);
+    return __shfl(v, (threadIdx.x & (kWave - 1) & ~(L - 1)) + FROM, kWave);
   }
 };
 
-// The sums over all lanes of dB's and dC's M values, from what LaneSums has of each: a
-// lane holds that of value value_of(lane).
-template <int M>
-__device__ __forceinline__ float lane_total(float dB, float dC) {
-  const int lane = threadIdx.x;
-  if constexpr (M == 16) {
-    const float v = merge_dpp<kQuadXor2>(dB, dC, lane & 2);
-    return v + moved<kQuadXor1>(v);
-  } else {
-    float v = merge_dpp<kHalfMirror>(dB, dC, lane & 4);
-    v += moved<kQuadXor2>(v);
-    return v + moved<kQuadXor1>(v);
+// One element of two neighbouring channels, as it lies in memory.
+template <bool BF16>
+struct Pair;
+template <>
+struct Pair<true> {
+  uint32_t w;
+  __device__ __forceinline__ void load(const char* row, uint32_t a, uint32_t b) {
+    w = (uint32_t) * (const uint16_t*)(row + a) | (uint32_t) * (const uint16_t*)(row + b) << 16;
   }
-}
-// Which of the 2 M values (dB's first) a lane holds.
-template <int M>
-__device__ __forceinline__ int value_of(int lane) {
-  const int n = (lane >> 5 & 1) | (lane >> 4 & 1) << 1 | (lane >> 3 & 1) << 2;
-  return M == 16 ? n | (lane >> 2 & 1) << 3 | (lane >> 1 & 1) << 4 : n | (lane >> 2 & 1) << 3;
+  __device__ __forceinline__ float get(int c) const { return c ? bf16_hi(w) : bf16_lo(w); }
+};
+template <>
+struct Pair<false> {
+  float v[2];
+  __device__ __forceinline__ void load(const char* row, uint32_t a, uint32_t b) {
+    v[0] = *(const float*)(row + a);
+    v[1] = *(const float*)(row + b);
+  }
+  __device__ __forceinline__ float get(int c) const { return v[c]; }
+};
+
+// LDS writes of a wave's lanes before it are seen by their reads behind it (a wave's LDS
+// operations keep their order; this keeps the compiler's).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The second walk, down the tokens.  A wave holds NS of the N states of 64 channels;
-// SL = N / NS waves share the channels, and the waves of a workgroup add up
-// what dB and dC get from their channels.
-template <int NS, int SL, bool BF16>
-__global__ __launch_bounds__(kWave * kWaves) void scan_bwd_kernel(const BwdArgs b) {
-  constexpr int N = NS * SL;
-  constexpr int kMaxChannels = kWaves / SL;     // channel blocks of a workgroup
-  __shared__ float bc[2][kMaxChannels][SL][kMark][2 * NS];
-  // of several slices: their parts of x's and the time step's gradients, and of u
-  __shared__ float parts[SL > 1 ? kMaxChannels : 1][SL > 1 ? SL : 1][SL > 1 ? kMark : 1][3]
-                        [SL > 1 ? kWave : 1];
-  __shared__ float start[kWaves][NS][kWave];
+constexpr int kBatch = 4;      // tokens whose dB and dC are summed over a wave's lanes at once
+
+template <int N, bool BF16>
+__global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdArgs b) {
+  using La = Lanes<N>;
+  constexpr int L = La::L, OWN = La::kOwn, TURNS = La::kTurns;
+  constexpr int el = BF16 ? 2 : 4;
+  __shared__ f32x4 bc_in[2][kMark][2][L];                 // B and C of a block
+  __shared__ f32x4 values[kWaves][kBatch][2][kWave];      // dB and dC of each lane
+  __shared__ f32x4 sums[2][kWaves][kMark][2][L];          // and of each wave
+  __shared__ f32x4 start[kWaves][2][kWave];               // the state at the run's start
 
   const ScanArgs& a = b.f;
-  const int waves = (int)blockDim.x / kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int slice = wave % SL, cw = wave / SL, nchan = waves / SL;
-  const int lane = threadIdx.x % kWave;
-  // the workgroup's block of nchan * 64 channels, and the wave's 64 of them
-  const int wide = (a.group_dim + nchan * kWave - 1) / (nchan * kWave);
+  const int lane = threadIdx.x % kWave, q = lane % L;
+  const int wide = (a.group_dim + La::kChannels * kWaves - 1) / (La::kChannels * kWaves);
   const int64_t per_slot = a.ngroups * wide;
   const int64_t slot = blockIdx.x / per_slot;
   const int rest = (int)(blockIdx.x % per_slot);
   const int group = rest / wide, block = rest % wide;
-  const int at = (block * nchan + cw) * kWave;
-  const int lanes = a.group_dim - at < kWave ? a.group_dim - at : kWave;   // may be <= 0
-  const bool mine = lane < lanes;
-  const int own = mine ? lane : (lanes > 0 ? lanes - 1 : 0);
-  ScanPlace pl(a, 0, 1);
-  pl.slot = slot;
-  pl.group = group;
-  pl.channel = (int64_t)group * a.group_dim + (lanes > 0 ? at : 0);
-  pl.lanes = lanes;
-  const int64_t d = pl.channel + own;
-  const int n0 = slice * NS;
+  // the lane's channels; past the group's end they stand for nothing (zeros), and read the
+  // last one's rows
+  const int at = (block * kWaves + wave) * La::kChannels + lane / L * 2;
+  const bool on[2] = {at < a.group_dim, at + 1 < a.group_dim};
+  const int64_t base = (int64_t)group * a.group_dim;
+  const int64_t d[2] = {base + (on[0] ? at : a.group_dim - 1),
+                        base + (on[1] ? at + 1 : a.group_dim - 1)};
 
-  float* dA_row = b.dA_part + slot * (N + 2) * a.dim + d;
   const Run r = find_run(a.runs, slot);
+  float* dA_row = b.dA_part + slot * (N + 2) * a.dim;
   if (!r.on || r.begin >= r.end) {
-    if (mine) {
 #pragma unroll
-      for (int n = 0; n < NS; ++n) dA_row[(n0 + n) * a.dim] = 0.0f;
-      if (slice == 0) dA_row[N * a.dim] = dA_row[(N + 1) * a.dim] = 0.0f;
+    for (int c = 0; c < 2; ++c) {
+      if (!on[c]) continue;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) dA_row[(4 * q + n) * a.dim + d[c]] = 0.0f;
+      if (q == 0) dA_row[N * a.dim + d[c]] = dA_row[(N + 1) * a.dim + d[c]] = 0.0f;
       // an empty sequence passes its final state's gradient on
       if (r.on && b.out.dinit != nullptr) {
-        float v[NS];
-#pragma unroll
-        for (int n = 0; n < NS; ++n) v[n] = 0.0f;
-        if (b.dfinal) load_states<NS>(b.dfinal + (r.seq * a.dim + d) * N + n0, v);
-        store_states<NS>(b.out.dinit + (r.seq * a.dim + d) * N + n0, v);
+        const int64_t i = (r.seq * a.dim + d[c]) * N + 4 * q;
+        *(f32x4*)(b.out.dinit + i) =
+            b.dfinal ? *(const f32x4*)(b.dfinal + i) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
       }
     }
     return;
   }
 
-  float A2[NS], R[NS], dA[NS];
-  load_states<NS>(a.in.A + d * N + n0, A2);
+  float A2[2][4], R[2][4], dA[2][4];
+  float bias[2], skip[2];
 #pragma unroll
-  for (int n = 0; n < NS; ++n) {
-    A2[n] *= kLog2e;
-    R[n] = 0.0f;
-    dA[n] = 0.0f;
-  }
-  // the state at the run's start
-  {
-    float h[NS];
+  for (int c = 0; c < 2; ++c) {
+    const f32x4 A = *(const f32x4*)(a.in.A + d[c] * N + 4 * q);
+    f32x4 h = {0.0f, 0.0f, 0.0f, 0.0f}, back = h;
+    const int64_t state = (r.seq * a.dim + d[c]) * N + 4 * q;
 #pragma unroll
-    for (int n = 0; n < NS; ++n) h[n] = 0.0f;
+    for (int n = 0; n < 4; ++n) {
+      A2[c][n] = A[n] * kLog2e;
+      dA[c][n] = 0.0f;
+    }
+    // the state at the run's start, and the gradient of the state at its end
     if (r.index == 0) {
-      if (a.init != nullptr) load_states<NS>(a.init + (r.seq * a.dim + d) * N + n0, h);
+      if (a.init != nullptr) h = *(const f32x4*)(a.init + state);
     } else {
       for (int64_t s = r.first; s < slot; ++s) {
-        const float total = a.totals[s * a.dim + d];
+        const float total = a.totals[s * a.dim + d[c]];
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          const float left = a.states[(s * N + n0 + n) * a.dim + d];
-          h[n] = s == r.first ? left : __builtin_fmaf(exp2_hw(total * A2[n]), h[n], left);
+        for (int n = 0; n < 4; ++n) {
+          const float left = a.states[(s * N + 4 * q + n) * a.dim + d[c]];
+          h[n] = s == r.first ? left : __builtin_fmaf(exp2_hw(total * A2[c][n]), h[n], left);
         }
       }
     }
+    if (b.dfinal != nullptr) back = *(const f32x4*)(b.dfinal + state);
+    for (int64_t s = r.first + r.count - 1; s > slot; --s) {
+      const float total = a.totals[s * a.dim + d[c]];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) start[wave][n][lane] = h[n];
-  }
-  // the gradient of the state at its end
-  if (b.dfinal != nullptr) load_states<NS>(b.dfinal + (r.seq * a.dim + d) * N + n0, R);
-  for (int64_t s = r.first + r.count - 1; s > slot; --s) {
-    const float total = a.totals[s * a.dim + d];
+      for (int n = 0; n < 4; ++n)
+        back[n] = __builtin_fmaf(exp2_hw(total * A2[c][n]), back[n],
+                                 b.back[(s * N + 4 * q + n) * a.dim + d[c]]);
+    }
+    start[wave][c][lane] = on[c] ? h : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-      R[n] = __builtin_fmaf(exp2_hw(total * A2[n]), R[n],
-                            b.back[(s * N + n0 + n) * a.dim + d]);
+    for (int n = 0; n < 4; ++n) R[c][n] = on[c] ? back[n] : 0.0f;
+    bias[c] = a.in.dt_bias ? a.in.dt_bias[d[c]] : 0.0f;
+    skip[c] = a.in.D ? a.in.D[d[c]] : 0.0f;
   }
 
-  const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
-  const float skip = a.in.D ? a.in.D[d] : 0.0f;
   const bool gated = a.in.z != nullptr;
-  const Rows<BF16> rows(a, pl, own, N);
-  constexpr int el = BF16 ? 2 : 4;
+  const uint32_t off[2] = {(uint32_t)(d[0] - base) * el, (uint32_t)(d[1] - base) * el};
+  const char* x_row = (const char*)a.in.x + base * el;
+  const char* dt_row = (const char*)a.in.dt + base * el;
+  const char* z_row = (const char*)a.in.z + base * el;
+  const char* dy_row = (const char*)b.dy + base * el;
+  const int64_t x_step = a.x_stride * el, dt_step = a.dt_stride * el, z_step = a.z_stride * el;
   const int64_t out_step = a.dim * el;
-  const char* dy = (const char*)b.dy + pl.channel * el;
-  char* dx_out = (char*)b.out.dx + pl.channel * el;
-  char* ddt_out = (char*)b.out.ddt + pl.channel * el;
-  char* dz_out = gated ? (char*)b.out.dz + pl.channel * el : nullptr;
-  float dD = 0.0f, dbias = 0.0f;
-  int turn = 0;
+  const char* B_row = (const char*)a.in.B + (int64_t)group * N * el;
+  const char* C_row = (const char*)a.in.C + (int64_t)group * N * el;
+  const int64_t b_step = a.b_stride * el, c_step = a.c_stride * el;
 
-  const int64_t blocks = (r.end - r.begin + kMark - 1) / kMark;
+  const int blocks = (int)((r.end - r.begin + kMark - 1) / kMark);
   const int64_t mark0 = first_mark(r, slot);
-  for (int64_t m = blocks - 1; m >= 0; --m, turn ^= 1) {
-    const int64_t t0 = r.begin + m * kMark;
+  float dD[2] = {0.0f, 0.0f}, dbias[2] = {0.0f, 0.0f};
+
+  // what a block reads: its tokens' rows, B and C, and the state at its start
+  Pair<BF16> x[OWN], raw[OWN], z[OWN], g[OWN];
+  constexpr int kBC = 2 * N * kMark / (kWave * kWaves);     // values of B and C a thread
+  float bc[kBC > 0 ? kBC : 1];
+  float mark[2][4], mark_total[2];
+  auto load = [&](int m) {
+    const int64_t t0 = r.begin + (int64_t)m * kMark;
     const int count = r.end - t0 < kMark ? (int)(r.end - t0) : kMark;
-    float x[kMark], raw[kMark], z[kMark], g[kMark], delta[kMark];
 #pragma unroll
-    for (int j = 0; j < kMark; ++j) {
+    for (int i = 0; i < OWN; ++i) {
+      const int j = i * TURNS + q % TURNS;
       const int64_t t = t0 + (j < count ? j : count - 1);
-      x[j] = load_one<BF16>(rows.x + t * rows.x_step, own);
-      raw[j] = load_one<BF16>(rows.dt + t * rows.dt_step, own);
-      g[j] = load_one<BF16>(dy + t * out_step, own);
-      z[j] = gated ? load_one<BF16>(rows.z + t * rows.z_step, own) : 0.0f;
+      x[i].load(x_row + t * x_step, off[0], off[1]);
+      raw[i].load(dt_row + t * dt_step, off[0], off[1]);
+      g[i].load(dy_row + t * out_step, off[0], off[1]);
+      if (gated) z[i].load(z_row + t * z_step, off[0], off[1]);
     }
-    float h[kMark + 1][NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) h[0][n] = start[wave][n][lane];
+    for (int i = 0; i < (kBC > 0 ? kBC : 1); ++i) {
+      const int v = (int)threadIdx.x + i * kWave * kWaves;
+      const int j = v / (2 * N), k = v % (2 * N);
+      if (j < count)
+        bc[i] = k < N ? load_one<BF16>(B_row + (t0 + j) * b_step, k)
+                      : load_one<BF16>(C_row + (t0 + j) * c_step, k - N);
+    }
     if (m > 0) {
-      // the first run's marks include the initial state
-      const float total = b.mark_totals[(mark0 + m) * a.dim + d];
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const float part = b.marks[((mark0 + m) * N + n0 + n) * a.dim + d];
-        h[0][n] = r.index == 0 ? part : __builtin_fmaf(exp2_hw(total * A2[n]), h[0][n], part);
+      for (int c = 0; c < 2; ++c) {
+        mark_total[c] = b.mark_totals[(mark0 + m) * a.dim + d[c]];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          mark[c][n] = b.marks[((mark0 + m) * N + 4 * q + n) * a.dim + d[c]];
       }
     }
-    float u[kMark], du[kMark];
+  };
+  auto stage = [&](int turn) {
 #pragma unroll
-    for (int j = 0; j < kMark; ++j) {
-      u[j] = 0.0f;
-      if (j >= count) break;
-      const States<NS, BF16> B(rows.B, (t0 + j) * rows.b_step + n0 * el);
-      const float v = raw[j] + bias;
-      delta[j] = a.softplus ? softplus_f(v) : v;
-      const float dx = delta[j] * x[j];
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-        h[j + 1][n] = __builtin_fmaf(exp2_hw(delta[j] * A2[n]), h[j][n], dx * B[n]);
-      du[j] = g[j];
-      if (gated) {
-        const States<NS, BF16> C(rows.C, (t0 + j) * rows.c_step + n0 * el);
-#pragma unroll
-        for (int n = 0; n < NS; ++n) u[j] = __builtin_fmaf(C[n], h[j + 1][n], u[j]);
-        du[j] = g[j] * z[j] * sigmoid_f(z[j]);
-      }
+    for (int i = 0; i < (kBC > 0 ? kBC : 1); ++i) {
+      const int v = (int)threadIdx.x + i * kWave * kWaves;
+      if (v < 2 * N * kMark) ((float*)bc_in[turn])[v] = bc[i];
     }
-    float inner[kMark], ddelta[kMark];
+  };
+
+  load(blocks - 1);
+  stage(0);
+  __syncthreads();
+  int turn = 0;
+  for (int m = blocks - 1; m >= 0; --m, turn ^= 1) {
+    const int64_t t0 = r.begin + (int64_t)m * kMark;
+    const int count = r.end - t0 < kMark ? (int)(r.end - t0) : kMark;
+    // the time steps and gradients of the lane's own tokens
+    Pair<BF16> xo[OWN], rawo[OWN], zo[OWN], go[OWN];
+    float delta[OWN][2], dx[OWN][2], du[OWN][2];
 #pragma unroll
-    for (int j = kMark - 1; j >= 0; --j) {
-      if (j < count) {
-        const States<NS, BF16> B(rows.B, (t0 + j) * rows.b_step + n0 * el);
-        const States<NS, BF16> C(rows.C, (t0 + j) * rows.c_step + n0 * el);
-        const float dx = mine ? delta[j] * x[j] : 0.0f;
-        const float gj = mine ? du[j] : 0.0f;
-        LaneSums<NS> sB, sC;
-        inner[j] = ddelta[j] = 0.0f;
+    for (int i = 0; i < OWN; ++i) {
+      xo[i] = x[i];
+      rawo[i] = raw[i];
+      zo[i] = z[i];
+      go[i] = g[i];
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          const float dh = __builtin_fmaf(C[n], du[j], R[n]);
-          sC.add(n, gj * h[j + 1][n]);
-          sB.add(n, dx * dh);
-          inner[j] = __builtin_fmaf(B[n], dh, inner[j]);
-          R[n] = dh * exp2_hw(delta[j] * A2[n]);
-          const float kept = R[n] * h[j][n];
-          ddelta[j] = __builtin_fmaf(kept, A2[n], ddelta[j]);
-          dA[n] = __builtin_fmaf(kept, delta[j], dA[n]);
+      for (int c = 0; c < 2; ++c) {
+        const float v = rawo[i].get(c) + bias[c];
+        delta[i][c] = a.softplus ? softplus_f(v) : v;
+        dx[i][c] = on[c] ? delta[i][c] * xo[i].get(c) : 0.0f;
+        du[i][c] = go[i].get(c);
+        if (gated) {
+          const float zz = zo[i].get(c);
+          du[i][c] *= zz * sigmoid_f(zz);
         }
-        const float v = lane_total<NS>(sB.sum, sC.sum);
-        bc[turn][cw][slice][j][value_of<NS>(lane)] = v;
+        if (!on[c]) du[i][c] = 0.0f;
       }
     }
-    if constexpr (SL > 1) {
+    float h[kMark + 1][2][4];
 #pragma unroll
-      for (int j = 0; j < kMark; ++j) {
-        if (j < count) {
-          parts[cw][slice][j][0][lane] = inner[j];
-          parts[cw][slice][j][1][lane] = ddelta[j];
-          parts[cw][slice][j][2][lane] = u[j];
+    for (int c = 0; c < 2; ++c) {
+      const f32x4 s = start[wave][c][lane];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        h[0][c][n] = s[n];
+        // (the first run's marks include the initial state)
+        if (m > 0)
+          h[0][c][n] = r.index == 0 ? mark[c][n]
+                                    : __builtin_fmaf(exp2_hw(mark_total[c] * A2[c][n]), s[n],
+                                                     mark[c][n]);
+        if (!on[c]) h[0][c][n] = 0.0f;
+      }
+    }
+    if (m > 0) load(m - 1);
+
+    auto up = [&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      if (j >= count) return;
+      const f32x4 B = bc_in[turn][j][0][q];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float dl = La::template bcast<j % TURNS>(delta[j / TURNS][c]);
+        const float dxj = La::template bcast<j % TURNS>(dx[j / TURNS][c]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          h[j + 1][c][n] = __builtin_fmaf(exp2_hw(dl * A2[c][n]), h[j][c][n], dxj * B[n]);
+      }
+    };
+    float inner[OWN][2], ddelta[OWN][2], u[OWN][2];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) inner[i][c] = ddelta[i][c] = u[i][c] = 0.0f;
+    auto down = [&](auto jj) {
+      constexpr int j = decltype(jj)::value, i = j / TURNS;
+      if (j >= count) return;
+      const f32x4 B = bc_in[turn][j][0][q], C = bc_in[turn][j][1][q];
+      f32x4 vB, vC;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float dl = La::template bcast<j % TURNS>(delta[i][c]);
+        const float dxj = La::template bcast<j % TURNS>(dx[i][c]);
+        const float duj = La::template bcast<j % TURNS>(du[i][c]);
+        float in = 0.0f, dd = 0.0f, uu = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float dh = __builtin_fmaf(C[n], duj, R[c][n]);
+          vC[n] = c ? __builtin_fmaf(duj, h[j + 1][c][n], vC[n]) : duj * h[j + 1][c][n];
+          vB[n] = c ? __builtin_fmaf(dxj, dh, vB[n]) : dxj * dh;
+          in = __builtin_fmaf(B[n], dh, in);
+          uu = __builtin_fmaf(C[n], h[j + 1][c][n], uu);
+          R[c][n] = dh * exp2_hw(dl * A2[c][n]);
+          const float kept = R[c][n] * h[j][c][n];
+          dd = __builtin_fmaf(kept, A2[c][n], dd);
+          dA[c][n] = __builtin_fmaf(kept, dl, dA[c][n]);
+        }
+        in = La::sum(in);
+        dd = La::sum(dd);
+        if (gated) uu = La::sum(uu);
+        const bool own = q % TURNS == j % TURNS;
+        inner[i][c] = own ? in : inner[i][c];
+        ddelta[i][c] = own ? dd : ddelta[i][c];
+        u[i][c] = own ? uu : u[i][c];
+      }
+      values[wave][j % kBatch][0][lane] = vB;
+      values[wave][j % kBatch][1][lane] = vC;
+    };
+    // The sums of a batch's dB and dC over the wave's pairs: 8 L of them (token, half, lane
+    // of the pair), of kPairs vectors each, are shared by the 64 lanes, eight vectors a lane.
+    auto batch = [&](int j0) {
+      if (j0 >= count) return;
+      constexpr int kTasks = 2 * kBatch * L;
+      constexpr int kParts = kTasks < kWave ? kWave / kTasks : 1;   // lanes of a sum
+      constexpr int kRounds = kTasks > kWave ? kTasks / kWave : 1;
+      constexpr int kEach = La::kPairs / kParts;
+      wave_sync();
+#pragma unroll
+      for (int round = 0; round < kRounds; ++round) {
+        const int part = lane % kParts, task = lane / kParts + round * kWave;
+        const int k = task % L, half = task / L % 2, j = task / (2 * L);
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kEach; ++s) {
+          const int p = part * kEach + (s + j) % kEach;     // (spread over the banks)
+          sum += values[wave][j][half][p * L + k];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (kParts >= 2) sum[e] += moved<kXor1>(sum[e]);
+          if (kParts >= 4) sum[e] += moved<kXor2>(sum[e]);
+        }
+        if (part == 0 && j0 + j < count) sums[turn][wave][j0 + j][half][k] = sum;
+      }
+      wave_sync();
+    };
+    up(std::integral_constant<int, 0>{});
+    up(std::integral_constant<int, 1>{});
+    up(std::integral_constant<int, 2>{});
+    up(std::integral_constant<int, 3>{});
+    up(std::integral_constant<int, 4>{});
+    up(std::integral_constant<int, 5>{});
+    up(std::integral_constant<int, 6>{});
+    up(std::integral_constant<int, 7>{});
+    down(std::integral_constant<int, 7>{});
+    down(std::integral_constant<int, 6>{});
+    down(std::integral_constant<int, 5>{});
+    down(std::integral_constant<int, 4>{});
+    batch(4);
+    down(std::integral_constant<int, 3>{});
+    down(std::integral_constant<int, 2>{});
+    down(std::integral_constant<int, 1>{});
+    down(std::integral_constant<int, 0>{});
+    batch(0);
+
+    // the lane's own tokens
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      const int j = i * TURNS + q;
+      if (q >= TURNS || j >= count) continue;
+      const int64_t t = t0 + j;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float xx = xo[i].get(c);
+        float ddt = __builtin_fmaf(ddelta[i][c], kLn2, inner[i][c] * xx);
+        if (a.softplus) ddt *= sigmoid_f(rawo[i].get(c) + bias[c]);
+        dbias[c] += ddt;
+        dD[c] = __builtin_fmaf(du[i][c], xx, dD[c]);
+        if (!on[c]) continue;
+        const int64_t row = t * out_step + base * el;
+        store_one<BF16>((char*)b.out.dx + row + off[c], 0,
+                        __builtin_fmaf(inner[i][c], delta[i][c], skip[c] * du[i][c]));
+        store_one<BF16>((char*)b.out.ddt + row + off[c], 0, ddt);
+        if (gated) {
+          const float zz = zo[i].get(c), sig = sigmoid_f(zz);
+          const float slope = sig * __builtin_fmaf(zz, 1.0f - sig, 1.0f);
+          store_one<BF16>((char*)b.out.dz + row + off[c], 0,
+                          go[i].get(c) * __builtin_fmaf(skip[c], xx, u[i][c]) * slope);
         }
       }
     }
+    if (m > 0) stage(turn ^ 1);
     __syncthreads();
     // dB and dC of this block of channels
-    for (int i = threadIdx.x; i < count * SL * 2 * NS; i += (int)blockDim.x) {
-      const int v = i % (2 * NS), s = i / (2 * NS) % SL, j = i / (2 * NS * SL);
-      float sum = 0.0f;
-      for (int c = 0; c < nchan; ++c) sum += bc[turn][c][s][j][v];
+    for (int i = threadIdx.x; i < count * 2 * L; i += kWave * kWaves) {
+      const int k = i % L, half = i / L % 2, j = i / (2 * L);
+      f32x4 sum = sums[turn][0][j][half][k];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += sums[turn][w][j][half][k];
       const int64_t row = ((int64_t)block * a.runs.tokens + t0 + j) * a.ngroups + group;
-      b.bc_part[(row * 2 + v / NS) * N + s * NS + v % NS] = sum;
-    }
-#pragma unroll
-    for (int j = 0; j < kMark; ++j) {
-      if (j < count && j % SL == slice) {
-        float in = inner[j], dd = ddelta[j], uj = u[j];
-        if constexpr (SL > 1) {
-          in = dd = uj = 0.0f;
-#pragma unroll
-          for (int s = 0; s < SL; ++s) {
-            in += parts[cw][s][j][0][lane];
-            dd += parts[cw][s][j][1][lane];
-            uj += parts[cw][s][j][2][lane];
-          }
-        }
-        const int64_t t = t0 + j;
-        const float v = raw[j] + bias;
-        float ddt = __builtin_fmaf(dd, kLn2, in * x[j]);
-        if (a.softplus) ddt *= sigmoid_f(v);
-        dbias += ddt;
-        dD = __builtin_fmaf(du[j], x[j], dD);
-        if (mine) {
-          store_one<BF16>(dx_out + t * out_step, lane, __builtin_fmaf(in, delta[j], skip * du[j]));
-          store_one<BF16>(ddt_out + t * out_step, lane, ddt);
-          if (gated) {
-            const float sig = sigmoid_f(z[j]);
-            const float slope = sig * __builtin_fmaf(z[j], 1.0f - sig, 1.0f);
-            store_one<BF16>(dz_out + t * out_step, lane,
-                            g[j] * __builtin_fmaf(skip, x[j], uj) * slope);
-          }
-        }
-      }
-    }
-    if constexpr (SL > 1) __syncthreads();    // (parts are written again)
-  }
-  // sums over the tokens; of several slices each has some of the tokens
-  if constexpr (SL > 1) {
-    parts[cw][slice][0][0][lane] = dD;
-    parts[cw][slice][0][1][lane] = dbias;
-    __syncthreads();
-    dD = dbias = 0.0f;
-#pragma unroll
-    for (int s = 0; s < SL; ++s) {
-      dD += parts[cw][s][0][0][lane];
-      dbias += parts[cw][s][0][1][lane];
+      *(f32x4*)(b.bc_part + (row * 2 + half) * N + 4 * k) = sum;
     }
   }
-  if (!mine) return;
 #pragma unroll
-  for (int n = 0; n < NS; ++n) dA_row[(n0 + n) * a.dim] = dA[n];
-  if (slice == 0) {
-    dA_row[N * a.dim] = dD;
-    dA_row[(N + 1) * a.dim] = dbias;
+  for (int c = 0; c < 2; ++c) {
+    const float sD = La::sum(dD[c]), sb = La::sum(dbias[c]);
+    if (!on[c]) continue;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) dA_row[(4 * q + n) * a.dim + d[c]] = dA[c][n];
+    if (q == 0) {
+      dA_row[N * a.dim + d[c]] = sD;
+      dA_row[(N + 1) * a.dim + d[c]] = sb;
+    }
+    if (r.index == 0 && b.out.dinit != nullptr)
+      *(f32x4*)(b.out.dinit + (r.seq * a.dim + d[c]) * N + 4 * q) =
+          (f32x4){R[c][0], R[c][1], R[c][2], R[c][3]};
   }
-  if (r.index == 0 && b.out.dinit != nullptr)
-    store_states<NS>(b.out.dinit + (r.seq * a.dim + d) * N + n0, R);
 }
 
 // dB and dC: the sums over the blocks of a group's channels.
@@ -489,19 +569,10 @@ int64_t run_length(const ScanShape& s) {
 int64_t most_slots(const ScanShape& s) { return s.tokens / run_length(s) + s.nseq; }
 int64_t most_marks(const ScanShape& s) { return s.tokens / kMark + most_slots(s) + 1; }
 
-// Waves of a workgroup of the second walk: N / 16 for each of up to 64 * (4 / slices)
-// channels of a group.
-struct Wide {
-  int slices, channels, blocks;
-};
-Wide wide_of(const ScanShape& s) {
-  Wide w;
-  w.slices = s.n <= 16 ? 1 : (int)(s.n / 16);
-  const int64_t blocks = (s.dim / s.ngroups + kWave - 1) / kWave;
-  const int most = kWaves / w.slices;
-  w.channels = (int)(blocks < most ? blocks : most);
-  w.blocks = (int)((blocks + w.channels - 1) / w.channels);
-  return w;
+// Blocks of a group's channels that the second walk's workgroups take.
+int64_t wide_blocks(const ScanShape& s) {
+  const int64_t channels = kWaves * (512 / s.n);
+  return (s.dim / s.ngroups + channels - 1) / channels;
 }
 
 size_t aligned(size_t n) { return (n + 15) & ~(size_t)15; }
@@ -525,25 +596,27 @@ BwdLayout layout(const ScanShape& s) {
   l.marks = take(marks * N * D);
   l.mark_totals = take(marks * D);
   l.dA = take(slots * (N + 2) * D);
-  l.bc = take((size_t)wide_of(s).blocks * (size_t)(s.tokens * s.ngroups) * 2 * N);
+  l.bc = take((size_t)wide_blocks(s) * (size_t)(s.tokens * s.ngroups) * 2 * N);
   l.all = at;
   return l;
 }
 
-template <int NS, int SL, bool BF16>
-void launch_n(const BwdArgs& b, const Wide& w, int64_t slots, int64_t blocks, hipStream_t st) {
-  hipLaunchKernelGGL((scan_local_kernel<NS * SL, BF16>), dim3((unsigned)(slots * blocks)),
+template <int N, bool BF16>
+void launch_n(const BwdArgs& b, int64_t blocks, int64_t wide, hipStream_t st) {
+  hipLaunchKernelGGL((scan_local_kernel<N, BF16>), dim3((unsigned)(b.slots * blocks)),
                      dim3(kWave), 0, st, b);
-  hipLaunchKernelGGL((scan_bwd_kernel<NS, SL, BF16>),
-                     dim3((unsigned)(slots * b.f.ngroups * w.blocks)),
-                     dim3(kWave * w.channels * w.slices), 0, st, b);
+  hipLaunchKernelGGL((scan_bwd_kernel<N, BF16>),
+                     dim3((unsigned)(b.slots * b.f.ngroups * wide)), dim3(kWave * kWaves), 0, st,
+                     b);
 }
 
 }  // namespace
 
 bool scan_bwd_fits(const ScanShape& s) {
   const int64_t rows = 2 * s.n * s.ngroups;
-  return most_slots(s) < kScanMaxBlocks / channel_blocks(s) &&
+  // (the second walk's workgroups have four waves of at least 8 channels each)
+  return most_slots(s) < kScanMaxBlocks / 4 / (s.ngroups * wide_blocks(s)) &&
+         most_slots(s) < kScanMaxBlocks / channel_blocks(s) &&
          s.tokens <= (kScanMaxBlocks / 4 - 1) * 256 / rows;
 }
 
@@ -570,31 +643,27 @@ int launch_scan_bwd(const ScanInputs& in, const float* init, const int32_t* cu, 
   b.dy = dy;
   b.dfinal = dfinal;
   b.out = out;
-  const Wide w = wide_of(s);
-  const int64_t blocks = channel_blocks(s);
+  const int64_t blocks = channel_blocks(s), wide = wide_blocks(s);
   hipStream_t st = (hipStream_t)stream;
   switch (s.n) {
-#define SSD_SCAN(N, NS, SL)                                        \
-  case N:                                                          \
-    if (bf16)                                                      \
-      launch_n<NS, SL, true>(b, w, b.slots, blocks, st);           \
-    else                                                           \
-      launch_n<NS, SL, false>(b, w, b.slots, blocks, st);          \
+#define SSD_SCAN(N)                                  \
+  case N:                                            \
+    bf16 ? launch_n<N, true>(b, blocks, wide, st) : launch_n<N, false>(b, blocks, wide, st); \
     break
-    SSD_SCAN(8, 8, 1);
-    SSD_SCAN(16, 16, 1);
-    SSD_SCAN(32, 16, 2);
+    SSD_SCAN(8);
+    SSD_SCAN(16);
+    SSD_SCAN(32);
     default:
-      SSD_SCAN(64, 16, 4);
+      SSD_SCAN(64);
 #undef SSD_SCAN
   }
   const int64_t values = s.tokens * s.ngroups * 2 * s.n;
   const dim3 grid((unsigned)((values + 255) / 256));
   if (bf16)
-    hipLaunchKernelGGL((scan_sum_bc_kernel<true>), grid, dim3(256), 0, st, b, (int)s.n, w.blocks);
+    hipLaunchKernelGGL((scan_sum_bc_kernel<true>), grid, dim3(256), 0, st, b, (int)s.n, (int)wide);
   else
     hipLaunchKernelGGL((scan_sum_bc_kernel<false>), grid, dim3(256), 0, st, b, (int)s.n,
-                       w.blocks);
+                       (int)wide);
   hipLaunchKernelGGL(scan_sum_slots_kernel,
                      dim3((unsigned)((s.dim + kWave - 1) / kWave * (s.n + 2))), dim3(256), 0, st,
                      b, (int)s.n);
