@@ -79,30 +79,32 @@ __device__ __forceinline__ Run find_run(const RunGrid& g, int64_t slot) {
 
 __device__ __forceinline__ float rcp_hw(float v) { return __builtin_amdgcn_rcpf(v); }
 
-// 1 / (1 + exp(-v)), from exp(-|v|) so that nothing overflows.
+// 1 / (1 + exp(-v)); exp(-v) may overflow, to a result of 0 that is below 2^-127.
 __device__ __forceinline__ float sigmoid_f(float v) {
-  const float e = exp2_hw(-kLog2e * __builtin_fabsf(v)), r = rcp_hw(1.0f + e);
-  return v < 0.0f ? e * r : r;
+  return rcp_hw(1.0f + exp2_hw(-kLog2e * v));
 }
 
 // ln(1 + exp(v)) = max(v, 0) + ln(1 + e) with e = exp(-|v|), and
-// ln(1 + e) = 2 artanh(s) = 2 (s + s^3/3 + s^5/5 + ...) with s = e / (2 + e) <= 1/3:
-// good to a few roundings of the result for every v, also where it is small (1 + e
-// would lose e's digits).  Seven terms leave 2e-8 of it.
-__device__ __forceinline__ float softplus_of(float v, float e) {
+// ln(1 + e) = 2 artanh(s) with s = e / (2 + e) <= 1/3: good to a few roundings of the
+// result for every v, also where it is small (1 + e would lose e's digits).  The
+// polynomial is artanh(s) / s in s^2, fitted to 4e-9 of it by weighted least squares.
+__device__ __forceinline__ float softplus_f(float v) {
+  const float e = exp2_hw(-kLog2e * __builtin_fabsf(v));
   const float s = e * rcp_hw(2.0f + e), q = s * s;
-  float p = 1.0f / 13.0f;
-  p = __builtin_fmaf(p, q, 1.0f / 11.0f);
-  p = __builtin_fmaf(p, q, 1.0f / 9.0f);
-  p = __builtin_fmaf(p, q, 1.0f / 7.0f);
-  p = __builtin_fmaf(p, q, 0.2f);
-  p = __builtin_fmaf(p, q, 1.0f / 3.0f);
+  float p = 0.14089166f;
+  p = __builtin_fmaf(p, q, 0.13980302f);
+  p = __builtin_fmaf(p, q, 0.20012455f);
+  p = __builtin_fmaf(p, q, 0.33333157f);
   p = __builtin_fmaf(p, q, 1.0f);
   // (a NaN comes through e)
   return __builtin_fmaf(s + s, p, __builtin_fmaxf(v, 0.0f));
 }
-__device__ __forceinline__ float softplus_f(float v) {
-  return softplus_of(v, exp2_hw(-kLog2e * __builtin_fabsf(v)));
+
+// `yes` where `on`, formed in any case: a branch for every token would cut the walks into
+// blocks, across which the compiler moves work to where it fills the registers.
+__device__ __forceinline__ float pick(bool on, float yes, float no) {
+  asm volatile("" : "+v"(yes));
+  return on ? yes : no;
 }
 
 // One element of an array of fp32 or bf16, and back (rounded once).

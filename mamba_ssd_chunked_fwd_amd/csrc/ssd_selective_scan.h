@@ -23,9 +23,10 @@ struct ScanArgs {
   int group_dim;       // channels of a group
   int group_blocks;    // blocks of 64 channels of a group
   int softplus;
-  // Of a split call, for each slot: the state that the run leaves [slots, N, dim]
-  // (the slot of a sequence's last run, whose state nobody asks for, holds the initial
-  // state instead, so that final_state may be init_state's buffer), and the sum of
+  int joined;          // whether scan_join_kernel has been through the states
+  // Of a split call, for each slot: the state that the run leaves [slots, N, dim] (in the
+  // forward call the slot of a sequence's last run, whose state nobody asks for, holds the
+  // initial state instead, so that final_state may be init_state's buffer), and the sum of
   // its time steps [slots, dim].
   float *states, *totals;
 };
@@ -85,12 +86,14 @@ __device__ __forceinline__ void store_states(float* p, const float (&v)[N]) {
 template <int N, bool BF16>
 struct States {
   static constexpr int kWords = BF16 ? N / 2 : N;
+  // short ones are read a token ahead; the others would not leave enough scalar registers
+  static constexpr bool kAhead = kWords <= 8;
   uint32_t w[kWords];
-  // p: the first token's; `at`: bytes to the token's
-  __device__ __forceinline__ States(const void* p, int64_t at) {
+  States() = default;
+  __device__ __forceinline__ explicit States(const void* p) {
     typedef uint32_t words __attribute__((ext_vector_type(4), aligned(4)));
     typedef const __attribute__((address_space(4))) words* scalar;
-    const scalar q = (scalar)(uintptr_t)((const char*)p + at);
+    const scalar q = (scalar)(uintptr_t)p;
 #pragma unroll
     for (int k = 0; k < kWords / 4; ++k) {
       const words v = q[k];
@@ -104,45 +107,88 @@ struct States {
   }
 };
 
-// Tokens read at a time, one such block ahead of the arithmetic.
-constexpr int kBlock = 4;
+// B and C (or B alone) of the tokens of a run, one after the other.
+template <int N, bool BF16, bool BOTH>
+struct StateRows {
+  typedef States<N, BF16> S;
+  const char *b, *c;
+  int64_t b_step, c_step;
+  int left;
+  S nb, nc;
+  __device__ __forceinline__ StateRows(const char* b_, const char* c_, int64_t bs, int64_t cs,
+                                       int tokens)
+      : b(b_), c(c_), b_step(bs), c_step(cs), left(tokens) {
+    if (S::kAhead && tokens > 0) read(nb, nc);
+  }
+  __device__ __forceinline__ void read(S& B, S& C) {
+    // (keeps the reads of many tokens from gathering and filling the scalar registers)
+    asm volatile("" : "+s"(b));
+    if (BOTH) asm volatile("" : "+s"(c));
+    B = S(b);
+    if (BOTH) C = S(c);
+    if (--left > 0) {       // (the row behind the last one need not exist)
+      b += b_step;
+      c += c_step;
+    }
+  }
+  __device__ __forceinline__ void next(S& B, S& C) {
+    if constexpr (S::kAhead) {
+      B = nb;
+      C = nc;
+      read(nb, nc);
+    } else {
+      read(B, C);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+};
 
-// The rows of a wave's inputs: uniform bases and a lane's place in them.
+// The rows of a wave's inputs from some token on: uniform pointers, which move from row to
+// row (multiples of the steps would fill the scalar registers), and the lane's place.
 template <bool BF16>
 struct Rows {
   const char *x, *dt, *z, *B, *C;
   int64_t x_step, dt_step, z_step, b_step, c_step;   // bytes between rows
   uint32_t lane;
-  __device__ __forceinline__ Rows(const ScanArgs& a, const ScanPlace& pl, uint32_t lane_, int n) {
+  __device__ __forceinline__ Rows(const ScanArgs& a, const ScanPlace& pl, int64_t t, int own,
+                                  int n) {
     constexpr int el = BF16 ? 2 : 4;
-    x = (const char*)a.in.x + pl.channel * el;
-    dt = (const char*)a.in.dt + pl.channel * el;
-    z = (const char*)a.in.z + pl.channel * el;
-    B = (const char*)a.in.B + (int64_t)pl.group * n * el;
-    C = (const char*)a.in.C + (int64_t)pl.group * n * el;
     x_step = a.x_stride * el;
     dt_step = a.dt_stride * el;
-    z_step = a.z_stride * el;
+    z_step = (a.in.z ? a.z_stride : a.x_stride) * el;
     b_step = a.b_stride * el;
     c_step = a.c_stride * el;
-    lane = lane_;
+    x = (const char*)a.in.x + pl.channel * el + t * x_step;
+    dt = (const char*)a.in.dt + pl.channel * el + t * dt_step;
+    // (without a gate rows of x are read in the place of z's, and not used)
+    z = (const char*)(a.in.z ? a.in.z : a.in.x) + pl.channel * el + t * z_step;
+    B = (const char*)a.in.B + (int64_t)pl.group * n * el + t * b_step;
+    C = (const char*)a.in.C + (int64_t)pl.group * n * el + t * c_step;
+    lane = (uint32_t)own * el;
   }
 };
 
-// The state at the start of a run: those that the runs before it leave, each decayed
-// by the runs between, from the first on.
-template <int N>
-__device__ __forceinline__ void fold_runs(const ScanArgs& a, int64_t first, int64_t slot,
-                                          int64_t d, const float (&A2)[N], float (&h)[N]) {
-  for (int64_t s = first; s < slot; ++s) {
-    const float total = a.totals[s * a.dim + d];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const float left = a.states[(s * N + n) * a.dim + d];
-      // (the first run's state includes the initial one)
-      h[n] = s == first ? left : __builtin_fmaf(exp2_hw(total * A2[n]), h[n], left);
-    }
-  }
+// The element `lane` bytes into a row, as it lies in memory, and as a float.
+template <bool BF16>
+struct Raw {
+  typedef uint16_t type;
+  static __device__ __forceinline__ float get(type v) { return __uint_as_float((uint32_t)v << 16); }
+};
+template <>
+struct Raw<false> {
+  typedef float type;
+  static __device__ __forceinline__ float get(type v) { return v; }
+};
+template <bool BF16>
+__device__ __forceinline__ typename Raw<BF16>::type load_raw(const char* row, uint32_t lane) {
+  return *(const typename Raw<BF16>::type*)(row + lane);
+}
+template <bool BF16>
+__device__ __forceinline__ void store_raw(char* row, uint32_t lane, float v) {
+  if constexpr (BF16)
+    *(uint16_t*)(row + lane) = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu);
+  else
+    *(float*)(row + lane) = v;
 }
 
 template <int N>
@@ -156,6 +202,37 @@ __device__ __forceinline__ void load_run(const ScanArgs& a, int64_t slot, int64_
                                          float (&h)[N]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) h[n] = a.states[(slot * N + n) * a.dim + d];
+}
+
+// ---- the states at the runs' starts
+// Few runs: each goes through those before it itself (no launch).  Many: a launch of their
+// own (scan_join_kernel) replaces what the runs leave by what they start from.
+constexpr int kFoldRuns = 12;      // runs that a sequence may have for the first form
+
+// The first form, for some of a channel's states: `left(s, n)` is what run s leaves of
+// state n (the first run's includes the initial state).
+template <int N, class Left>
+__device__ __forceinline__ void fold_runs(const ScanArgs& a, int64_t first, int64_t slot,
+                                          int64_t d, const float (&A2)[N], float (&h)[N],
+                                          Left left) {
+  for (int64_t s = first; s < slot; ++s) {
+    const float total = a.totals[s * a.dim + d];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float v = left(s, n);
+      h[n] = s == first ? v : __builtin_fmaf(exp2_hw(total * A2[n]), h[n], v);
+    }
+  }
+}
+
+// The second form's launch (in ssd_selective_scan.hip).  With `back` it also replaces the
+// gradients at the runs' starts by those at their ends.
+void launch_scan_join(const ScanArgs& a, int64_t n, float* back, const float* dfinal,
+                      hipStream_t st);
+
+// Whether a sequence may have so many runs that their states are joined by a launch.
+inline bool joins(const RunGrid& g) {
+  return g.cu != nullptr ? g.tokens / g.run > kFoldRuns : g.per_seq > kFoldRuns;
 }
 
 }  // namespace ssd

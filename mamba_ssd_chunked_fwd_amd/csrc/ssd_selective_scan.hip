@@ -7,23 +7,93 @@
 namespace ssd {
 namespace {
 
-template <bool BF16, bool OUT>
-struct TokenBlock {
-  float x[kBlock], dt[kBlock], z[kBlock];
-  __device__ __forceinline__ void load(const Rows<BF16>& r, int64_t t0, int64_t end, bool gated) {
+// The states at the starts of many runs: a lane owns one state of one channel and goes
+// through a sequence's runs, eight of them on the way at once; a workgroup has 64 channels and four of the N
+// states, and every gridDim.y'th sequence.  With `back` it also goes down, through the
+// gradients at the runs' starts.
+template <int N>
+__global__ __launch_bounds__(256) void scan_join_kernel(const ScanArgs a, float* back,
+                                                        const float* dfinal) {
+  const int lane = threadIdx.x % kWave;
+  const int blocks = (int)((a.dim + kWave - 1) / kWave);
+  const int n = (int)(blockIdx.x / blocks) * 4 + threadIdx.x / kWave;
+  const int64_t d = (int64_t)(blockIdx.x % blocks) * kWave + lane;
+  const bool on = d < a.dim;
+  const float A2 = on ? a.in.A[d * N + n] * kLog2e : 0.0f;
+  const RunGrid& g = a.runs;
+  constexpr int kAhead = 8;
+  // 64 sequences at a time: those that have more than one run
+  for (int64_t i0 = blockIdx.y; i0 < g.nseq; i0 += (int64_t)gridDim.y * kWave) {
+    const int64_t mine = i0 + (int64_t)gridDim.y * lane;
+    int64_t first = 0, count = 0;
+    if (mine < g.nseq) {
+      int64_t begin, end;
+      if (g.cu != nullptr) {
+        begin = seq_bound(g, mine);
+        end = seq_bound(g, mine + 1);
+        first = begin / g.run + mine;
+      } else {
+        begin = mine * (g.tokens / g.nseq);
+        end = begin + g.tokens / g.nseq;
+        first = mine * g.per_seq;
+      }
+      count = end > begin ? (end - begin + g.run - 1) / g.run : 0;
+    }
+    uint64_t many = __ballot(count > 1);
+    while (many != 0) {
+      const int k = __builtin_ctzll(many);
+      many &= many - 1;
+      const int64_t s0 = __shfl(first, k, kWave), runs = __shfl(count, k, kWave);
+      const int64_t seq = i0 + (int64_t)gridDim.y * k;
+      if (!on) continue;
+      float* state = a.states + (s0 * N + n) * a.dim + d;
+      const float* total = a.totals + s0 * a.dim + d;
+      const int64_t step = N * a.dim;
+      float h = a.init != nullptr ? a.init[(seq * a.dim + d) * N + n] : 0.0f;
+      for (int64_t s = 0; s < runs; s += kAhead) {
+        float left[kAhead], decay[kAhead];
 #pragma unroll
-    for (int j = 0; j < kBlock; ++j) {
-      const int64_t t = t0 + j < end ? t0 + j : end - 1;
-      x[j] = load_one<BF16>(r.x + t * r.x_step, r.lane);
-      dt[j] = load_one<BF16>(r.dt + t * r.dt_step, r.lane);
-      if (OUT) z[j] = gated ? load_one<BF16>(r.z + t * r.z_step, r.lane) : 0.0f;
+        for (int e = 0; e < kAhead; ++e) {
+          const int64_t at = s + e < runs ? s + e : runs - 1;
+          left[e] = state[at * step];
+          decay[e] = exp2_hw(total[at * a.dim] * A2);
+        }
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          if (s + e >= runs) break;
+          state[(s + e) * step] = h;
+          h = s + e == 0 ? left[e] : __builtin_fmaf(decay[e], h, left[e]);
+        }
+      }
+      if (back == nullptr) continue;
+      float* grad = back + (s0 * N + n) * a.dim + d;
+      float R = dfinal != nullptr ? dfinal[(seq * a.dim + d) * N + n] : 0.0f;
+      for (int64_t s = runs - 1; s >= 0; s -= kAhead) {
+        float left[kAhead], decay[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          const int64_t at = s - e > 0 ? s - e : 0;
+          left[e] = grad[at * step];
+          decay[e] = exp2_hw(total[at * a.dim] * A2);
+        }
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          if (s - e < 0) break;
+          grad[(s - e) * step] = R;
+          R = __builtin_fmaf(decay[e], R, left[e]);
+        }
+      }
     }
   }
-};
+}
+
+// Tokens read at a time; one such block is on the way while another is worked on.
+constexpr int kBlock = 4;
 
 // One run of one sequence for 64 channels of a group.
 //   OUT: outputs, from the state that the runs before it leave
 //   else: the state that the run leaves (from zeros, the first run from the initial state)
+// Lanes past the group's end do what its last channel's lane does, and store the same.
 template <int N, bool BF16, bool OUT>
 __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
   const ScanPlace pl(a);
@@ -31,9 +101,7 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
   if (!r.on) return;
   const bool last = r.index == r.count - 1;
   if (!OUT && last) return;
-  const int lane = threadIdx.x;
-  const bool mine = lane < pl.lanes;
-  const int own = mine ? lane : pl.lanes - 1;
+  const int own = (int)threadIdx.x < pl.lanes ? (int)threadIdx.x : pl.lanes - 1;
   const int64_t d = pl.channel + own;
 
   float A2[N], h[N];
@@ -42,46 +110,67 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
   for (int n = 0; n < N; ++n) A2[n] *= kLog2e;
 #pragma unroll
   for (int n = 0; n < N; ++n) h[n] = 0.0f;
-  if (r.index == 0 && a.init != nullptr) {
+  if (OUT && a.joined && r.count > 1) {
+    load_run<N>(a, pl.slot, d, h);
+  } else if (r.index == 0 && a.init != nullptr) {
     if (OUT && !last) {
       load_run<N>(a, r.first + r.count - 1, d, h);
     } else {
       load_states<N>(a.init + (r.seq * a.dim + d) * N, h);
-      if (!OUT && mine) store_run<N>(a, r.first + r.count - 1, d, h);
+      if (!OUT && !a.joined) store_run<N>(a, r.first + r.count - 1, d, h);
     }
+  } else if (OUT) {
+    fold_runs<N>(a, r.first, pl.slot, d, A2, h, [&](int64_t s, int n) {
+      return a.states[(s * N + n) * a.dim + d];
+    });
   }
-  if constexpr (OUT) fold_runs<N>(a, r.first, pl.slot, d, A2, h);
   const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
   const float skip = OUT && a.in.D ? a.in.D[d] : 0.0f;
   const bool gated = OUT && a.in.z != nullptr;
 
-  const Rows<BF16> rows(a, pl, own, N);
-  char* y = OUT ? (char*)a.y + pl.channel * (BF16 ? 2 : 4) : nullptr;
+  Rows<BF16> rows(a, pl, r.begin, own, N);
   const int64_t y_step = a.dim * (BF16 ? 2 : 4);
+  char* y = OUT ? (char*)a.y + pl.channel * (BF16 ? 2 : 4) + r.begin * y_step : nullptr;
+  const int tokens = (int)(r.end - r.begin);    // (fewer than 2^31)
+  StateRows<N, BF16, OUT> bc(rows.B, rows.C, rows.b_step, rows.c_step, tokens);
   double total = 0.0;
-  TokenBlock<BF16, OUT> next;
-  if (r.begin < r.end) next.load(rows, r.begin, r.end, gated);
-  for (int64_t t0 = r.begin; t0 < r.end; t0 += kBlock) {
-    const TokenBlock<BF16, OUT> cur = next;
-    next.load(rows, t0 + kBlock, r.end, gated);
+  typedef typename Raw<BF16>::type raw;
+  struct Block {
+    raw x[kBlock], dt[kBlock], z[kBlock];
+  };
+  // the next block's rows, `left` of them there (the others read the last one's)
+  auto load = [&](Block& b, int left) {
 #pragma unroll
     for (int j = 0; j < kBlock; ++j) {
-      if (t0 + j >= r.end) break;
-      const States<N, BF16> B(rows.B, (t0 + j) * rows.b_step);
-      const float v = cur.dt[j] + bias;
-      const float delta = a.softplus ? softplus_f(v) : v;
-      const float x = cur.x[j], dx = delta * x;
+      b.x[j] = load_raw<BF16>(rows.x, rows.lane);
+      b.dt[j] = load_raw<BF16>(rows.dt, rows.lane);
+      if (OUT) b.z[j] = load_raw<BF16>(rows.z, rows.lane);
+      if (j + 1 < left || left >= kBlock) {
+        rows.x += rows.x_step;
+        rows.dt += rows.dt_step;
+        rows.z += rows.z_step;
+      }
+    }
+  };
+  auto work = [&](const Block& b, int left) {
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      if (j >= left) break;
+      States<N, BF16> B, C;
+      bc.next(B, C);
+      const float v = Raw<BF16>::get(b.dt[j]) + bias;
+      const float delta = pick(a.softplus, softplus_f(v), v);
+      const float x = Raw<BF16>::get(b.x[j]), dx = delta * x;
       if constexpr (OUT) {
-        const States<N, BF16> C(rows.C, (t0 + j) * rows.c_step);
         float u[2] = {skip * x, 0.0f};
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           h[n] = __builtin_fmaf(exp2_hw(delta * A2[n]), h[n], dx * B[n]);
           u[n & 1] = __builtin_fmaf(C[n], h[n], u[n & 1]);
         }
-        float out = u[0] + u[1];
-        if (gated) out *= cur.z[j] * sigmoid_f(cur.z[j]);
-        if (mine) store_one<BF16>(y + (t0 + j) * y_step, lane, out);
+        const float z = Raw<BF16>::get(b.z[j]), out = u[0] + u[1];
+        store_raw<BF16>(y, rows.lane, pick(gated, out * (z * sigmoid_f(z)), out));
+        y += y_step;
       } else {
         total += delta;
 #pragma unroll
@@ -89,8 +178,20 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
           h[n] = __builtin_fmaf(exp2_hw(delta * A2[n]), h[n], dx * B[n]);
       }
     }
+  };
+  Block even, odd;
+  if (tokens > 0) load(even, tokens);
+  int t = 0;
+  for (; t + 3 * kBlock <= tokens; t += 2 * kBlock) {
+    load(odd, kBlock);
+    work(even, kBlock);
+    load(even, kBlock);
+    work(odd, kBlock);
   }
-  if (!mine) return;
+  for (; t < tokens; t += kBlock) {
+    work(even, tokens - t);
+    if (t + kBlock < tokens) load(even, tokens - t - kBlock);
+  }
   if constexpr (OUT) {
     if (last && a.fin != nullptr) store_states<N>(a.fin + (r.seq * a.dim + d) * N, h);
   } else {
@@ -106,7 +207,7 @@ int64_t run_length(const ScanShape& s) {
   const int64_t blocks = s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
   if (s.nseq * blocks >= 1024) return 4 * mean;
-  int64_t run = (s.tokens * blocks + 4095) / 4096;
+  int64_t run = (s.tokens * blocks + 8191) / 8192;
   run = (run + kBlock - 1) / kBlock * kBlock;
   return run < 32 ? 32 : run;
 }
@@ -129,16 +230,39 @@ ScanPlan make_plan(const ScanShape& s, const int32_t* cu) {
 // More slots than without cu, so that the workspace's size does not ask for it.
 int64_t most_slots(const ScanShape& s) { return s.tokens / run_length(s) + s.nseq; }
 
+template <int N>
+void join_n(const ScanArgs& a, float* back, const float* dfinal, hipStream_t st) {
+  const int64_t blocks = (a.dim + kWave - 1) / kWave * (N / 4);
+  const int64_t want = 2048 / blocks;
+  const int64_t across = want < 1 ? 1 : (want < a.runs.nseq ? want : a.runs.nseq);
+  hipLaunchKernelGGL((scan_join_kernel<N>), dim3((unsigned)blocks, (unsigned)across), dim3(256),
+                     0, st, a, back, dfinal);
+}
+
 template <int N, bool BF16>
 int launch_n(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
   const dim3 grid((unsigned)(p.slots * p.blocks));
-  if (p.split)
+  if (p.split) {
     hipLaunchKernelGGL((scan_kernel<N, BF16, false>), grid, dim3(kWave), 0, st, a);
+    if (a.joined) launch_scan_join(a, N, nullptr, nullptr, st);
+  }
   hipLaunchKernelGGL((scan_kernel<N, BF16, true>), grid, dim3(kWave), 0, st, a);
   return (int)hipGetLastError();
 }
 
 }  // namespace
+
+void launch_scan_join(const ScanArgs& a, int64_t n, float* back, const float* dfinal,
+                      hipStream_t st) {
+  if (n == 8)
+    join_n<8>(a, back, dfinal, st);
+  else if (n == 16)
+    join_n<16>(a, back, dfinal, st);
+  else if (n == 32)
+    join_n<32>(a, back, dfinal, st);
+  else
+    join_n<64>(a, back, dfinal, st);
+}
 
 bool scan_fits(const ScanShape& s) {
   const int64_t blocks = s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
@@ -159,6 +283,7 @@ int launch_scan_fwd(const ScanInputs& in, const float* init, const int32_t* cu, 
   a.y = y;
   a.fin = fin;
   a.runs = p.runs;
+  a.joined = joins(p.runs);
   a.states = (float*)ws;
   a.totals = (float*)ws + p.slots * s.dim * s.n;
   hipStream_t st = (hipStream_t)stream;

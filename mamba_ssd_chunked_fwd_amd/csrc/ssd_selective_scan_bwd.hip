@@ -34,15 +34,14 @@ __device__ __forceinline__ int64_t first_mark(const Run& r, int64_t slot) {
 // The first walk, up the tokens: of each run the state that it leaves, the states inside
 // it, and the gradient that its outputs give the state at its start,
 //   sum_t (prod_{s<=t} exp(delta_s A)) C_t du_t
+// Lanes past the group's end do what its last channel's lane does, and store the same.
 template <int N, bool BF16>
 __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   const ScanArgs& a = b.f;
   const ScanPlace pl(a);
   const Run r = find_run(a.runs, pl.slot);
   if (!r.on) return;
-  const int lane = threadIdx.x;
-  const bool mine = lane < pl.lanes;
-  const int own = mine ? lane : pl.lanes - 1;
+  const int own = (int)threadIdx.x < pl.lanes ? (int)threadIdx.x : pl.lanes - 1;
   const int64_t d = pl.channel + own;
 
   float A2[N], h[N], decay[N], back[N];
@@ -56,48 +55,80 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   }
   if (r.index == 0 && a.init != nullptr) load_states<N>(a.init + (r.seq * a.dim + d) * N, h);
   const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
-  const Rows<BF16> rows(a, pl, own, N);
-  const char* dy = (const char*)b.dy + pl.channel * (BF16 ? 2 : 4);
+  const bool gated = a.in.z != nullptr;
+  Rows<BF16> rows(a, pl, r.begin, own, N);
   const int64_t dy_step = a.dim * (BF16 ? 2 : 4);
-  int64_t mark = first_mark(r, pl.slot);
+  const char* dy = (const char*)b.dy + pl.channel * (BF16 ? 2 : 4) + r.begin * dy_step;
+  const int64_t mark0 = first_mark(r, pl.slot);
+  const int tokens = (int)(r.end - r.begin);
+  StateRows<N, BF16, true> bc(rows.B, rows.C, rows.b_step, rows.c_step, tokens);
   double total = 0.0;
-  for (int64_t t0 = r.begin; t0 < r.end; t0 += kMark, ++mark) {
-    if (t0 > r.begin && mine) {
+  constexpr int kBlock = 4;
+  static_assert(kMark == 2 * kBlock, "marks lie between pairs of blocks");
+  typedef typename Raw<BF16>::type raw;
+  struct Block {
+    raw x[kBlock], dt[kBlock], z[kBlock], g[kBlock];
+  };
+  auto load = [&](Block& k, int left) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) b.marks[(mark * N + n) * a.dim + d] = h[n];
-      b.mark_totals[mark * a.dim + d] = (float)total;
-    }
-    float x[kMark], dt[kMark], g[kMark];
-#pragma unroll
-    for (int j = 0; j < kMark; ++j) {
-      const int64_t t = t0 + j < r.end ? t0 + j : r.end - 1;
-      x[j] = load_one<BF16>(rows.x + t * rows.x_step, own);
-      dt[j] = load_one<BF16>(rows.dt + t * rows.dt_step, own);
-      g[j] = load_one<BF16>(dy + t * dy_step, own);
-      if (a.in.z != nullptr) {
-        const float z = load_one<BF16>(rows.z + t * rows.z_step, own);
-        g[j] *= z * sigmoid_f(z);
+    for (int j = 0; j < kBlock; ++j) {
+      k.x[j] = load_raw<BF16>(rows.x, rows.lane);
+      k.dt[j] = load_raw<BF16>(rows.dt, rows.lane);
+      k.g[j] = load_raw<BF16>(dy, rows.lane);
+      k.z[j] = load_raw<BF16>(rows.z, rows.lane);
+      if (j + 1 < left || left >= kBlock) {
+        rows.x += rows.x_step;
+        rows.dt += rows.dt_step;
+        rows.z += rows.z_step;
+        dy += dy_step;
       }
     }
+  };
+  auto mark = [&](int64_t t) {
+    const int64_t m = mark0 + t / kMark;
+    int64_t step = a.dim;
+    asm("" : "+s"(step));      // (its multiples would stay in scalar registers)
+    float* p = b.marks + m * N * step + d;
 #pragma unroll
-    for (int j = 0; j < kMark; ++j) {
-      if (t0 + j >= r.end) break;
-      const States<N, BF16> B(rows.B, (t0 + j) * rows.b_step);
-      const States<N, BF16> C(rows.C, (t0 + j) * rows.c_step);
-      const float v = dt[j] + bias;
-      const float delta = a.softplus ? softplus_f(v) : v;
-      const float dx = delta * x[j];
+    for (int n = 0; n < N; ++n, p += step) *p = h[n];
+    b.mark_totals[m * step + d] = (float)total;
+  };
+  auto work = [&](const Block& k, int left) {
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      if (j >= left) break;
+      States<N, BF16> B, C;
+      bc.next(B, C);
+      const float v = Raw<BF16>::get(k.dt[j]) + bias;
+      const float delta = pick(a.softplus, softplus_f(v), v);
+      const float dx = delta * Raw<BF16>::get(k.x[j]);
+      const float dy = Raw<BF16>::get(k.g[j]), z = Raw<BF16>::get(k.z[j]);
+      const float g = pick(gated, dy * (z * sigmoid_f(z)), dy);
       total += delta;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const float e = exp2_hw(delta * A2[n]);
         h[n] = __builtin_fmaf(e, h[n], dx * B[n]);
         decay[n] *= e;
-        back[n] = __builtin_fmaf(decay[n], C[n] * g[j], back[n]);
+        back[n] = __builtin_fmaf(decay[n], C[n] * g, back[n]);
       }
     }
+  };
+  Block even, odd;
+  if (tokens > 0) load(even, tokens);
+  int t = 0;
+  for (; t + 3 * kBlock <= tokens; t += 2 * kBlock) {
+    if (t > 0) mark(t);
+    load(odd, kBlock);
+    work(even, kBlock);
+    load(even, kBlock);
+    work(odd, kBlock);
   }
-  if (!mine) return;
+  for (; t < tokens; t += kBlock) {
+    if (t > 0 && t % kMark == 0) mark(t);
+    work(even, tokens - t);
+    if (t + kBlock < tokens) load(even, tokens - t - kBlock);
+  }
   store_run<N>(a, pl.slot, d, h);
   a.totals[pl.slot * a.dim + d] = (float)total;
 #pragma unroll
@@ -112,7 +143,7 @@ constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kRowRor8 = 0x128;
 template <int CTRL>
 __device__ __forceinline__ float moved(float v) {
   return __uint_as_float(
-      __builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xF, 0xF, false));
+      __builtin_amdgcn_mov_dpp(__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
 
 template <int N>
@@ -229,25 +260,30 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
       dA[c][n] = 0.0f;
     }
     // the state at the run's start, and the gradient of the state at its end
-    if (r.index == 0) {
-      if (a.init != nullptr) h = *(const f32x4*)(a.init + state);
+    if (a.joined && r.count > 1) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        h[n] = a.states[(slot * N + 4 * q + n) * a.dim + d[c]];
+        back[n] = b.back[(slot * N + 4 * q + n) * a.dim + d[c]];
+      }
     } else {
-      for (int64_t s = r.first; s < slot; ++s) {
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (r.index == 0) {
+        if (a.init != nullptr) load_states<4>(a.init + state, v);
+      } else {
+        fold_runs<4>(a, r.first, slot, d[c], A2[c], v, [&](int64_t s, int n) {
+          return a.states[(s * N + 4 * q + n) * a.dim + d[c]];
+        });
+      }
+      h = (f32x4){v[0], v[1], v[2], v[3]};
+      if (b.dfinal != nullptr) back = *(const f32x4*)(b.dfinal + state);
+      for (int64_t s = r.first + r.count - 1; s > slot; --s) {
         const float total = a.totals[s * a.dim + d[c]];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float left = a.states[(s * N + 4 * q + n) * a.dim + d[c]];
-          h[n] = s == r.first ? left : __builtin_fmaf(exp2_hw(total * A2[c][n]), h[n], left);
-        }
+        for (int n = 0; n < 4; ++n)
+          back[n] = __builtin_fmaf(exp2_hw(total * A2[c][n]), back[n],
+                                   b.back[(s * N + 4 * q + n) * a.dim + d[c]]);
       }
-    }
-    if (b.dfinal != nullptr) back = *(const f32x4*)(b.dfinal + state);
-    for (int64_t s = r.first + r.count - 1; s > slot; --s) {
-      const float total = a.totals[s * a.dim + d[c]];
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        back[n] = __builtin_fmaf(exp2_hw(total * A2[c][n]), back[n],
-                                 b.back[(s * N + 4 * q + n) * a.dim + d[c]]);
     }
     start[wave][c][lane] = on[c] ? h : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -562,7 +598,7 @@ int64_t run_length(const ScanShape& s) {
   const int64_t blocks = channel_blocks(s);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
   if (s.nseq * blocks >= 1024) return (4 * mean + kMark - 1) / kMark * kMark;
-  int64_t run = (s.tokens * blocks + 2047) / 2048;
+  int64_t run = (s.tokens * blocks + 4095) / 4096;
   run = (run + kMark - 1) / kMark * kMark;
   return run < 32 ? 32 : run;
 }
@@ -605,6 +641,7 @@ template <int N, bool BF16>
 void launch_n(const BwdArgs& b, int64_t blocks, int64_t wide, hipStream_t st) {
   hipLaunchKernelGGL((scan_local_kernel<N, BF16>), dim3((unsigned)(b.slots * blocks)),
                      dim3(kWave), 0, st, b);
+  if (b.f.joined) launch_scan_join(b.f, N, b.back, b.dfinal, st);
   hipLaunchKernelGGL((scan_bwd_kernel<N, BF16>),
                      dim3((unsigned)(b.slots * b.f.ngroups * wide)), dim3(kWave * kWaves), 0, st,
                      b);
@@ -633,6 +670,7 @@ int launch_scan_bwd(const ScanInputs& in, const float* init, const int32_t* cu, 
   a = make_scan_args(in, init, s, softplus);
   a.runs = make_run_grid(cu, s.tokens, s.nseq, run_length(s));
   b.slots = run_slots(a.runs);
+  a.joined = joins(a.runs);
   a.states = (float*)(base + l.states);
   a.totals = (float*)(base + l.totals);
   b.back = (float*)(base + l.back);
