@@ -16,7 +16,8 @@
  * before any HIP call.  Pointers are 16-byte aligned and arrays contiguous,
  * but where an entry names a row stride: such an input may be columns of a
  * wider array (the halves of one projection), starts on a multiple of its element
- * size (B and C: of 4 bytes), and its rows are `stride` elements apart (0: contiguous).
+ * size (B and C: of 4 bytes), and its rows are `stride` elements apart (0: contiguous; up
+ * to 2^26).
  * No output may overlap an input or another output unless an entry says so.
  *
  * Sequences are packed as in ssd_linattn_fwd: cu_seqlens, if not NULL, is a

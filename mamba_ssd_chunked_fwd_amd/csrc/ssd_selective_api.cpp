@@ -22,10 +22,12 @@ ssd_status from_hip(int err) { return err == 0 ? SSD_OK : SSD_ERR_HIP; }
 constexpr int64_t kMaxDim = 1 << 20;
 constexpr int64_t kMaxSequences = (1 << 22) - 1;
 
-// A row stride, 0 standing for contiguous rows; -1 if it is none.
+// A row stride, 0 standing for contiguous rows; -1 if it is none.  (Eight rows of fp32
+// lie within 2^31 bytes.)
+constexpr int64_t kMaxStride = 1 << 26;
 int64_t stride_of(int64_t stride, int64_t row) {
   if (stride == 0) return row;
-  return stride < row || stride > INT32_MAX ? -1 : stride;
+  return stride < row || stride > kMaxStride ? -1 : stride;
 }
 
 // Whether two byte ranges of length n (either may be null) share any byte.

@@ -23,6 +23,7 @@ struct ScanArgs {
   int group_dim;       // channels of a group
   int group_blocks;    // blocks of 64 channels of a group
   int softplus;
+  int paired;          // whether two channels' elements are read and written at once
   int joined;          // whether scan_join_kernel has been through the states
   // Of a split call, for each slot: the state that the run leaves [slots, N, dim] (in the
   // forward call the slot of a sequence's last run, whose state nobody asks for, holds the
@@ -46,6 +47,12 @@ inline ScanArgs make_scan_args(const ScanInputs& in, const float* init, const Sc
   a.group_dim = (int)(s.dim / s.ngroups);
   a.group_blocks = (a.group_dim + kWave - 1) / kWave;
   a.softplus = softplus;
+  // every pair of a group's channels there, and on 4 bytes in every row
+  const auto even = [](const void* p, int64_t stride) {
+    return (uintptr_t)p % 4 == 0 && stride % 2 == 0;
+  };
+  a.paired = a.group_dim % 2 == 0 && even(in.x, s.x_stride) && even(in.dt, s.dt_stride) &&
+             (in.z == nullptr || even(in.z, s.z_stride));
   return a;
 }
 
@@ -179,16 +186,23 @@ struct Raw<false> {
   typedef float type;
   static __device__ __forceinline__ float get(type v) { return v; }
 };
+// A uniform row and a lane's place in it, as a buffer access: no 64-bit address for each
+// lane is formed.
+__device__ __forceinline__ rsrc_t row_rsrc(const void* row) { return make_rsrc(row, 0x7FFFFFFF); }
 template <bool BF16>
 __device__ __forceinline__ typename Raw<BF16>::type load_raw(const char* row, uint32_t lane) {
-  return *(const typename Raw<BF16>::type*)(row + lane);
+  if constexpr (BF16)
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row_rsrc(row), (int)lane, 0, 0);
+  else
+    return load_f32(row_rsrc(row), lane);
 }
 template <bool BF16>
 __device__ __forceinline__ void store_raw(char* row, uint32_t lane, float v) {
   if constexpr (BF16)
-    *(uint16_t*)(row + lane) = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu);
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu), row_rsrc(row),
+                                          (int)lane, 0, 0);
   else
-    *(float*)(row + lane) = v;
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), row_rsrc(row), (int)lane, 0, 0);
 }
 
 template <int N>

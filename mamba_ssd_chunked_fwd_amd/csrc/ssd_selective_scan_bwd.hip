@@ -171,25 +171,58 @@ struct Lanes {
   }
 };
 
-// One element of two neighbouring channels, as it lies in memory.
+// One element of two neighbouring channels, as it lies in memory: `at` bytes into a row, and
+// `apart` bytes behind it; in one access where every lane has both (`paired`).
 template <bool BF16>
 struct Pair;
 template <>
 struct Pair<true> {
   uint32_t w;
-  __device__ __forceinline__ void load(const char* row, uint32_t a, uint32_t b) {
-    w = (uint32_t) * (const uint16_t*)(row + a) | (uint32_t) * (const uint16_t*)(row + b) << 16;
+  __device__ __forceinline__ void load(rsrc_t row, uint32_t at, uint32_t apart, bool paired) {
+    if (paired)
+      w = load_b32(row, at);
+    else
+      w = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, (int)at, 0, 0) |
+          (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row, (int)(at + apart), 0, 0)
+              << 16;
   }
   __device__ __forceinline__ float get(int c) const { return c ? bf16_hi(w) : bf16_lo(w); }
+  static __device__ __forceinline__ void store(rsrc_t row, uint32_t at, const float (&v)[2],
+                                               const bool (&on)[2], bool paired) {
+    const uint32_t u = pack_bf16(v[0], v[1]);
+    if (paired) {
+      if (on[0]) __builtin_amdgcn_raw_buffer_store_b32(u, row, (int)at, 0, 0);
+    } else {
+      if (on[0]) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)u, row, (int)at, 0, 0);
+      if (on[1])
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(u >> 16), row, (int)at + 2, 0, 0);
+    }
+  }
 };
 template <>
 struct Pair<false> {
   float v[2];
-  __device__ __forceinline__ void load(const char* row, uint32_t a, uint32_t b) {
-    v[0] = *(const float*)(row + a);
-    v[1] = *(const float*)(row + b);
+  __device__ __forceinline__ void load(rsrc_t row, uint32_t at, uint32_t apart, bool paired) {
+    if (paired) {
+      const u32x2 u = load_b64(row, at);
+      v[0] = __uint_as_float(u[0]);
+      v[1] = __uint_as_float(u[1]);
+    } else {
+      v[0] = load_f32(row, at);
+      v[1] = load_f32(row, at + apart);
+    }
   }
   __device__ __forceinline__ float get(int c) const { return v[c]; }
+  static __device__ __forceinline__ void store(rsrc_t row, uint32_t at, const float (&v)[2],
+                                               const bool (&on)[2], bool paired) {
+    const u32x2 u = {__float_as_uint(v[0]), __float_as_uint(v[1])};
+    if (paired) {
+      if (on[0]) __builtin_amdgcn_raw_buffer_store_b64(u, row, (int)at, 0, 0);
+    } else {
+      if (on[0]) __builtin_amdgcn_raw_buffer_store_b32(u[0], row, (int)at, 0, 0);
+      if (on[1]) __builtin_amdgcn_raw_buffer_store_b32(u[1], row, (int)at + 4, 0, 0);
+    }
+  }
 };
 
 // LDS writes of a wave's lanes before it are seen by their reads behind it (a wave's LDS
@@ -202,7 +235,7 @@ __device__ __forceinline__ void wave_sync() {
 
 constexpr int kBatch = 4;      // tokens whose dB and dC are summed over a wave's lanes at once
 
-template <int N, bool BF16>
+template <int N, bool BF16, bool PAIRED>
 __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdArgs b) {
   using La = Lanes<N>;
   constexpr int L = La::L, OWN = La::kOwn, TURNS = La::kTurns;
@@ -221,11 +254,11 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
   const int rest = (int)(blockIdx.x % per_slot);
   const int group = rest / wide, block = rest % wide;
   // the lane's channels; past the group's end they stand for nothing (zeros), and read the
-  // last one's rows
+  // last one's rows (the last two's where they are read in pairs: a group is even then)
   const int at = (block * kWaves + wave) * La::kChannels + lane / L * 2;
   const bool on[2] = {at < a.group_dim, at + 1 < a.group_dim};
   const int64_t base = (int64_t)group * a.group_dim;
-  const int64_t d[2] = {base + (on[0] ? at : a.group_dim - 1),
+  const int64_t d[2] = {base + (on[0] ? at : a.group_dim - (PAIRED ? 2 : 1)),
                         base + (on[1] ? at + 1 : a.group_dim - 1)};
 
   const Run r = find_run(a.runs, slot);
@@ -292,13 +325,16 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
     skip[c] = a.in.D ? a.in.D[d[c]] : 0.0f;
   }
 
+  constexpr bool paired = PAIRED;
   const bool gated = a.in.z != nullptr;
-  const uint32_t off[2] = {(uint32_t)(d[0] - base) * el, (uint32_t)(d[1] - base) * el};
+  const uint32_t place = (uint32_t)(d[0] - base) * el, apart = (uint32_t)(d[1] - d[0]) * el;
   const char* x_row = (const char*)a.in.x + base * el;
   const char* dt_row = (const char*)a.in.dt + base * el;
-  const char* z_row = (const char*)a.in.z + base * el;
+  // (without a gate rows of x are read in the place of z's, and not used)
+  const char* z_row = (const char*)(gated ? a.in.z : a.in.x) + base * el;
   const char* dy_row = (const char*)b.dy + base * el;
-  const int64_t x_step = a.x_stride * el, dt_step = a.dt_stride * el, z_step = a.z_stride * el;
+  const int64_t x_step = a.x_stride * el, dt_step = a.dt_stride * el;
+  const int64_t z_step = (gated ? a.z_stride : a.x_stride) * el;
   const int64_t out_step = a.dim * el;
   const char* B_row = (const char*)a.in.B + (int64_t)group * N * el;
   const char* C_row = (const char*)a.in.C + (int64_t)group * N * el;
@@ -308,76 +344,94 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
   const int64_t mark0 = first_mark(r, slot);
   float dD[2] = {0.0f, 0.0f}, dbias[2] = {0.0f, 0.0f};
 
+  // Where the lane's own tokens of a block of `count` lie behind its first row (those
+  // behind the last one read its row).
+  struct Place {
+    uint32_t x, dt, z, y;
+  } own_at[OWN];
+  auto put = [&](int count) {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      const int t = i * TURNS + q % TURNS;
+      const uint32_t j = (uint32_t)(t < count ? t : count - 1);
+      own_at[i] = {place + j * (uint32_t)x_step, place + j * (uint32_t)dt_step,
+                   place + j * (uint32_t)z_step, place + j * (uint32_t)out_step};
+    }
+  };
   // what a block reads: its tokens' rows, B and C, and the state at its start
-  Pair<BF16> x[OWN], raw[OWN], z[OWN], g[OWN];
-  constexpr int kBC = 2 * N * kMark / (kWave * kWaves);     // values of B and C a thread
-  float bc[kBC > 0 ? kBC : 1];
+  struct Own {
+    Pair<BF16> x, raw, z, g;
+  } next[OWN];
+  constexpr int kBC = (2 * N * kMark + kWave * kWaves - 1) / (kWave * kWaves);
+  float bc[kBC];      // values of B and C a thread
   float mark[2][4], mark_total[2];
+  const uint32_t mark_at[2] = {(uint32_t)(d[0] - base) * 4, (uint32_t)(d[1] - base) * 4};
+  const uint32_t mark_row = (uint32_t)(4 * q) * (uint32_t)a.dim * 4;
   auto load = [&](int m) {
     const int64_t t0 = r.begin + (int64_t)m * kMark;
     const int count = r.end - t0 < kMark ? (int)(r.end - t0) : kMark;
+    const rsrc_t xr = row_rsrc(x_row + t0 * x_step), dtr = row_rsrc(dt_row + t0 * dt_step);
+    const rsrc_t zr = row_rsrc(z_row + t0 * z_step), yr = row_rsrc(dy_row + t0 * out_step);
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
-      const int j = i * TURNS + q % TURNS;
-      const int64_t t = t0 + (j < count ? j : count - 1);
-      x[i].load(x_row + t * x_step, off[0], off[1]);
-      raw[i].load(dt_row + t * dt_step, off[0], off[1]);
-      g[i].load(dy_row + t * out_step, off[0], off[1]);
-      if (gated) z[i].load(z_row + t * z_step, off[0], off[1]);
+      next[i].x.load(xr, own_at[i].x, apart, paired);
+      next[i].raw.load(dtr, own_at[i].dt, apart, paired);
+      next[i].z.load(zr, own_at[i].z, apart, paired);
+      next[i].g.load(yr, own_at[i].y, apart, paired);
     }
 #pragma unroll
-    for (int i = 0; i < (kBC > 0 ? kBC : 1); ++i) {
+    for (int i = 0; i < kBC; ++i) {
       const int v = (int)threadIdx.x + i * kWave * kWaves;
-      const int j = v / (2 * N), k = v % (2 * N);
+      const int j = v / (2 * N), k = v % N;
+      bc[i] = 0.0f;
       if (j < count)
-        bc[i] = k < N ? load_one<BF16>(B_row + (t0 + j) * b_step, k)
-                      : load_one<BF16>(C_row + (t0 + j) * c_step, k - N);
+        bc[i] = v % (2 * N) < N ? load_one<BF16>(B_row + (t0 + j) * b_step, k)
+                                : load_one<BF16>(C_row + (t0 + j) * c_step, k);
     }
     if (m > 0) {
+      const char* p = (const char*)(b.marks + (mark0 + m) * N * a.dim + base);
+      const rsrc_t total = row_rsrc(b.mark_totals + (mark0 + m) * a.dim + base);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        mark_total[c] = b.mark_totals[(mark0 + m) * a.dim + d[c]];
+        mark_total[c] = load_f32(total, mark_at[c]);
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-          mark[c][n] = b.marks[((mark0 + m) * N + 4 * q + n) * a.dim + d[c]];
+          mark[c][n] = load_f32(row_rsrc(p + n * (int64_t)a.dim * 4), mark_at[c] + mark_row);
       }
     }
   };
   auto stage = [&](int turn) {
 #pragma unroll
-    for (int i = 0; i < (kBC > 0 ? kBC : 1); ++i) {
+    for (int i = 0; i < kBC; ++i) {
       const int v = (int)threadIdx.x + i * kWave * kWaves;
       if (v < 2 * N * kMark) ((float*)bc_in[turn])[v] = bc[i];
     }
   };
 
+  put((int)(r.end - r.begin) - (blocks - 1) * kMark);
   load(blocks - 1);
   stage(0);
+  put(kMark);
   __syncthreads();
   int turn = 0;
   for (int m = blocks - 1; m >= 0; --m, turn ^= 1) {
     const int64_t t0 = r.begin + (int64_t)m * kMark;
     const int count = r.end - t0 < kMark ? (int)(r.end - t0) : kMark;
     // the time steps and gradients of the lane's own tokens
-    Pair<BF16> xo[OWN], rawo[OWN], zo[OWN], go[OWN];
+    Own own[OWN];
     float delta[OWN][2], dx[OWN][2], du[OWN][2];
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
-      xo[i] = x[i];
-      rawo[i] = raw[i];
-      zo[i] = z[i];
-      go[i] = g[i];
+      own[i] = next[i];
+      // what is past the run's end, or the group's, has neither time nor input nor gradient:
+      // nothing branches on it
+      const bool there = i * TURNS + q % TURNS < count;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float v = rawo[i].get(c) + bias[c];
-        delta[i][c] = a.softplus ? softplus_f(v) : v;
-        dx[i][c] = on[c] ? delta[i][c] * xo[i].get(c) : 0.0f;
-        du[i][c] = go[i].get(c);
-        if (gated) {
-          const float zz = zo[i].get(c);
-          du[i][c] *= zz * sigmoid_f(zz);
-        }
-        if (!on[c]) du[i][c] = 0.0f;
+        const float v = own[i].raw.get(c) + bias[c], z = own[i].z.get(c), dy = own[i].g.get(c);
+        delta[i][c] = pick(there, pick(a.softplus, softplus_f(v), v), 0.0f);
+        dx[i][c] = pick(there & on[c], delta[i][c] * own[i].x.get(c), 0.0f);
+        du[i][c] = pick(there & on[c], pick(gated, dy * (z * sigmoid_f(z)), dy), 0.0f);
       }
     }
     float h[kMark + 1][2][4];
@@ -395,20 +449,26 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
         if (!on[c]) h[0][c][n] = 0.0f;
       }
     }
-    if (m > 0) load(m - 1);
-
+    // (tokens stay apart: work and reads of many at once would not fit the registers)
+    auto fence = [] {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
     auto up = [&](auto jj) {
       constexpr int j = decltype(jj)::value;
-      if (j >= count) return;
       const f32x4 B = bc_in[turn][j][0][q];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float dl = La::template bcast<j % TURNS>(delta[j / TURNS][c]);
         const float dxj = La::template bcast<j % TURNS>(dx[j / TURNS][c]);
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          h[j + 1][c][n] = __builtin_fmaf(exp2_hw(dl * A2[c][n]), h[j][c][n], dxj * B[n]);
+        for (int n = 0; n < 4; ++n) {
+          float v = __builtin_fmaf(exp2_hw(dl * A2[c][n]), h[j][c][n], dxj * B[n]);
+          asm volatile("" : "+v"(v));      // (formed here, not where it is used)
+          h[j + 1][c][n] = v;
+        }
       }
+      fence();
     };
     float inner[OWN][2], ddelta[OWN][2], u[OWN][2];
 #pragma unroll
@@ -417,12 +477,12 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
       for (int c = 0; c < 2; ++c) inner[i][c] = ddelta[i][c] = u[i][c] = 0.0f;
     auto down = [&](auto jj) {
       constexpr int j = decltype(jj)::value, i = j / TURNS;
-      if (j >= count) return;
       const f32x4 B = bc_in[turn][j][0][q], C = bc_in[turn][j][1][q];
       f32x4 vB, vC;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float dl = La::template bcast<j % TURNS>(delta[i][c]);
+        float dl = La::template bcast<j % TURNS>(delta[i][c]);
+        asm volatile("" : "+v"(dl));     // (its products are formed again, not kept)
         const float dxj = La::template bcast<j % TURNS>(dx[i][c]);
         const float duj = La::template bcast<j % TURNS>(du[i][c]);
         float in = 0.0f, dd = 0.0f, uu = 0.0f;
@@ -440,19 +500,19 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
         }
         in = La::sum(in);
         dd = La::sum(dd);
-        if (gated) uu = La::sum(uu);
+        uu = La::sum(uu);
         const bool own = q % TURNS == j % TURNS;
-        inner[i][c] = own ? in : inner[i][c];
-        ddelta[i][c] = own ? dd : ddelta[i][c];
-        u[i][c] = own ? uu : u[i][c];
+        inner[i][c] = pick(own, in, inner[i][c]);
+        ddelta[i][c] = pick(own, dd, ddelta[i][c]);
+        u[i][c] = pick(own, uu, u[i][c]);
       }
       values[wave][j % kBatch][0][lane] = vB;
       values[wave][j % kBatch][1][lane] = vC;
+      fence();
     };
     // The sums of a batch's dB and dC over the wave's pairs: 8 L of them (token, half, lane
     // of the pair), of kPairs vectors each, are shared by the 64 lanes, eight vectors a lane.
     auto batch = [&](int j0) {
-      if (j0 >= count) return;
       constexpr int kTasks = 2 * kBatch * L;
       constexpr int kParts = kTasks < kWave ? kWave / kTasks : 1;   // lanes of a sum
       constexpr int kRounds = kTasks > kWave ? kTasks / kWave : 1;
@@ -473,9 +533,32 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
           if (kParts >= 2) sum[e] += moved<kXor1>(sum[e]);
           if (kParts >= 4) sum[e] += moved<kXor2>(sum[e]);
         }
-        if (part == 0 && j0 + j < count) sums[turn][wave][j0 + j][half][k] = sum;
+        if (part == 0) sums[turn][wave][j0 + j][half][k] = sum;
       }
       wave_sync();
+    };
+    // the lane's own tokens
+    auto finish = [&](int i) {
+      const int j = i * TURNS + q;
+      if (q >= TURNS || j >= count) return;
+      float vx[2], vdt[2], vz[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float x = own[i].x.get(c), v = own[i].raw.get(c) + bias[c];
+        const float z = own[i].z.get(c), sig = sigmoid_f(z);
+        const float ddt = __builtin_fmaf(ddelta[i][c], kLn2, inner[i][c] * x);
+        vdt[c] = pick(a.softplus, ddt * sigmoid_f(v), ddt);
+        dbias[c] += vdt[c];
+        dD[c] = __builtin_fmaf(du[i][c], x, dD[c]);
+        vx[c] = __builtin_fmaf(inner[i][c], delta[i][c], skip[c] * du[i][c]);
+        vz[c] = own[i].g.get(c) * __builtin_fmaf(skip[c], x, u[i][c]) *
+                (sig * __builtin_fmaf(z, 1.0f - sig, 1.0f));
+      }
+      const int64_t row = t0 * out_step + base * el;
+      Pair<BF16>::store(row_rsrc((char*)b.out.dx + row), own_at[i].y, vx, on, paired);
+      Pair<BF16>::store(row_rsrc((char*)b.out.ddt + row), own_at[i].y, vdt, on, paired);
+      if (gated)
+        Pair<BF16>::store(row_rsrc((char*)b.out.dz + row), own_at[i].y, vz, on, paired);
     };
     up(std::integral_constant<int, 0>{});
     up(std::integral_constant<int, 1>{});
@@ -490,38 +573,19 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
     down(std::integral_constant<int, 5>{});
     down(std::integral_constant<int, 4>{});
     batch(4);
+    // (tokens are finished, and the next block's rows asked for, where registers are free)
+#pragma unroll
+    for (int i = OWN - 1; i >= 0; --i)
+      if (i * TURNS >= kBatch) finish(i);
+    if (m > 0) load(m - 1);
     down(std::integral_constant<int, 3>{});
     down(std::integral_constant<int, 2>{});
     down(std::integral_constant<int, 1>{});
     down(std::integral_constant<int, 0>{});
     batch(0);
-
-    // the lane's own tokens
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int j = i * TURNS + q;
-      if (q >= TURNS || j >= count) continue;
-      const int64_t t = t0 + j;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float xx = xo[i].get(c);
-        float ddt = __builtin_fmaf(ddelta[i][c], kLn2, inner[i][c] * xx);
-        if (a.softplus) ddt *= sigmoid_f(rawo[i].get(c) + bias[c]);
-        dbias[c] += ddt;
-        dD[c] = __builtin_fmaf(du[i][c], xx, dD[c]);
-        if (!on[c]) continue;
-        const int64_t row = t * out_step + base * el;
-        store_one<BF16>((char*)b.out.dx + row + off[c], 0,
-                        __builtin_fmaf(inner[i][c], delta[i][c], skip[c] * du[i][c]));
-        store_one<BF16>((char*)b.out.ddt + row + off[c], 0, ddt);
-        if (gated) {
-          const float zz = zo[i].get(c), sig = sigmoid_f(zz);
-          const float slope = sig * __builtin_fmaf(zz, 1.0f - sig, 1.0f);
-          store_one<BF16>((char*)b.out.dz + row + off[c], 0,
-                          go[i].get(c) * __builtin_fmaf(skip[c], xx, u[i][c]) * slope);
-        }
-      }
-    }
+    for (int i = OWN - 1; i >= 0; --i)
+      if (i * TURNS < kBatch) finish(i);
     if (m > 0) stage(turn ^ 1);
     __syncthreads();
     // dB and dC of this block of channels
@@ -642,9 +706,11 @@ void launch_n(const BwdArgs& b, int64_t blocks, int64_t wide, hipStream_t st) {
   hipLaunchKernelGGL((scan_local_kernel<N, BF16>), dim3((unsigned)(b.slots * blocks)),
                      dim3(kWave), 0, st, b);
   if (b.f.joined) launch_scan_join(b.f, N, b.back, b.dfinal, st);
-  hipLaunchKernelGGL((scan_bwd_kernel<N, BF16>),
-                     dim3((unsigned)(b.slots * b.f.ngroups * wide)), dim3(kWave * kWaves), 0, st,
-                     b);
+  const dim3 grid((unsigned)(b.slots * b.f.ngroups * wide)), threads(kWave * kWaves);
+  if (b.f.paired)
+    hipLaunchKernelGGL((scan_bwd_kernel<N, BF16, true>), grid, threads, 0, st, b);
+  else
+    hipLaunchKernelGGL((scan_bwd_kernel<N, BF16, false>), grid, threads, 0, st, b);
 }
 
 }  // namespace
