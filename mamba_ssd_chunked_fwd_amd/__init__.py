@@ -26,6 +26,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple
@@ -852,43 +853,45 @@ def _rows_arg(t, name: str, shape, dtypes, device, size: int):
     """The address and the row stride (in elements) of a tensor whose rows (its last
     dimensions, ``shape`` being all of them) may be columns of a wider tensor.  It
     starts on a multiple of ``size`` bytes, and so does every row."""
+    if type(t) is torch.Tensor and t.dtype in dtypes and t.device == device and \
+            t.shape == shape and t.is_cuda:
+        p = t.data_ptr()
+        stride = 0 if t.is_contiguous() else _row_stride(name, t.shape, t.stride())
+        if p % size == 0 and stride * t.element_size() % size == 0:
+            return p, stride
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    p, el = t.data_ptr(), t.element_size()
-    if t.is_contiguous():
-        stride = 0
-    else:
-        stride = _row_stride(t, name)
-        if stride * el % size:
-            raise ValueError(f"rows of {name} must be a multiple of {size} bytes apart (pass a "
-                             f"copy)")
-    if p % size:
+    stride = 0 if t.is_contiguous() else _row_stride(name, t.shape, t.stride())
+    if stride * t.element_size() % size:
+        raise ValueError(f"rows of {name} must be a multiple of {size} bytes apart (pass a copy)")
+    if t.data_ptr() % size:
         raise ValueError(f"{name} must start on a {size}-byte boundary (pass a copy)")
-    return p, stride
+    return t.data_ptr(), stride
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
+@functools.lru_cache(maxsize=1024)
+def _row_stride(name: str, shape, strides) -> int:
     """Elements between the rows of x [b, L, dim] or [b, dim], or of B [b, L, G, N] or
     [b, G, N]: rows contiguous, one distance between all of them."""
-    lead = 2 if t.dim() == 4 or (t.dim() == 3 and name not in ("B", "C")) else 1
+    lead = 2 if len(shape) == 4 or (len(shape) == 3 and name not in ("B", "C")) else 1
     inner = 1
-    for n, s in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+    for n, s in zip(reversed(shape[lead:]), reversed(strides[lead:])):
         if n > 1 and s != inner:
             raise ValueError(f"{name}: the elements of a row must be contiguous (pass a copy)")
         inner *= n
-    b, L = (1, t.shape[0]) if lead == 1 else t.shape[:2]
+    b, L = (1, shape[0]) if lead == 1 else shape[:2]
     if b * L == 1:
         return inner
-    stride = t.stride(lead - 1) if L > 1 else t.stride(0)
-    if stride < inner or (lead == 2 and b > 1 and L > 1 and t.stride(0) != L * stride):
+    stride = strides[lead - 1] if L > 1 else strides[0]
+    if stride < inner or (lead == 2 and b > 1 and L > 1 and strides[0] != L * stride):
         raise ValueError(f"{name}: rows must be one distance apart (pass a copy)")
     return stride
 
@@ -1285,8 +1288,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     torch.no_grad()."""
     _no_graph("short_conv", x=x, weight=weight, bias=bias, init_state=init_state)
     d, ins = _conv_args(x, weight, bias, init_state, cu_seqlens)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    final = torch.empty((d.nseq, d.width - 1, d.dim), dtype=x.dtype, device=x.device)
+    y, final = x.new_empty(x.shape), x.new_empty((d.nseq, d.width - 1, d.dim))
     _run_conv_fwd(d, ins, x, y, final, activation)
     return y, final
 
@@ -1300,8 +1302,7 @@ def short_conv_backward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[to
     """Allocate and run ``ssd_short_conv_bwd``: (dx, dweight, dbias, dinit), None for
     each of the last two whose input is None."""
     d, ins = _conv_args(x, weight, bias, init_state, cu_seqlens)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = torch.empty_like(weight)
+    dx, dw = x.new_empty(x.shape), torch.empty_like(weight)
     db, dinit = (None if t is None else torch.empty_like(t) for t in (bias, init_state))
     keep, ws = _scratch(short_conv_workspace_bytes(d), x.device)
     _run_conv_bwd(d, ins, x, dy, dfinal, dx, dw, db, dinit, ws, activation)
@@ -1321,8 +1322,7 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     _no_graph("selective_scan", x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
               init_state=init_state)
     d, ins = _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    final = torch.empty((d.nseq, d.dim, d.dstate), dtype=torch.float32, device=x.device)
+    y, final = x.new_empty(x.shape), A.new_empty((d.nseq, d.dim, d.dstate))
     keep, ws = _scratch(selective_scan_workspace_bytes(d, x.dtype), x.device)
     _run_scan_fwd(d, ins, x, y, final, ws, softplus)
     return y, final
@@ -1340,7 +1340,7 @@ def selective_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
     d, ins = _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens)
 
     def like(t):
-        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return None if t is None else t.new_empty(t.shape)
 
     grads = [like(t) for t in (x, dt, A, B, C, D, z, dt_bias, init_state)]
     keep, ws = _scratch(selective_scan_workspace_bytes(d, x.dtype, backward=True), x.device)
@@ -1366,8 +1366,8 @@ def add_norm_quant(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
     group = D if group is None else int(group)
     if group < 1 or D % group:
         raise ValueError(f"group must be a divisor of {D}, not {group}")
-    codes = torch.empty(x.shape, dtype=dtype, device=x.device)
-    scales = torch.empty(x.shape[:-1] + (D // group,), dtype=torch.float32, device=x.device)
+    codes = x.new_empty(x.shape, dtype=dtype)
+    scales = x.new_empty(x.shape[:-1] + (D // group,), dtype=torch.float32)
     out = torch.empty_like(x if residual is None else residual)
     ssd_add_norm_quant_fwd(x, residual, res_scale, weight, codes, scales, out, eps)
     return codes, scales, out

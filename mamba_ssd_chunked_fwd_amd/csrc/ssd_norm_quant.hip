@@ -31,28 +31,36 @@ struct QuantArgs {
   double eps, inv_dim;
 };
 
+// Eight elements as they lie in memory, and as floats (zeros where fewer are left).
 template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void load_eight(const void* p, int64_t i, int left, float (&v)[kVec]) {
-  if constexpr (!WHOLE) {
+struct Eight {
+  uint32_t w[BF16 ? 4 : 8];
+  __device__ __forceinline__ void load(const void* p, int64_t i, int left) {
+    if constexpr (!WHOLE) {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = e < left ? load_one<BF16>(p, i + e) : 0.0f;
-  } else if constexpr (BF16) {
-    const u32x4 u = *(const u32x4*)((const uint16_t*)p + i);
+      for (int e = 0; e < kVec; ++e) {
+        if constexpr (BF16) {
+          const uint32_t v = e < left ? ((const uint16_t*)p)[i + e] : 0u;
+          w[e / 2] = e & 1 ? w[e / 2] | v << 16 : v;
+        } else {
+          w[e] = e < left ? ((const uint32_t*)p)[i + e] : 0u;
+        }
+      }
+    } else {
+      const u32x4* q = (const u32x4*)((const char*)p + i * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = bf16_lo(u[k]);
-      v[2 * k + 1] = bf16_hi(u[k]);
-    }
-  } else {
-    const f32x4 a = *(const f32x4*)((const float*)p + i);
-    const f32x4 b = *(const f32x4*)((const float*)p + i + 4);
+      for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+        const u32x4 u = q[h];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = a[k];
-      v[4 + k] = b[k];
+        for (int k = 0; k < 4; ++k) w[4 * h + k] = u[k];
+      }
     }
   }
-}
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (BF16) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    return __uint_as_float(w[e]);
+  }
+};
 template <bool BF16, bool WHOLE>
 __device__ __forceinline__ void store_eight(void* p, int64_t i, int left, const float (&v)[kVec]) {
   if constexpr (!WHOLE) {
@@ -66,12 +74,6 @@ __device__ __forceinline__ void store_eight(void* p, int64_t i, int left, const 
     *(f32x4*)((float*)p + i) = (f32x4){v[0], v[1], v[2], v[3]};
     *(f32x4*)((float*)p + i + 4) = (f32x4){v[4], v[5], v[6], v[7]};
   }
-}
-
-// The larger of two values that are not negative; a NaN stays (its bits are the largest).
-__device__ __forceinline__ double larger(double a, double b) {
-  const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
-  return x > y ? a : b;
 }
 
 // To 32 bits so that rounding the result again, to fewer bits, rounds v once: cut off, and
@@ -113,64 +115,87 @@ constexpr int kMaxWaves = 16;
 // GROUPED: groups of 16 to 256 channels; otherwise the row is one.
 template <int NV, bool XBF16, bool RBF16, bool E4M3, bool GROUPED, bool WHOLE>
 __global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const QuantArgs a) {
-  __shared__ double red[2][kMaxWaves];
+  __shared__ double red[2][2][kMaxWaves];
+  int turn = 0;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int waves = (int)blockDim.x / kWave;
   const double top = E4M3 ? 448.0 : 127.0;
 
-  float s[NV][kVec], w[NV][kVec];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * kVec;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) s[j][e] = w[j][e] = 1.0f;
-    if (c < a.dim) {
-      if (a.scale) load_eight<false, WHOLE>(a.scale, c, a.dim - c, s[j]);
-      if (a.weight) load_eight<false, WHOLE>(a.weight, c, a.dim - c, w[j]);
-    }
-  }
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    double h[NV][kVec], sum = 0.0;
+  // a lane's channels: their scale, weight and the next row's values
+  Eight<false, WHOLE> s[NV], w[NV];
+  Eight<XBF16, WHOLE> x[NV];
+  Eight<RBF16, WHOLE> r[NV];
+  const auto channel = [&](int j) { return ((int)threadIdx.x + j * (int)blockDim.x) * kVec; };
+  const auto load = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * kVec;
-      const int64_t i = row * a.dim + c;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) h[j][e] = 0.0;
+      const int c = channel(j);
       if (c >= a.dim) continue;
-      float x[kVec], r[kVec];
-      load_eight<XBF16, WHOLE>(a.x, i, a.dim - c, x);
+      x[j].load(a.x, row * a.dim + c, a.dim - c);
+      if (a.res) r[j].load(a.res, row * a.dim + c, a.dim - c);
+    }
+  };
+  // Rows of one vector a lane are read a row ahead, and scales and weights once; two vectors
+  // do not leave the registers for it.
+  constexpr bool kAhead = NV == 1;
+  const auto load_params = [&] {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) r[e] = 0.0f;
-      if (a.res) load_eight<RBF16, WHOLE>(a.res, i, a.dim - c, r);
+    for (int j = 0; j < NV; ++j) {
+      const int c = channel(j);
+      if (c >= a.dim) continue;
+      if (a.scale) s[j].load(a.scale, c, a.dim - c);
+      if (a.weight) w[j].load(a.weight, c, a.dim - c);
+    }
+  };
+  if (kAhead) {
+    load(blockIdx.x);
+    load_params();
+  }
+  const int64_t groups = a.dim / a.group;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    // h, the sum of its squares, then h o w (whose largest value is the group's: the row's
+    // factor is not needed for the codes)
+    double h[NV][kVec], most[NV], sum = 0.0;
+    if (!kAhead) {
+      load(row);
+      asm volatile("" ::: "memory");     // (scales and weights are not kept from row to row)
+      load_params();
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = channel(j);
+      float rounded[kVec];
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        h[j][e] = __builtin_fma((double)s[j][e], (double)x[e], (double)r[e]);
-        if (!WHOLE && c + e >= a.dim) h[j][e] = 0.0;
-        sum = __builtin_fma(h[j][e], h[j][e], sum);
-        r[e] = (float)h[j][e];
+        const double in = x[j].get(e), old = a.res ? (double)r[j].get(e) : 0.0;
+        double v = a.scale ? __builtin_fma((double)s[j].get(e), in, old) : in + old;
+        if (c + (WHOLE ? 0 : e) >= a.dim) v = 0.0;
+        sum = __builtin_fma(v, v, sum);
+        rounded[e] = (float)v;
+        h[j][e] = v;
       }
-      if (a.res_out) store_eight<RBF16, WHOLE>(a.res_out, i, a.dim - c, r);
+      if (a.res_out && c < a.dim)
+        store_eight<RBF16, WHOLE>(a.res_out, row * a.dim + c, a.dim - c, rounded);
     }
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
-    if (waves > 1) {
-      if (lane == 0) red[0][wave] = sum;
-      __syncthreads();
-      sum = 0.0;
-      for (int k = 0; k < waves; ++k) sum += red[0][k];
-    }
-    const double rstd = 1.0 / __builtin_sqrt(__builtin_fma(sum, a.inv_dim, a.eps));
-    double most[NV];
+    if (kAhead && row + gridDim.x < a.rows) load(row + gridDim.x);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      // (a value that is not finite makes bad a NaN, and the largest value with it)
+      double bad = 0.0;
       most[j] = 0.0;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        h[j][e] = h[j][e] * rstd * (double)w[j][e];
-        most[j] = larger(most[j], __builtin_fabs(h[j][e]));
+        if (a.weight) {
+          h[j][e] *= (double)w[j].get(e);
+          if (channel(j) + (WHOLE ? 0 : e) >= a.dim) h[j][e] = 0.0;
+        }
+        most[j] = __builtin_fmax(most[j], __builtin_fabs(h[j][e]));
+        bad = __builtin_fma(h[j][e], 0.0, bad);
       }
+      most[j] = bad == 0.0 ? most[j] : bad;
     }
+    // of two values, the larger, or one that is a NaN
+    const auto larger = [](double p, double q) { return p > q || p != p ? p : q; };
     if constexpr (GROUPED) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -178,25 +203,34 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const 
           most[j] = larger(most[j], __shfl_xor(most[j], off, kWave));
       }
     } else {
-      double m = most[0];
 #pragma unroll
-      for (int j = 1; j < NV; ++j) m = larger(m, most[j]);
+      for (int j = 1; j < NV; ++j) most[0] = larger(most[0], most[j]);
 #pragma unroll
-      for (int off = kWave / 2; off > 0; off >>= 1) m = larger(m, __shfl_xor(m, off, kWave));
-      if (waves > 1) {
-        if (lane == 0) red[1][wave] = m;
-        __syncthreads();
-        for (int k = 0; k < waves; ++k) m = larger(m, red[1][k]);
-      }
-#pragma unroll
-      for (int j = 0; j < NV; ++j) most[j] = m;
+      for (int off = kWave / 2; off > 0; off >>= 1)
+        most[0] = larger(most[0], __shfl_xor(most[0], off, kWave));
     }
-    const int64_t groups = a.dim / a.group;
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+    if (waves > 1) {
+      if (lane == 0) {
+        red[turn][0][wave] = sum;
+        red[turn][1][wave] = most[0];
+      }
+      __syncthreads();
+      sum = 0.0;
+      for (int k = 0; k < waves; ++k) {
+        sum += red[turn][0][k];
+        if (!GROUPED) most[0] = larger(most[0], red[turn][1][k]);
+      }
+      turn ^= 1;      // (written again behind the next row's barrier)
+    }
+    const double rstd = 1.0 / __builtin_sqrt(__builtin_fma(sum, a.inv_dim, a.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * kVec;
+      const int c = channel(j);
       if (c >= a.dim) continue;
-      const double inv = most[j] >= kLeast ? top / most[j] : 0.0;
+      const double m = GROUPED ? most[j] : most[0], y = m * rstd;
+      const double inv = y >= kLeast ? top / m : 0.0;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) h[j][e] *= inv;
       const u32x2 codes = encode<E4M3>(h[j]);
@@ -208,9 +242,9 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const 
         for (int e = 0; e < kVec; ++e)
           if (c + e < a.dim) out[e] = (uint8_t)(codes[e / 4] >> (8 * (e % 4)));
       }
-      if (c % a.group == 0) a.scales[row * groups + c / a.group] = (float)(most[j] / top);
+      if (GROUPED ? c % a.group == 0 : c == 0)
+        a.scales[row * groups + (GROUPED ? c / a.group : 0)] = (float)(y / top);
     }
-    if (waves > 1 && GROUPED) __syncthreads();   // (red[0] is written again)
   }
 }
 

@@ -22,6 +22,7 @@ struct ScanArgs {
   int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
   int group_dim;       // channels of a group
   int group_blocks;    // blocks of 64 channels of a group
+  Divide by_blocks, by_slot;   // by it, and by the blocks of all groups
   int softplus;
   int paired;          // whether two channels' elements are read and written at once
   int joined;          // whether scan_join_kernel has been through the states
@@ -46,6 +47,8 @@ inline ScanArgs make_scan_args(const ScanInputs& in, const float* init, const Sc
   a.c_stride = s.c_stride;
   a.group_dim = (int)(s.dim / s.ngroups);
   a.group_blocks = (a.group_dim + kWave - 1) / kWave;
+  a.by_blocks = Divide(a.group_blocks);
+  a.by_slot = Divide(a.group_blocks * s.ngroups);
   a.softplus = softplus;
   // every pair of a group's channels there, and on 4 bytes in every row
   const auto even = [](const void* p, int64_t stride) {
@@ -58,16 +61,13 @@ inline ScanArgs make_scan_args(const ScanInputs& in, const float* init, const Sc
 
 // The workgroup's 64 channels and its slot.
 struct ScanPlace {
-  int64_t slot, channel;
-  int group, lanes;
-  __device__ __forceinline__ explicit ScanPlace(const ScanArgs& a)
-      : ScanPlace(a, blockIdx.x, a.group_blocks) {}
-  __device__ __forceinline__ ScanPlace(const ScanArgs& a, int64_t item, int blocks) {
-    const int64_t per_slot = a.ngroups * blocks;
-    slot = item / per_slot;
-    const int rest = (int)(item % per_slot);
-    group = rest / blocks;
-    const int at = rest % blocks * kWave;
+  int slot, group, lanes;
+  int64_t channel;
+  __device__ __forceinline__ explicit ScanPlace(const ScanArgs& a) {
+    slot = (int)a.by_slot.of(blockIdx.x);
+    const uint32_t rest = blockIdx.x - (uint32_t)slot * a.by_slot.d;
+    group = (int)a.by_blocks.of(rest);
+    const int at = (int)(rest - (uint32_t)group * a.by_blocks.d) * kWave;
     channel = (int64_t)group * a.group_dim + at;
     lanes = a.group_dim - at < kWave ? a.group_dim - at : kWave;
   }
@@ -221,7 +221,7 @@ __device__ __forceinline__ void load_run(const ScanArgs& a, int64_t slot, int64_
 // ---- the states at the runs' starts
 // Few runs: each goes through those before it itself (no launch).  Many: a launch of their
 // own (scan_join_kernel) replaces what the runs leave by what they start from.
-constexpr int kFoldRuns = 12;      // runs that a sequence may have for the first form
+constexpr int kFoldRuns = 4;      // runs that a sequence may have for the first form
 
 // The first form, for some of a channel's states: `left(s, n)` is what run s leaves of
 // state n (the first run's includes the initial state).

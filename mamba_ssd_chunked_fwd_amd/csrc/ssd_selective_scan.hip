@@ -8,7 +8,7 @@ namespace ssd {
 namespace {
 
 // The states at the starts of many runs: a lane owns one state of one channel and goes
-// through a sequence's runs, eight of them on the way at once; a workgroup has 64 channels and four of the N
+// through a sequence's runs, 16 of them on the way at once; a workgroup has 64 channels and four of the N
 // states, and every gridDim.y'th sequence.  With `back` it also goes down, through the
 // gradients at the runs' starts.
 template <int N>
@@ -21,23 +21,20 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const ScanArgs a, float*
   const bool on = d < a.dim;
   const float A2 = on ? a.in.A[d * N + n] * kLog2e : 0.0f;
   const RunGrid& g = a.runs;
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   // 64 sequences at a time: those that have more than one run
   for (int64_t i0 = blockIdx.y; i0 < g.nseq; i0 += (int64_t)gridDim.y * kWave) {
     const int64_t mine = i0 + (int64_t)gridDim.y * lane;
-    int64_t first = 0, count = 0;
+    int first = 0, count = 0;
     if (mine < g.nseq) {
-      int64_t begin, end;
       if (g.cu != nullptr) {
-        begin = seq_bound(g, mine);
-        end = seq_bound(g, mine + 1);
-        first = begin / g.run + mine;
+        const int begin = seq_bound(g, (int)mine), end = seq_bound(g, (int)mine + 1);
+        first = (int)g.by_run.of(begin) + (int)mine;
+        count = end > begin ? (int)g.by_run.of(end - begin - 1) + 1 : 0;
       } else {
-        begin = mine * (g.tokens / g.nseq);
-        end = begin + g.tokens / g.nseq;
-        first = mine * g.per_seq;
+        first = (int)mine * g.per_seq;
+        count = g.per_seq;
       }
-      count = end > begin ? (end - begin + g.run - 1) / g.run : 0;
     }
     uint64_t many = __ballot(count > 1);
     while (many != 0) {
@@ -97,15 +94,16 @@ constexpr int kBlock = 4;
 template <int N, bool BF16, bool OUT>
 __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
   const ScanPlace pl(a);
+  const int own = (int)threadIdx.x < pl.lanes ? (int)threadIdx.x : pl.lanes - 1;
+  const int64_t d = pl.channel + own;
+  float A2[N], h[N];
+  load_states<N>(a.in.A + d * N, A2);
+  const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
+  const float skip = OUT && a.in.D ? a.in.D[d] : 0.0f;
   const Run r = find_run(a.runs, pl.slot);
   if (!r.on) return;
   const bool last = r.index == r.count - 1;
   if (!OUT && last) return;
-  const int own = (int)threadIdx.x < pl.lanes ? (int)threadIdx.x : pl.lanes - 1;
-  const int64_t d = pl.channel + own;
-
-  float A2[N], h[N];
-  load_states<N>(a.in.A + d * N, A2);
 #pragma unroll
   for (int n = 0; n < N; ++n) A2[n] *= kLog2e;
 #pragma unroll
@@ -116,7 +114,7 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
     if (OUT && !last) {
       load_run<N>(a, r.first + r.count - 1, d, h);
     } else {
-      load_states<N>(a.init + (r.seq * a.dim + d) * N, h);
+      load_states<N>(a.init + ((int64_t)r.seq * a.dim + d) * N, h);
       if (!OUT && !a.joined) store_run<N>(a, r.first + r.count - 1, d, h);
     }
   } else if (OUT) {
@@ -124,8 +122,6 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
       return a.states[(s * N + n) * a.dim + d];
     });
   }
-  const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
-  const float skip = OUT && a.in.D ? a.in.D[d] : 0.0f;
   const bool gated = OUT && a.in.z != nullptr;
 
   Rows<BF16> rows(a, pl, r.begin, own, N);
@@ -193,10 +189,10 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
     if (t + kBlock < tokens) load(even, tokens - t - kBlock);
   }
   if constexpr (OUT) {
-    if (last && a.fin != nullptr) store_states<N>(a.fin + (r.seq * a.dim + d) * N, h);
+    if (last && a.fin != nullptr) store_states<N>(a.fin + ((int64_t)r.seq * a.dim + d) * N, h);
   } else {
     store_run<N>(a, pl.slot, d, h);
-    a.totals[pl.slot * a.dim + d] = (float)total;
+    a.totals[(int64_t)pl.slot * a.dim + d] = (float)total;
   }
 }
 
@@ -206,10 +202,14 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
 int64_t run_length(const ScanShape& s) {
   const int64_t blocks = s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
-  if (s.nseq * blocks >= 1024) return 4 * mean;
-  int64_t run = (s.tokens * blocks + 8191) / 8192;
+  int64_t run = s.nseq * blocks >= 1024 ? 4 * mean : (s.tokens * blocks + 8191) / 8192;
+  // where there are waves for every SIMD in any case, a run's walk (0.36 us a token, twice) is
+  // weighed against the join (0.07 us a run): the sum is least at a tenth of the tokens' root
+  int64_t least = 8;
+  while (10 * least * least < s.tokens) least += kBlock;
+  if (run < least) run = least;
   run = (run + kBlock - 1) / kBlock * kBlock;
-  return run < 32 ? 32 : run;
+  return run > INT32_MAX ? INT32_MAX / kBlock * kBlock : run;
 }
 
 struct ScanPlan {

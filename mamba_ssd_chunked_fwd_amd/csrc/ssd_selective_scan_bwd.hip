@@ -25,10 +25,11 @@ struct BwdArgs {
   float* dA_part;        // [slots, N + 2, dim]: of dA, dD and ddt_bias
   float* bc_part;        // [blocks of a group, tokens, groups, 2, N]: of dB and dC
   int64_t slots;
+  Divide by_wide, by_wide_slot;   // by the second walk's blocks of a group, and of all
 };
 
 __device__ __forceinline__ int64_t first_mark(const Run& r, int64_t slot) {
-  return r.begin / kMark + slot;
+  return (int64_t)(r.begin / kMark) + slot;
 }
 
 // The first walk, up the tokens: of each run the state that it leaves, the states inside
@@ -39,13 +40,13 @@ template <int N, bool BF16>
 __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   const ScanArgs& a = b.f;
   const ScanPlace pl(a);
-  const Run r = find_run(a.runs, pl.slot);
-  if (!r.on) return;
   const int own = (int)threadIdx.x < pl.lanes ? (int)threadIdx.x : pl.lanes - 1;
   const int64_t d = pl.channel + own;
-
   float A2[N], h[N], decay[N], back[N];
   load_states<N>(a.in.A + d * N, A2);
+  const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
+  const Run r = find_run(a.runs, pl.slot);
+  if (!r.on) return;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     A2[n] *= kLog2e;
@@ -53,8 +54,7 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
     decay[n] = 1.0f;
     back[n] = 0.0f;
   }
-  if (r.index == 0 && a.init != nullptr) load_states<N>(a.init + (r.seq * a.dim + d) * N, h);
-  const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
+  if (r.index == 0 && a.init != nullptr) load_states<N>(a.init + ((int64_t)r.seq * a.dim + d) * N, h);
   const bool gated = a.in.z != nullptr;
   Rows<BF16> rows(a, pl, r.begin, own, N);
   const int64_t dy_step = a.dim * (BF16 ? 2 : 4);
@@ -130,9 +130,9 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
     if (t + kBlock < tokens) load(even, tokens - t - kBlock);
   }
   store_run<N>(a, pl.slot, d, h);
-  a.totals[pl.slot * a.dim + d] = (float)total;
+  a.totals[(int64_t)pl.slot * a.dim + d] = (float)total;
 #pragma unroll
-  for (int n = 0; n < N; ++n) b.back[(pl.slot * N + n) * a.dim + d] = back[n];
+  for (int n = 0; n < N; ++n) b.back[((int64_t)pl.slot * N + n) * a.dim + d] = back[n];
 }
 
 // ---- the second walk, down the tokens
@@ -248,11 +248,10 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
   const ScanArgs& a = b.f;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave, q = lane % L;
-  const int wide = (a.group_dim + La::kChannels * kWaves - 1) / (La::kChannels * kWaves);
-  const int64_t per_slot = a.ngroups * wide;
-  const int64_t slot = blockIdx.x / per_slot;
-  const int rest = (int)(blockIdx.x % per_slot);
-  const int group = rest / wide, block = rest % wide;
+  const int64_t slot = b.by_wide_slot.of(blockIdx.x);
+  const uint32_t rest = blockIdx.x - (uint32_t)slot * b.by_wide_slot.d;
+  const int group = (int)b.by_wide.of(rest);
+  const int block = (int)(rest - (uint32_t)group * b.by_wide.d);
   // the lane's channels; past the group's end they stand for nothing (zeros), and read the
   // last one's rows (the last two's where they are read in pairs: a group is even then)
   const int at = (block * kWaves + wave) * La::kChannels + lane / L * 2;
@@ -261,7 +260,7 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
   const int64_t d[2] = {base + (on[0] ? at : a.group_dim - (PAIRED ? 2 : 1)),
                         base + (on[1] ? at + 1 : a.group_dim - 1)};
 
-  const Run r = find_run(a.runs, slot);
+  const Run r = find_run(a.runs, (int)slot);
   float* dA_row = b.dA_part + slot * (N + 2) * a.dim;
   if (!r.on || r.begin >= r.end) {
 #pragma unroll
@@ -272,7 +271,7 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
       if (q == 0) dA_row[N * a.dim + d[c]] = dA_row[(N + 1) * a.dim + d[c]] = 0.0f;
       // an empty sequence passes its final state's gradient on
       if (r.on && b.out.dinit != nullptr) {
-        const int64_t i = (r.seq * a.dim + d[c]) * N + 4 * q;
+        const int64_t i = ((int64_t)r.seq * a.dim + d[c]) * N + 4 * q;
         *(f32x4*)(b.out.dinit + i) =
             b.dfinal ? *(const f32x4*)(b.dfinal + i) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
       }
@@ -286,7 +285,7 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
   for (int c = 0; c < 2; ++c) {
     const f32x4 A = *(const f32x4*)(a.in.A + d[c] * N + 4 * q);
     f32x4 h = {0.0f, 0.0f, 0.0f, 0.0f}, back = h;
-    const int64_t state = (r.seq * a.dim + d[c]) * N + 4 * q;
+    const int64_t state = ((int64_t)r.seq * a.dim + d[c]) * N + 4 * q;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       A2[c][n] = A[n] * kLog2e;
@@ -609,7 +608,7 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
       dA_row[(N + 1) * a.dim + d[c]] = sb;
     }
     if (r.index == 0 && b.out.dinit != nullptr)
-      *(f32x4*)(b.out.dinit + (r.seq * a.dim + d[c]) * N + 4 * q) =
+      *(f32x4*)(b.out.dinit + ((int64_t)r.seq * a.dim + d[c]) * N + 4 * q) =
           (f32x4){R[c][0], R[c][1], R[c][2], R[c][3]};
   }
 }
@@ -623,7 +622,7 @@ __global__ __launch_bounds__(256) void scan_sum_bc_kernel(const BwdArgs b, int n
     begin = seq_bound(a.runs, 0);
     end = seq_bound(a.runs, a.runs.nseq);
   }
-  const int64_t row = 2 * n * a.ngroups, all = a.runs.tokens * row;
+  const int64_t row = 2 * n * a.ngroups, all = (int64_t)a.runs.tokens * row;
   const int64_t i = begin * row + (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= end * row) return;
   float sum = 0.0f;
@@ -643,6 +642,7 @@ __global__ __launch_bounds__(256) void scan_sum_slots_kernel(const BwdArgs b, in
   const int64_t d = (int64_t)(blockIdx.x / (n + 2)) * kWave + lane;
   float sum = 0.0f;
   if (d < a.dim)
+#pragma unroll 8
     for (int64_t s = wave; s < b.slots; s += 4) sum += b.dA_part[(s * (n + 2) + k) * a.dim + d];
   part[wave][lane] = sum;
   __syncthreads();
@@ -658,13 +658,15 @@ int64_t channel_blocks(const ScanShape& s) {
   return s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
 }
 
+constexpr int64_t kLeastRun = 24;
+
 int64_t run_length(const ScanShape& s) {
   const int64_t blocks = channel_blocks(s);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
-  if (s.nseq * blocks >= 1024) return (4 * mean + kMark - 1) / kMark * kMark;
-  int64_t run = (s.tokens * blocks + 4095) / 4096;
+  int64_t run = s.nseq * blocks >= 1024 ? 4 * mean : (s.tokens * blocks + 4095) / 4096;
   run = (run + kMark - 1) / kMark * kMark;
-  return run < 32 ? 32 : run;
+  constexpr int64_t kMost = INT32_MAX / kMark * kMark;
+  return run < kLeastRun ? kLeastRun : (run > kMost ? kMost : run);
 }
 int64_t most_slots(const ScanShape& s) { return s.tokens / run_length(s) + s.nseq; }
 int64_t most_marks(const ScanShape& s) { return s.tokens / kMark + most_slots(s) + 1; }
@@ -748,6 +750,8 @@ int launch_scan_bwd(const ScanInputs& in, const float* init, const int32_t* cu, 
   b.dfinal = dfinal;
   b.out = out;
   const int64_t blocks = channel_blocks(s), wide = wide_blocks(s);
+  b.by_wide = Divide(wide);
+  b.by_wide_slot = Divide(wide * s.ngroups);
   hipStream_t st = (hipStream_t)stream;
   switch (s.n) {
 #define SSD_SCAN(N)                                  \

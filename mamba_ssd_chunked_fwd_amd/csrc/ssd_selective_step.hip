@@ -26,14 +26,15 @@ __device__ __forceinline__ f32x4 load_four(const void* p, int64_t i) {
 }
 
 template <int N, bool BF16>
-__global__ __launch_bounds__(256) void selective_step_kernel(const ScanArgs a, int blocks) {
+__global__ __launch_bounds__(256) void selective_step_kernel(const ScanArgs a, Divide by_blocks,
+                                                             Divide by_group) {
   constexpr int L = N / 4;              // lanes of a channel
-  const int64_t b = blockIdx.x / blocks;
-  const int64_t unit = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x;
-  const bool on = unit < a.dim * L;
+  const int64_t b = by_blocks.of(blockIdx.x);
+  const int unit = (int)(blockIdx.x - (uint32_t)b * by_blocks.d) * 256 + (int)threadIdx.x;
+  const bool on = unit < (int)a.dim * L;
   const int64_t d = on ? unit / L : a.dim - 1;
-  const int n = (int)(unit % L) * 4;
-  const int64_t g = d / a.group_dim;
+  const int n = unit % L * 4;
+  const int64_t g = by_group.of((uint32_t)d);
 
   float* hp = a.fin + (b * a.dim + d) * N + n;
   f32x4 h = *(const f32x4*)hp;
@@ -77,13 +78,16 @@ int launch_scan_step(const ScanInputs& in, float* state, void* y, bool softplus,
   a.fin = state;
   const int blocks = (int)((s.dim * (s.n / 4) + 255) / 256);
   const dim3 grid((unsigned)(s.tokens * blocks));
+  const Divide by_blocks(blocks), by_group(a.group_dim);
   hipStream_t st = (hipStream_t)stream;
 #define SSD_STEP(N)                                                                              \
   case N:                                                                                        \
     if (bf16)                                                                                    \
-      hipLaunchKernelGGL((selective_step_kernel<N, true>), grid, dim3(256), 0, st, a, blocks);   \
+      hipLaunchKernelGGL((selective_step_kernel<N, true>), grid, dim3(256), 0, st, a, by_blocks, \
+                         by_group);   \
     else                                                                                         \
-      hipLaunchKernelGGL((selective_step_kernel<N, false>), grid, dim3(256), 0, st, a, blocks);  \
+      hipLaunchKernelGGL((selective_step_kernel<N, false>), grid, dim3(256), 0, st, a, by_blocks, \
+                         by_group);  \
     break
   switch (s.n) {
     SSD_STEP(8);

@@ -17,7 +17,8 @@ struct ConvArgs {
   const void* init;
   RunGrid runs;
   int64_t dim, x_stride;
-  int vectors, blocks;       // vectors of a row, workgroups of a row
+  int vectors;               // vectors of a row
+  Divide by_blocks;          // by the workgroups of a row
   void *y, *fin;
   // gradients
   const void *dy, *dfinal;
@@ -27,32 +28,52 @@ struct ConvArgs {
   int64_t slots;
 };
 
-// V channels of a row: one 16-byte vector, or a single channel where rows do not start
-// on 16 bytes.
+// V channels of a row as they lie in memory (one vector of up to 16 bytes, or a single channel
+// where rows do not start on it), and as floats.
+template <bool BF16, int V>
+struct Vec {
+  static constexpr int kWords = V == 1 ? 1 : (BF16 ? V / 2 : V);
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (V == 1 && BF16) {
+      w[0] = ((const uint16_t*)p)[i];
+    } else if constexpr (kWords == 1) {
+      w[0] = ((const uint32_t*)p)[BF16 ? i / 2 : i];
+    } else if constexpr (kWords == 2) {
+      const u32x2 u = *(const u32x2*)((const char*)p + i * (BF16 ? 2 : 4));
+      w[0] = u[0];
+      w[1] = u[1];
+    } else {
+      const u32x4 u = *(const u32x4*)((const char*)p + i * (BF16 ? 2 : 4));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = u[k];
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if constexpr (BF16)
+        v[e] = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+      else
+        v[e] = __uint_as_float(w[e]);
+    }
+  }
+};
 template <bool BF16, int V>
 __device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = load_one<BF16>(p, i);
-  } else if constexpr (BF16) {
-    const u32x4 u = *(const u32x4*)((const uint16_t*)p + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = bf16_lo(u[k]);
-      v[2 * k + 1] = bf16_hi(u[k]);
-    }
-  } else {
-    const f32x4 u = *(const f32x4*)((const float*)p + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = u[k];
-  }
+  Vec<BF16, V> u;
+  u.load(p, i);
+  u.get(v);
 }
 template <bool BF16, int V>
 __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&v)[V]) {
   if constexpr (V == 1) {
     store_one<BF16>(p, i, v[0]);
-  } else if constexpr (BF16) {
+  } else if constexpr (BF16 && V == 8) {
     *(u32x4*)((uint16_t*)p + i) = (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
                                           pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+  } else if constexpr (BF16) {
+    *(u32x2*)((uint16_t*)p + i) = (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
   } else {
     *(f32x4*)((float*)p + i) = (f32x4){v[0], v[1], v[2], v[3]};
   }
@@ -82,21 +103,29 @@ __device__ __forceinline__ void load_row(const ConvArgs& a, const Run& r, int64_
   if (t >= r.seq_begin)
     load_vec<BF16, V>(a.x, t * a.x_stride + d, v);
   else if (a.init != nullptr)
-    load_vec<BF16, V>(a.init, (r.seq * (W - 1) + (t - r.seq_begin + W - 1)) * a.dim + d, v);
+    load_vec<BF16, V>(a.init, ((int64_t)r.seq * (W - 1) + (t - r.seq_begin + W - 1)) * a.dim + d, v);
   else
     zero(v);
 }
 
-constexpr int kTokens = 4;   // tokens whose loads are under way at once
+constexpr int kTokens = 4;   // tokens of a block; one is on the way while another is worked on
 
 // One run of one sequence for V channels a thread.
 template <int W, bool BF16, int V, bool SILU>
 __global__ __launch_bounds__(256) void short_conv_fwd_kernel(const ConvArgs a) {
-  const int64_t slot = blockIdx.x / a.blocks;
-  const int vec = (int)(blockIdx.x % a.blocks) * (int)blockDim.x + threadIdx.x;
-  const Run r = find_run(a.runs, slot);
+  const int64_t slot = a.by_blocks.of(blockIdx.x);
+  const int vec = (int)(blockIdx.x - (uint32_t)slot * a.by_blocks.d) * (int)blockDim.x + threadIdx.x;
+  const Run r = find_run(a.runs, (int)slot);
   if (!r.on || vec >= a.vectors) return;
   const int64_t d = (int64_t)vec * V;
+  // the next block's rows (those past the end read the last one's)
+  auto load = [&](Vec<BF16, V>(&x)[kTokens], int t0) {
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j)
+      x[j].load(a.x, (t0 + j < r.end ? t0 + j : r.end - 1) * a.x_stride + d);
+  };
+  Vec<BF16, V> even[kTokens], odd[kTokens];
+  if (r.begin < r.end) load(even, r.begin);
   float w[W][V], bias[V], ext[W - 1][V], old[W - 1][V];
   load_taps<W, V>(a, d, w, bias);
 #pragma unroll
@@ -105,31 +134,36 @@ __global__ __launch_bounds__(256) void short_conv_fwd_kernel(const ConvArgs a) {
 #pragma unroll
     for (int e = 0; e < V; ++e) old[k][e] = ext[k][e];
   }
-  for (int64_t t0 = r.begin; t0 < r.end; t0 += kTokens) {
-    float x[kTokens][V];
-#pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-      const int64_t t = t0 + j < r.end ? t0 + j : r.end - 1;
-      load_vec<BF16, V>(a.x, t * a.x_stride + d, x[j]);
-    }
+  auto work = [&](const Vec<BF16, V>(&x)[kTokens], int t0) {
 #pragma unroll
     for (int j = 0; j < kTokens; ++j) {
       if (t0 + j >= r.end) break;
-      float y[V];
+      float y[V], now[V];
+      x[j].get(now);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float v = bias[e];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) v = __builtin_fmaf(w[k][e], ext[k][e], v);
-        v = __builtin_fmaf(w[W - 1][e], x[j][e], v);
+        v = __builtin_fmaf(w[W - 1][e], now[e], v);
         y[e] = SILU ? v * sigmoid_f(v) : v;
 #pragma unroll
         for (int k = 0; k < W - 2; ++k) ext[k][e] = ext[k + 1][e];
-        ext[W - 2][e] = x[j][e];
+        ext[W - 2][e] = now[e];
       }
-      store_vec<BF16, V>(a.y, (t0 + j) * a.dim + d, y);
+      store_vec<BF16, V>(a.y, (int64_t)(t0 + j) * a.dim + d, y);
     }
+  };
+  int t0 = r.begin;
+  for (; t0 + 2 * kTokens < r.end; t0 += 2 * kTokens) {
+    load(odd, t0 + kTokens);
+    work(even, t0);
+    load(even, t0 + 2 * kTokens);
+    work(odd, t0 + kTokens);
   }
+  if (t0 + kTokens < r.end) load(odd, t0 + kTokens);
+  if (t0 < r.end) work(even, t0);
+  if (t0 + kTokens < r.end) work(odd, t0 + kTokens);
   // The final state comes from the first run, which alone has read the initial one
   // (they may be one buffer).
   if (r.index == 0 && a.fin != nullptr) {
@@ -148,7 +182,7 @@ __global__ __launch_bounds__(256) void short_conv_fwd_kernel(const ConvArgs a) {
           for (int k = j + 1; k < W - 1; ++k) v[e] = j + len == k ? old[k][e] : v[e];
         }
       }
-      store_vec<BF16, V>(a.fin, (r.seq * (W - 1) + j) * a.dim + d, v);
+      store_vec<BF16, V>(a.fin, ((int64_t)r.seq * (W - 1) + j) * a.dim + d, v);
     }
   }
 }
@@ -157,9 +191,9 @@ __global__ __launch_bounds__(256) void short_conv_fwd_kernel(const ConvArgs a) {
 // goes W-1 tokens past its end.
 template <int W, bool BF16, int V, bool SILU>
 __global__ __launch_bounds__(256) void short_conv_bwd_kernel(const ConvArgs a) {
-  const int64_t slot = blockIdx.x / a.blocks;
-  const int vec = (int)(blockIdx.x % a.blocks) * (int)blockDim.x + threadIdx.x;
-  const Run r = find_run(a.runs, slot);
+  const int64_t slot = a.by_blocks.of(blockIdx.x);
+  const int vec = (int)(blockIdx.x - (uint32_t)slot * a.by_blocks.d) * (int)blockDim.x + threadIdx.x;
+  const Run r = find_run(a.runs, (int)slot);
   if (vec >= a.vectors) return;
   const int64_t d = (int64_t)vec * V;
   float dw[W][V], db[V];
@@ -180,46 +214,54 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(const ConvArgs a) {
       if (token ? t < r.begin || t >= r.end : r.index != 0 || a.dinit == nullptr) return;
       if (j >= 0 && a.dfinal != nullptr) {
         float f[V];
-        load_vec<BF16, V>(a.dfinal, (r.seq * (W - 1) + j) * a.dim + d, f);
+        load_vec<BF16, V>(a.dfinal, ((int64_t)r.seq * (W - 1) + j) * a.dim + d, f);
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] += f[e];
       }
       if (token)
         store_vec<BF16, V>(a.dx, t * a.dim + d, v);
       else
-        store_vec<BF16, V>(a.dinit, (r.seq * (W - 1) + (t - r.seq_begin + W - 1)) * a.dim + d, v);
+        store_vec<BF16, V>(a.dinit, ((int64_t)r.seq * (W - 1) + (t - r.seq_begin + W - 1)) * a.dim + d, v);
     };
-    int64_t past = r.end + W - 1 < r.seq_end ? r.end + W - 1 : r.seq_end;
-    if (r.begin >= r.end) past = r.begin;
-    for (int64_t t0 = r.begin; t0 < past; t0 += kTokens) {
-      float x[kTokens][V], dy[kTokens][V];
+    const int past = r.begin >= r.end ? r.begin
+                                      : (r.seq_end - r.end < W - 1 ? r.seq_end : r.end + W - 1);
+    struct Rows {
+      Vec<BF16, V> x, dy;
+    } even[kTokens], odd[kTokens];
+    auto load = [&](Rows(&b)[kTokens], int t0) {
 #pragma unroll
       for (int j = 0; j < kTokens; ++j) {
         const int64_t t = t0 + j < past ? t0 + j : past - 1;
-        load_vec<BF16, V>(a.x, t * a.x_stride + d, x[j]);
-        load_vec<BF16, V>(a.dy, t * a.dim + d, dy[j]);
+        b[j].x.load(a.x, t * a.x_stride + d);
+        b[j].dy.load(a.dy, t * a.dim + d);
       }
+    };
+    auto work = [&](const Rows(&b)[kTokens], int t0) {
 #pragma unroll
       for (int j = 0; j < kTokens; ++j) {
-        const int64_t t = t0 + j;
+        const int t = t0 + j;
         if (t >= past) break;
+        float g[V];
+        b[j].x.get(ext[W - 1]);
+        b[j].dy.get(g);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          ext[W - 1][e] = x[j][e];
-          float g = dy[j][e];
           if (SILU) {
             float v = bias[e];
 #pragma unroll
             for (int k = 0; k < W; ++k) v = __builtin_fmaf(w[k][e], ext[k][e], v);
             const float s = sigmoid_f(v);
-            g *= s * __builtin_fmaf(v, 1.0f - s, 1.0f);
+            g[e] *= s * __builtin_fmaf(v, 1.0f - s, 1.0f);
           }
 #pragma unroll
-          for (int k = 0; k < W; ++k) acc[k][e] = __builtin_fmaf(w[k][e], g, acc[k][e]);
-          if (t < r.end) {
-            db[e] += g;
+          for (int k = 0; k < W; ++k) acc[k][e] = __builtin_fmaf(w[k][e], g[e], acc[k][e]);
+        }
+        if (t < r.end) {     // (past it a token counts for the rows before it alone)
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][e] = __builtin_fmaf(g, ext[k][e], dw[k][e]);
+          for (int e = 0; e < V; ++e) {
+            db[e] += g[e];
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k][e] = __builtin_fmaf(g[e], ext[k][e], dw[k][e]);
           }
         }
         emit(t - (W - 1), acc[0]);
@@ -233,7 +275,18 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(const ConvArgs a) {
         }
         zero(acc[W - 1]);
       }
+    };
+    int t0 = r.begin;
+    if (t0 < past) load(even, t0);
+    for (; t0 + 2 * kTokens < past; t0 += 2 * kTokens) {
+      load(odd, t0 + kTokens);
+      work(even, t0);
+      load(even, t0 + 2 * kTokens);
+      work(odd, t0 + kTokens);
     }
+    if (t0 + kTokens < past) load(odd, t0 + kTokens);
+    if (t0 < past) work(even, t0);
+    if (t0 + kTokens < past) work(odd, t0 + kTokens);
     if (past == r.seq_end) {
 #pragma unroll
       for (int k = 0; k < W - 1; ++k) emit(past - (W - 1) + k, acc[k]);
@@ -265,6 +318,7 @@ __global__ __launch_bounds__(kWave * kSumWaves) void short_conv_sum_kernel(const
   const int64_t d = (int64_t)(blockIdx.x / (width + 1)) * kWave + lane;
   float sum = 0.0f;
   if (d < a.dim)
+#pragma unroll 8
     for (int64_t s = wave; s < a.slots; s += kSumWaves)
       sum += a.part[(s * (width + 1) + k) * a.dim + d];
   part[wave][lane] = sum;
@@ -283,8 +337,8 @@ __global__ __launch_bounds__(kWave * kSumWaves) void short_conv_sum_kernel(const
 // One token of every sequence: V channels of one sequence a thread.
 template <int W, bool BF16, int V, bool SILU>
 __global__ __launch_bounds__(256) void short_conv_step_kernel(const ConvArgs a) {
-  const int64_t b = blockIdx.x / a.blocks;
-  const int vec = (int)(blockIdx.x % a.blocks) * (int)blockDim.x + threadIdx.x;
+  const int64_t b = a.by_blocks.of(blockIdx.x);
+  const int vec = (int)(blockIdx.x - (uint32_t)b * a.by_blocks.d) * (int)blockDim.x + threadIdx.x;
   if (vec >= a.vectors) return;
   const int64_t d = (int64_t)vec * V;
   float w[W][V], bias[V], ext[W][V], y[V];
@@ -340,7 +394,8 @@ template <bool B>
 using Flag = std::integral_constant<bool, B>;
 template <int I>
 using Int = std::integral_constant<int, I>;
-template <class F>
+// V: channels of a whole bf16 vector.
+template <int V, class F>
 void choose(const ConvShape& s, bool bf16, bool vec, bool silu, F f) {
   auto w = [&](auto b, auto v, auto a) {
     if (s.width == 2)
@@ -352,7 +407,7 @@ void choose(const ConvShape& s, bool bf16, bool vec, bool silu, F f) {
   };
   auto act = [&](auto b, auto v) { silu ? w(b, v, Flag<true>{}) : w(b, v, Flag<false>{}); };
   if (bf16)
-    vec ? act(Flag<true>{}, Int<8>{}) : act(Flag<true>{}, Int<1>{});
+    vec ? act(Flag<true>{}, Int<V>{}) : act(Flag<true>{}, Int<1>{});
   else
     vec ? act(Flag<false>{}, Int<4>{}) : act(Flag<false>{}, Int<1>{});
 }
@@ -387,10 +442,10 @@ int launch_short_conv_fwd(const void* x, const float* weight, const float* bias,
   a.y = y;
   a.fin = fin;
   const bool vec = whole_vectors(s, bf16) && (uintptr_t)x % 16 == 0;
-  choose(s, bf16, vec, silu, [&](auto w, auto b, auto v, auto act) {
+  choose<8>(s, bf16, vec, silu, [&](auto w, auto b, auto v, auto act) {
     const ConvGrid g = conv_grid(s, v.value);
     a.vectors = g.vectors;
-    a.blocks = g.blocks;
+    a.by_blocks = Divide(g.blocks);
     hipLaunchKernelGGL(
         (short_conv_fwd_kernel<decltype(w)::value, decltype(b)::value, decltype(v)::value,
                                decltype(act)::value>),
@@ -418,10 +473,10 @@ int launch_short_conv_bwd(const void* x, const float* weight, const float* bias,
   a.dbias = dbias;
   const bool vec = whole_vectors(s, bf16) && (uintptr_t)x % 16 == 0;
   hipStream_t st = (hipStream_t)stream;
-  choose(s, bf16, vec, silu, [&](auto w, auto b, auto v, auto act) {
+  choose<4>(s, bf16, vec, silu, [&](auto w, auto b, auto v, auto act) {
     const ConvGrid g = conv_grid(s, v.value);
     a.vectors = g.vectors;
-    a.blocks = g.blocks;
+    a.by_blocks = Divide(g.blocks);
     hipLaunchKernelGGL(
         (short_conv_bwd_kernel<decltype(w)::value, decltype(b)::value, decltype(v)::value,
                                decltype(act)::value>),
@@ -446,10 +501,10 @@ int launch_short_conv_step(const void* x, const float* weight, const float* bias
   a.y = y;
   a.fin = state;
   const bool vec = whole_vectors(s, bf16) && (uintptr_t)x % 16 == 0;
-  choose(s, bf16, vec, silu, [&](auto w, auto b, auto v, auto act) {
+  choose<8>(s, bf16, vec, silu, [&](auto w, auto b, auto v, auto act) {
     const ConvGrid g = conv_grid(s, v.value);
     a.vectors = g.vectors;
-    a.blocks = g.blocks;
+    a.by_blocks = Divide(g.blocks);
     hipLaunchKernelGGL(
         (short_conv_step_kernel<decltype(w)::value, decltype(b)::value, decltype(v)::value,
                                 decltype(act)::value>),

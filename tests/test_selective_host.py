@@ -253,18 +253,21 @@ def test_binding_rejects_cpu_tensors_and_bad_names():
 
 def test_row_strides():
     """Rows that are columns of a wider tensor, and layouts that have no one stride."""
+    def stride(t, name="x"):
+        return ssd._row_stride(name, t.shape, t.stride())
+
     wide = torch.zeros(2, 5, 96)
-    assert ssd._row_stride(wide[..., 32:64], "x") == 96
-    assert ssd._row_stride(wide[0, :, :32], "x") == 96
-    assert ssd._row_stride(wide[:, 0, :32], "x") == 5 * 96      # a batch's first tokens
-    assert ssd._row_stride(wide[:, :1, :32], "x") == 5 * 96
-    assert ssd._row_stride(wide[..., 32:64].unflatten(-1, (2, 16)), "B") == 96
-    assert ssd._row_stride(wide[0, :, 32:64].unflatten(-1, (2, 16)), "B") == 96
+    assert stride(wide[..., 32:64]) == 96
+    assert stride(wide[0, :, :32]) == 96
+    assert stride(wide[:, 0, :32]) == 5 * 96      # a batch's first tokens
+    assert stride(wide[:, :1, :32]) == 5 * 96
+    assert stride(wide[..., 32:64].unflatten(-1, (2, 16)), "B") == 96
+    assert stride(wide[0, :, 32:64].unflatten(-1, (2, 16)), "B") == 96
     for bad in (wide[:, :3], wide.transpose(1, 2), wide[..., ::2], wide[:1, :1].expand(2, 5, 96)):
         with pytest.raises(ValueError, match="pass a copy"):
-            ssd._row_stride(bad, "x")
+            stride(bad)
     with pytest.raises(ValueError, match="pass a copy"):
-        ssd._row_stride(wide.unflatten(-1, (2, 48))[..., :16], "B")
+        stride(wide.unflatten(-1, (2, 48))[..., :16], "B")
 
 
 def conv_inputs():
