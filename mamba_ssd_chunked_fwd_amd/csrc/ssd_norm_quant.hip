@@ -56,6 +56,10 @@ struct Eight {
       }
     }
   }
+  __device__ __forceinline__ void fill(uint32_t v) {
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 4 : 8); ++k) w[k] = v;
+  }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (BF16) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
     return __uint_as_float(w[e]);
@@ -121,7 +125,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const 
   const int waves = (int)blockDim.x / kWave;
   const double top = E4M3 ? 448.0 : 127.0;
 
-  // a lane's channels: their scale, weight and the next row's values
+  // a lane's channels: their scale, weight and the next row's values.  What is not there, and
+  // lanes past the row's end, have ones and zeros, so nothing below asks for them.
   Eight<false, WHOLE> s[NV], w[NV];
   Eight<XBF16, WHOLE> x[NV];
   Eight<RBF16, WHOLE> r[NV];
@@ -135,6 +140,13 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const 
       if (a.res) r[j].load(a.res, row * a.dim + c, a.dim - c);
     }
   };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    x[j].fill(0);
+    r[j].fill(0);
+    s[j].fill(__float_as_uint(1.0f));
+    w[j].fill(__float_as_uint(1.0f));
+  }
   // Rows of one vector a lane are read a row ahead, and scales and weights once; two vectors
   // do not leave the registers for it.
   constexpr bool kAhead = NV == 1;
@@ -167,9 +179,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const 
       float rounded[kVec];
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        const double in = x[j].get(e), old = a.res ? (double)r[j].get(e) : 0.0;
-        double v = a.scale ? __builtin_fma((double)s[j].get(e), in, old) : in + old;
-        if (c + (WHOLE ? 0 : e) >= a.dim) v = 0.0;
+        const double v = __builtin_fma((double)s[j].get(e), (double)x[j].get(e),
+                                       (double)r[j].get(e));
         sum = __builtin_fma(v, v, sum);
         rounded[e] = (float)v;
         h[j][e] = v;
@@ -185,10 +196,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void add_norm_quant_kernel(const 
       most[j] = 0.0;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        if (a.weight) {
-          h[j][e] *= (double)w[j].get(e);
-          if (channel(j) + (WHOLE ? 0 : e) >= a.dim) h[j][e] = 0.0;
-        }
+        h[j][e] *= (double)w[j].get(e);
         most[j] = __builtin_fmax(most[j], __builtin_fabs(h[j][e]));
         bad = __builtin_fma(h[j][e], 0.0, bad);
       }
@@ -275,8 +283,8 @@ int launch_add_norm_quant(const void* x, const void* res, const float* scale, co
   const int vectors = (int)((dim + kVec - 1) / kVec);
   const int nv = vectors > kMaxWaves * kWave ? 2 : 1;
   const int waves = (vectors + nv * kWave - 1) / (nv * kWave);
-  // 16 waves per CU
-  const int64_t most = 4096 / waves;
+  // as many whole workgroups for each of the 256 CUs as its registers hold (20 waves)
+  const int64_t most = 256 * (waves > 20 ? 1 : 20 / waves);
   const int blocks = (int)(rows < most ? rows : most);
   const bool grouped = group == 16 || group == 32 || group == 64 || group == 128 || group == 256;
   const bool whole = dim % kVec == 0;

@@ -93,8 +93,6 @@ __device__ __forceinline__ void store_states(float* p, const float (&v)[N]) {
 template <int N, bool BF16>
 struct States {
   static constexpr int kWords = BF16 ? N / 2 : N;
-  // short ones are read a token ahead; the others would not leave enough scalar registers
-  static constexpr bool kAhead = kWords <= 8;
   uint32_t w[kWords];
   States() = default;
   __device__ __forceinline__ explicit States(const void* p) {
@@ -114,10 +112,14 @@ struct States {
   }
 };
 
-// B and C (or B alone) of the tokens of a run, one after the other.
-template <int N, bool BF16, bool BOTH>
+// B and C (or B alone) of the tokens of a run, one after the other, in pieces of 32 bytes, each piece read while the one before it is worked on: more would not leave
+// enough scalar registers.
+template <int NS, bool BF16, bool BOTH>
 struct StateRows {
-  typedef States<N, BF16> S;
+  static constexpr int kMost = BF16 ? 16 : 8;
+  static constexpr int kPiece = NS < kMost ? NS : kMost, kPieces = NS / kPiece;
+  static constexpr int kBytes = kPiece * (BF16 ? 2 : 4);
+  typedef States<kPiece, BF16> S;
   const char *b, *c;
   int64_t b_step, c_step;
   int left;
@@ -125,26 +127,27 @@ struct StateRows {
   __device__ __forceinline__ StateRows(const char* b_, const char* c_, int64_t bs, int64_t cs,
                                        int tokens)
       : b(b_), c(c_), b_step(bs), c_step(cs), left(tokens) {
-    if (S::kAhead && tokens > 0) read(nb, nc);
+    if (tokens > 0) read(0);
   }
-  __device__ __forceinline__ void read(S& B, S& C) {
+  __device__ __forceinline__ void read(int k) {
     // (keeps the reads of many tokens from gathering and filling the scalar registers)
     asm volatile("" : "+s"(b));
     if (BOTH) asm volatile("" : "+s"(c));
-    B = S(b);
-    if (BOTH) C = S(c);
-    if (--left > 0) {       // (the row behind the last one need not exist)
-      b += b_step;
-      c += c_step;
-    }
+    nb = S(b + k * kBytes);
+    if (BOTH) nc = S(c + k * kBytes);
   }
-  __device__ __forceinline__ void next(S& B, S& C) {
-    if constexpr (S::kAhead) {
-      B = nb;
-      C = nc;
-      read(nb, nc);
+  // Piece k of the present token; behind the last one comes the next token.
+  __device__ __forceinline__ void next(int k, S& B, S& C) {
+    B = nb;
+    C = nc;
+    if (k + 1 < kPieces) {
+      read(k + 1);
     } else {
-      read(B, C);
+      if (--left > 0) {       // (the row behind the last one need not exist)
+        b += b_step;
+        c += c_step;
+      }
+      read(0);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -157,8 +160,9 @@ struct Rows {
   const char *x, *dt, *z, *B, *C;
   int64_t x_step, dt_step, z_step, b_step, c_step;   // bytes between rows
   uint32_t lane;
+  // n: states of a group, from which the n0'th on are wanted
   __device__ __forceinline__ Rows(const ScanArgs& a, const ScanPlace& pl, int64_t t, int own,
-                                  int n) {
+                                  int n, int n0) {
     constexpr int el = BF16 ? 2 : 4;
     x_step = a.x_stride * el;
     dt_step = a.dt_stride * el;
@@ -169,8 +173,8 @@ struct Rows {
     dt = (const char*)a.in.dt + pl.channel * el + t * dt_step;
     // (without a gate rows of x are read in the place of z's, and not used)
     z = (const char*)(a.in.z ? a.in.z : a.in.x) + pl.channel * el + t * z_step;
-    B = (const char*)a.in.B + (int64_t)pl.group * n * el + t * b_step;
-    C = (const char*)a.in.C + (int64_t)pl.group * n * el + t * c_step;
+    B = (const char*)a.in.B + ((int64_t)pl.group * n + n0) * el + t * b_step;
+    C = (const char*)a.in.C + ((int64_t)pl.group * n + n0) * el + t * c_step;
     lane = (uint32_t)own * el;
   }
 };
@@ -205,11 +209,12 @@ __device__ __forceinline__ void store_raw(char* row, uint32_t lane, float v) {
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), row_rsrc(row), (int)lane, 0, 0);
 }
 
-template <int N>
-__device__ __forceinline__ void store_run(const ScanArgs& a, int64_t slot, int64_t d,
-                                          const float (&h)[N]) {
+// NS of the N states of a channel in a slot's record, from the n0'th on.
+template <int N, int NS>
+__device__ __forceinline__ void store_run(float* to, const ScanArgs& a, int64_t slot, int64_t d,
+                                          int n0, const float (&h)[NS]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) a.states[(slot * N + n) * a.dim + d] = h[n];
+  for (int n = 0; n < NS; ++n) to[(slot * N + n0 + n) * a.dim + d] = h[n];
 }
 template <int N>
 __device__ __forceinline__ void load_run(const ScanArgs& a, int64_t slot, int64_t d,

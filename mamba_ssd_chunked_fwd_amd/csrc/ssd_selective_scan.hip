@@ -91,13 +91,16 @@ constexpr int kBlock = 4;
 //   OUT: outputs, from the state that the runs before it leave
 //   else: the state that the run leaves (from zeros, the first run from the initial state)
 // Lanes past the group's end do what its last channel's lane does, and store the same.
-template <int N, bool BF16, bool OUT>
-__global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
+// Outputs need all N states of a channel; without, a wave takes NS of them (blockIdx.y).
+template <int N, int NS, bool BF16, bool OUT>
+__global__ __launch_bounds__(kWave, NS == 64 ? 2 : 1) void scan_kernel(const ScanArgs a) {
+  static_assert(!OUT || NS == N, "outputs are sums over the states");
   const ScanPlace pl(a);
+  const int n0 = OUT ? 0 : (int)blockIdx.y * NS;
   const int own = (int)threadIdx.x < pl.lanes ? (int)threadIdx.x : pl.lanes - 1;
   const int64_t d = pl.channel + own;
-  float A2[N], h[N];
-  load_states<N>(a.in.A + d * N, A2);
+  float A2[NS], h[NS];
+  load_states<NS>(a.in.A + d * N + n0, A2);
   const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
   const float skip = OUT && a.in.D ? a.in.D[d] : 0.0f;
   const Run r = find_run(a.runs, pl.slot);
@@ -105,30 +108,35 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
   const bool last = r.index == r.count - 1;
   if (!OUT && last) return;
 #pragma unroll
-  for (int n = 0; n < N; ++n) A2[n] *= kLog2e;
-#pragma unroll
-  for (int n = 0; n < N; ++n) h[n] = 0.0f;
-  if (OUT && a.joined && r.count > 1) {
-    load_run<N>(a, pl.slot, d, h);
-  } else if (r.index == 0 && a.init != nullptr) {
-    if (OUT && !last) {
-      load_run<N>(a, r.first + r.count - 1, d, h);
-    } else {
-      load_states<N>(a.init + ((int64_t)r.seq * a.dim + d) * N, h);
-      if (!OUT && !a.joined) store_run<N>(a, r.first + r.count - 1, d, h);
+  for (int n = 0; n < NS; ++n) {
+    A2[n] *= kLog2e;
+    h[n] = 0.0f;
+  }
+  if constexpr (OUT) {
+    if (a.joined && r.count > 1) {
+      load_run<N>(a, pl.slot, d, h);
+    } else if (r.index > 0) {
+      fold_runs<N>(a, r.first, pl.slot, d, A2, h, [&](int64_t s, int n) {
+        return a.states[(s * N + n) * a.dim + d];
+      });
+    } else if (a.init != nullptr) {
+      if (last)
+        load_states<N>(a.init + ((int64_t)r.seq * a.dim + d) * N, h);
+      else
+        load_run<N>(a, r.first + r.count - 1, d, h);
     }
-  } else if (OUT) {
-    fold_runs<N>(a, r.first, pl.slot, d, A2, h, [&](int64_t s, int n) {
-      return a.states[(s * N + n) * a.dim + d];
-    });
+  } else if (r.index == 0 && a.init != nullptr) {
+    load_states<NS>(a.init + ((int64_t)r.seq * a.dim + d) * N + n0, h);
+    if (!a.joined) store_run<N>(a.states, a, r.first + r.count - 1, d, n0, h);
   }
   const bool gated = OUT && a.in.z != nullptr;
 
-  Rows<BF16> rows(a, pl, r.begin, own, N);
+  Rows<BF16> rows(a, pl, r.begin, own, N, n0);
   const int64_t y_step = a.dim * (BF16 ? 2 : 4);
   char* y = OUT ? (char*)a.y + pl.channel * (BF16 ? 2 : 4) + r.begin * y_step : nullptr;
   const int tokens = (int)(r.end - r.begin);    // (fewer than 2^31)
-  StateRows<N, BF16, OUT> bc(rows.B, rows.C, rows.b_step, rows.c_step, tokens);
+  typedef StateRows<NS, BF16, OUT> Bc;
+  Bc bc(rows.B, rows.C, rows.b_step, rows.c_step, tokens);
   double total = 0.0;
   typedef typename Raw<BF16>::type raw;
   struct Block {
@@ -152,26 +160,27 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
 #pragma unroll
     for (int j = 0; j < kBlock; ++j) {
       if (j >= left) break;
-      States<N, BF16> B, C;
-      bc.next(B, C);
       const float v = Raw<BF16>::get(b.dt[j]) + bias;
       const float delta = pick(a.softplus, softplus_f(v), v);
       const float x = Raw<BF16>::get(b.x[j]), dx = delta * x;
-      if constexpr (OUT) {
-        float u[2] = {skip * x, 0.0f};
+      float u[2] = {skip * x, 0.0f};
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          h[n] = __builtin_fmaf(exp2_hw(delta * A2[n]), h[n], dx * B[n]);
-          u[n & 1] = __builtin_fmaf(C[n], h[n], u[n & 1]);
+      for (int k = 0; k < Bc::kPieces; ++k) {
+        typename Bc::S B, C;
+        bc.next(k, B, C);
+#pragma unroll
+        for (int i = 0; i < Bc::kPiece; ++i) {
+          const int n = k * Bc::kPiece + i;
+          h[n] = __builtin_fmaf(exp2_hw(delta * A2[n]), h[n], dx * B[i]);
+          if (OUT) u[n & 1] = __builtin_fmaf(C[i], h[n], u[n & 1]);
         }
+      }
+      if constexpr (OUT) {
         const float z = Raw<BF16>::get(b.z[j]), out = u[0] + u[1];
         store_raw<BF16>(y, rows.lane, pick(gated, out * (z * sigmoid_f(z)), out));
         y += y_step;
       } else {
         total += delta;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          h[n] = __builtin_fmaf(exp2_hw(delta * A2[n]), h[n], dx * B[n]);
       }
     }
   };
@@ -191,7 +200,7 @@ __global__ __launch_bounds__(kWave) void scan_kernel(const ScanArgs a) {
   if constexpr (OUT) {
     if (last && a.fin != nullptr) store_states<N>(a.fin + ((int64_t)r.seq * a.dim + d) * N, h);
   } else {
-    store_run<N>(a, pl.slot, d, h);
+    store_run<N>(a.states, a, pl.slot, d, n0, h);
     a.totals[(int64_t)pl.slot * a.dim + d] = (float)total;
   }
 }
@@ -243,10 +252,12 @@ template <int N, bool BF16>
 int launch_n(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
   const dim3 grid((unsigned)(p.slots * p.blocks));
   if (p.split) {
-    hipLaunchKernelGGL((scan_kernel<N, BF16, false>), grid, dim3(kWave), 0, st, a);
+    constexpr int NS = N < 32 ? N : 32;
+    hipLaunchKernelGGL((scan_kernel<N, NS, BF16, false>), dim3(grid.x, N / NS), dim3(kWave), 0,
+                       st, a);
     if (a.joined) launch_scan_join(a, N, nullptr, nullptr, st);
   }
-  hipLaunchKernelGGL((scan_kernel<N, BF16, true>), grid, dim3(kWave), 0, st, a);
+  hipLaunchKernelGGL((scan_kernel<N, N, BF16, true>), grid, dim3(kWave), 0, st, a);
   return (int)hipGetLastError();
 }
 

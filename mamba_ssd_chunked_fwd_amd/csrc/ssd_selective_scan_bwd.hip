@@ -36,32 +36,36 @@ __device__ __forceinline__ int64_t first_mark(const Run& r, int64_t slot) {
 // it, and the gradient that its outputs give the state at its start,
 //   sum_t (prod_{s<=t} exp(delta_s A)) C_t du_t
 // Lanes past the group's end do what its last channel's lane does, and store the same.
-template <int N, bool BF16>
+// A wave takes NS of a channel's N states (blockIdx.y).
+template <int N, int NS, bool BF16>
 __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   const ScanArgs& a = b.f;
   const ScanPlace pl(a);
+  const int n0 = (int)blockIdx.y * NS;
   const int own = (int)threadIdx.x < pl.lanes ? (int)threadIdx.x : pl.lanes - 1;
   const int64_t d = pl.channel + own;
-  float A2[N], h[N], decay[N], back[N];
-  load_states<N>(a.in.A + d * N, A2);
+  float A2[NS], h[NS], decay[NS], back[NS];
+  load_states<NS>(a.in.A + d * N + n0, A2);
   const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
   const Run r = find_run(a.runs, pl.slot);
   if (!r.on) return;
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
+  for (int n = 0; n < NS; ++n) {
     A2[n] *= kLog2e;
     h[n] = 0.0f;
     decay[n] = 1.0f;
     back[n] = 0.0f;
   }
-  if (r.index == 0 && a.init != nullptr) load_states<N>(a.init + ((int64_t)r.seq * a.dim + d) * N, h);
+  if (r.index == 0 && a.init != nullptr)
+    load_states<NS>(a.init + ((int64_t)r.seq * a.dim + d) * N + n0, h);
   const bool gated = a.in.z != nullptr;
-  Rows<BF16> rows(a, pl, r.begin, own, N);
+  Rows<BF16> rows(a, pl, r.begin, own, N, n0);
   const int64_t dy_step = a.dim * (BF16 ? 2 : 4);
   const char* dy = (const char*)b.dy + pl.channel * (BF16 ? 2 : 4) + r.begin * dy_step;
   const int64_t mark0 = first_mark(r, pl.slot);
   const int tokens = (int)(r.end - r.begin);
-  StateRows<N, BF16, true> bc(rows.B, rows.C, rows.b_step, rows.c_step, tokens);
+  typedef StateRows<NS, BF16, true> Bc;
+  Bc bc(rows.B, rows.C, rows.b_step, rows.c_step, tokens);
   double total = 0.0;
   constexpr int kBlock = 4;
   static_assert(kMark == 2 * kBlock, "marks lie between pairs of blocks");
@@ -88,7 +92,7 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
     const int64_t m = mark0 + t / kMark;
     int64_t step = a.dim;
     asm("" : "+s"(step));      // (its multiples would stay in scalar registers)
-    float* p = b.marks + m * N * step + d;
+    float* p = b.marks + (m * N + n0) * step + d;
 #pragma unroll
     for (int n = 0; n < N; ++n, p += step) *p = h[n];
     b.mark_totals[m * step + d] = (float)total;
@@ -97,8 +101,6 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
 #pragma unroll
     for (int j = 0; j < kBlock; ++j) {
       if (j >= left) break;
-      States<N, BF16> B, C;
-      bc.next(B, C);
       const float v = Raw<BF16>::get(k.dt[j]) + bias;
       const float delta = pick(a.softplus, softplus_f(v), v);
       const float dx = delta * Raw<BF16>::get(k.x[j]);
@@ -106,11 +108,17 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
       const float g = pick(gated, dy * (z * sigmoid_f(z)), dy);
       total += delta;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float e = exp2_hw(delta * A2[n]);
-        h[n] = __builtin_fmaf(e, h[n], dx * B[n]);
-        decay[n] *= e;
-        back[n] = __builtin_fmaf(decay[n], C[n] * g, back[n]);
+      for (int p = 0; p < Bc::kPieces; ++p) {
+        typename Bc::S B, C;
+        bc.next(p, B, C);
+#pragma unroll
+        for (int i = 0; i < Bc::kPiece; ++i) {
+          const int n = p * Bc::kPiece + i;
+          const float e = exp2_hw(delta * A2[n]);
+          h[n] = __builtin_fmaf(e, h[n], dx * B[i]);
+          decay[n] *= e;
+          back[n] = __builtin_fmaf(decay[n], C[i] * g, back[n]);
+        }
       }
     }
   };
@@ -129,10 +137,9 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
     work(even, tokens - t);
     if (t + kBlock < tokens) load(even, tokens - t - kBlock);
   }
-  store_run<N>(a, pl.slot, d, h);
+  store_run<N>(a.states, a, pl.slot, d, n0, h);
+  store_run<N>(b.back, a, pl.slot, d, n0, back);
   a.totals[(int64_t)pl.slot * a.dim + d] = (float)total;
-#pragma unroll
-  for (int n = 0; n < N; ++n) b.back[((int64_t)pl.slot * N + n) * a.dim + d] = back[n];
 }
 
 // ---- the second walk, down the tokens
@@ -236,7 +243,7 @@ __device__ __forceinline__ void wave_sync() {
 constexpr int kBatch = 4;      // tokens whose dB and dC are summed over a wave's lanes at once
 
 template <int N, bool BF16, bool PAIRED>
-__global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdArgs b) {
+__global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kernel(const BwdArgs b) {
   using La = Lanes<N>;
   constexpr int L = La::L, OWN = La::kOwn, TURNS = La::kTurns;
   constexpr int el = BF16 ? 2 : 4;
@@ -453,6 +460,8 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
     };
+    // The decays of the last tokens wait in LDS, where their dB and dC will lie; those of the
+    // first are formed again.
     auto up = [&](auto jj) {
       constexpr int j = decltype(jj)::value;
       const f32x4 B = bc_in[turn][j][0][q];
@@ -460,12 +469,15 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
       for (int c = 0; c < 2; ++c) {
         const float dl = La::template bcast<j % TURNS>(delta[j / TURNS][c]);
         const float dxj = La::template bcast<j % TURNS>(dx[j / TURNS][c]);
+        f32x4 decay;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          float v = __builtin_fmaf(exp2_hw(dl * A2[c][n]), h[j][c][n], dxj * B[n]);
+          decay[n] = exp2_hw(dl * A2[c][n]);
+          float v = __builtin_fmaf(decay[n], h[j][c][n], dxj * B[n]);
           asm volatile("" : "+v"(v));      // (formed here, not where it is used)
           h[j + 1][c][n] = v;
         }
+        if (j >= kMark - kBatch) values[wave][j % kBatch][c][lane] = decay;
       }
       fence();
     };
@@ -477,11 +489,21 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
     auto down = [&](auto jj) {
       constexpr int j = decltype(jj)::value, i = j / TURNS;
       const f32x4 B = bc_in[turn][j][0][q], C = bc_in[turn][j][1][q];
-      f32x4 vB, vC;
+      f32x4 vB, vC, decay[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float dl = La::template bcast<j % TURNS>(delta[i][c]);
-        asm volatile("" : "+v"(dl));     // (its products are formed again, not kept)
+        if (j >= kMark - kBatch) {
+          decay[c] = values[wave][j % kBatch][c][lane];
+        } else {
+          float dl = La::template bcast<j % TURNS>(delta[i][c]);
+          asm volatile("" : "+v"(dl));     // (its products are formed again, not kept)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) decay[c][n] = exp2_hw(dl * A2[c][n]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float dl = La::template bcast<j % TURNS>(delta[i][c]);
         const float dxj = La::template bcast<j % TURNS>(dx[i][c]);
         const float duj = La::template bcast<j % TURNS>(du[i][c]);
         float in = 0.0f, dd = 0.0f, uu = 0.0f;
@@ -492,7 +514,7 @@ __global__ __launch_bounds__(kWave * kWaves, 2) void scan_bwd_kernel(const BwdAr
           vB[n] = c ? __builtin_fmaf(dxj, dh, vB[n]) : dxj * dh;
           in = __builtin_fmaf(B[n], dh, in);
           uu = __builtin_fmaf(C[n], h[j + 1][c][n], uu);
-          R[c][n] = dh * exp2_hw(dl * A2[c][n]);
+          R[c][n] = dh * decay[c][n];
           const float kept = R[c][n] * h[j][c][n];
           dd = __builtin_fmaf(kept, A2[c][n], dd);
           dA[c][n] = __builtin_fmaf(kept, dl, dA[c][n]);
@@ -663,7 +685,7 @@ constexpr int64_t kLeastRun = 24;
 int64_t run_length(const ScanShape& s) {
   const int64_t blocks = channel_blocks(s);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
-  int64_t run = s.nseq * blocks >= 1024 ? 4 * mean : (s.tokens * blocks + 4095) / 4096;
+  int64_t run = s.nseq * blocks >= 2048 ? 4 * mean : (s.tokens * blocks + 4095) / 4096;
   run = (run + kMark - 1) / kMark * kMark;
   constexpr int64_t kMost = INT32_MAX / kMark * kMark;
   return run < kLeastRun ? kLeastRun : (run > kMost ? kMost : run);
@@ -705,8 +727,9 @@ BwdLayout layout(const ScanShape& s) {
 
 template <int N, bool BF16>
 void launch_n(const BwdArgs& b, int64_t blocks, int64_t wide, hipStream_t st) {
-  hipLaunchKernelGGL((scan_local_kernel<N, BF16>), dim3((unsigned)(b.slots * blocks)),
-                     dim3(kWave), 0, st, b);
+  constexpr int NS = N < 16 ? N : 16;
+  hipLaunchKernelGGL((scan_local_kernel<N, NS, BF16>),
+                     dim3((unsigned)(b.slots * blocks), N / NS), dim3(kWave), 0, st, b);
   if (b.f.joined) launch_scan_join(b.f, N, b.back, b.dfinal, st);
   const dim3 grid((unsigned)(b.slots * b.f.ngroups * wide)), threads(kWave * kWaves);
   if (b.f.paired)
