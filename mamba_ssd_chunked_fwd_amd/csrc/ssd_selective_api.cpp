@@ -8,6 +8,7 @@
 
 #include "ssd_selective.h"
 #include "ssd_selective_launch.h"
+#include "ssd_selective_plan.h"
 
 namespace {
 
@@ -59,7 +60,7 @@ ssd_status check_conv(const ssd_short_conv_dims* d, Form form, ssd::ConvShape* o
   if (d->width < 2 || d->width > 4 || d->dim > kMaxDim || nseq > kMaxSequences)
     return SSD_ERR_UNSUPPORTED;
   const ssd::ConvShape s{d->tokens, nseq, d->dim, d->width, stride};
-  if (!ssd::short_conv_fits(s, form == Form::kBackward, form == Form::kStep))
+  if (!ssd::conv_grid_fits(s, form == Form::kBackward, form == Form::kStep))
     return SSD_ERR_UNSUPPORTED;
   *out = s;
   return SSD_OK;
@@ -92,9 +93,8 @@ ssd_status check_scan(const ssd_selective_scan_dims* d, Form form, ssd_dtype dty
   // rows of B and C are read in 4-byte words
   if (dtype == SSD_BF16 && (s.b_stride % 2 != 0 || s.c_stride % 2 != 0))
     return SSD_ERR_INVALID_ARGUMENT;
-  if (form == Form::kForward ? !ssd::scan_fits(s)
-                             : (form == Form::kBackward ? !ssd::scan_bwd_fits(s)
-                                                        : !ssd::scan_step_fits(s)))
+  if (form == Form::kStep ? !ssd::scan_step_grid_fits(s)
+                          : !ssd::scan_grid_fits(s, form == Form::kBackward))
     return SSD_ERR_UNSUPPORTED;
   *out = s;
   return SSD_OK;
@@ -138,7 +138,7 @@ ssd_status ssd_short_conv_fwd(const void* x, const float* weight, const float* b
 size_t ssd_short_conv_bwd_workspace_bytes(const ssd_short_conv_dims* dims) {
   ssd::ConvShape s;
   if (check_conv(dims, Form::kBackward, &s) != SSD_OK) return 0;
-  return ssd::short_conv_bwd_workspace(s);
+  return ssd::conv_bwd_bytes(s);
 }
 
 ssd_status ssd_short_conv_bwd(const void* x, const float* weight, const float* bias,
@@ -157,7 +157,7 @@ ssd_status ssd_short_conv_bwd(const void* x, const float* weight, const float* b
       !ok_opt(dinit))
     return SSD_ERR_INVALID_ARGUMENT;
   if (overlap(dfinal, dinit, conv_state_bytes(s, dtype))) return SSD_ERR_INVALID_ARGUMENT;
-  if (!ok_workspace(workspace, workspace_bytes, ssd::short_conv_bwd_workspace(s)))
+  if (!ok_workspace(workspace, workspace_bytes, ssd::conv_bwd_bytes(s)))
     return SSD_ERR_WORKSPACE;
   return from_hip(ssd::launch_short_conv_bwd(x, weight, bias, init_state, cu_seqlens, dy, dfinal,
                                              dx, dweight, dbias, dinit, workspace,
@@ -182,14 +182,14 @@ size_t ssd_selective_scan_fwd_workspace_bytes(const ssd_selective_scan_dims* dim
                                               ssd_dtype dtype) {
   ssd::ScanShape s;
   if (check_scan(dims, Form::kForward, dtype, &s) != SSD_OK) return 0;
-  return ssd::scan_fwd_workspace(s);
+  return ssd::scan_fwd_bytes(s);
 }
 
 size_t ssd_selective_scan_bwd_workspace_bytes(const ssd_selective_scan_dims* dims,
                                               ssd_dtype dtype) {
   ssd::ScanShape s;
   if (check_scan(dims, Form::kBackward, dtype, &s) != SSD_OK) return 0;
-  return ssd::scan_bwd_workspace(s);
+  return ssd::bwd_layout(s).all;
 }
 
 ssd_status ssd_selective_scan_fwd(const void* x, const void* dt, const float* A, const void* B,
@@ -208,7 +208,7 @@ ssd_status ssd_selective_scan_fwd(const void* x, const void* dt, const float* A,
     return SSD_ERR_INVALID_ARGUMENT;
   if (init_state != final_state && overlap(init_state, final_state, scan_state_bytes(s)))
     return SSD_ERR_INVALID_ARGUMENT;
-  if (!ok_workspace(workspace, workspace_bytes, ssd::scan_fwd_workspace(s)))
+  if (!ok_workspace(workspace, workspace_bytes, ssd::scan_fwd_bytes(s)))
     return SSD_ERR_WORKSPACE;
   return from_hip(ssd::launch_scan_fwd(in, init_state, cu_seqlens, y, final_state, workspace,
                                        softplus != 0, dtype == SSD_BF16, s, stream));
@@ -234,7 +234,7 @@ ssd_status ssd_selective_scan_bwd(const void* x, const void* dt, const float* A,
       !ok_opt(ddt_bias) || !ok_opt(dinit) || (z == nullptr) != (dz == nullptr))
     return SSD_ERR_INVALID_ARGUMENT;
   if (overlap(dfinal, dinit, scan_state_bytes(s))) return SSD_ERR_INVALID_ARGUMENT;
-  if (!ok_workspace(workspace, workspace_bytes, ssd::scan_bwd_workspace(s)))
+  if (!ok_workspace(workspace, workspace_bytes, ssd::bwd_layout(s).all))
     return SSD_ERR_WORKSPACE;
   return from_hip(ssd::launch_scan_bwd(in, init_state, cu_seqlens, dy, dfinal, out, workspace,
                                        softplus != 0, dtype == SSD_BF16, s, stream));

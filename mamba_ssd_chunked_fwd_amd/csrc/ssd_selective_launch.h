@@ -16,8 +16,6 @@ struct ConvShape {
   int64_t tokens, nseq, dim, width, x_stride;
 };
 
-// Whether the grids of the launches below hold the shape.
-bool short_conv_fits(const ConvShape& s, bool backward, bool step);
 int launch_short_conv_fwd(const void* x, const float* weight, const float* bias, const void* init,
                           const int32_t* cu, void* y, void* fin, bool silu, bool bf16,
                           const ConvShape& s, void* stream);
@@ -25,7 +23,6 @@ int launch_short_conv_bwd(const void* x, const float* weight, const float* bias,
                           const int32_t* cu, const void* dy, const void* dfinal, void* dx,
                           float* dweight, float* dbias, void* dinit, void* ws, bool silu,
                           bool bf16, const ConvShape& s, void* stream);
-size_t short_conv_bwd_workspace(const ConvShape& s);
 int launch_short_conv_step(const void* x, const float* weight, const float* bias, void* state,
                            void* y, bool silu, bool bf16, const ConvShape& s, void* stream);
 
@@ -49,21 +46,12 @@ struct ScanGradients {
   void* dz;
   float *ddt_bias, *dinit;
 };
-// Workgroups of a scan's launches, of 64 threads each, stay below this.
-constexpr int64_t kScanMaxBlocks = (int64_t)1 << 26;
-
-// Whether the grids of the launches below hold the shape.
-bool scan_fits(const ScanShape& s);
-bool scan_bwd_fits(const ScanShape& s);
-bool scan_step_fits(const ScanShape& s);
 int launch_scan_fwd(const ScanInputs& in, const float* init, const int32_t* cu, void* y,
                     float* fin, void* ws, bool softplus, bool bf16, const ScanShape& s,
                     void* stream);
-size_t scan_fwd_workspace(const ScanShape& s);
 int launch_scan_bwd(const ScanInputs& in, const float* init, const int32_t* cu, const void* dy,
                     const float* dfinal, const ScanGradients& out, void* ws, bool softplus,
                     bool bf16, const ScanShape& s, void* stream);
-size_t scan_bwd_workspace(const ScanShape& s);
 int launch_scan_step(const ScanInputs& in, float* state, void* y, bool softplus, bool bf16,
                      const ScanShape& s, void* stream);
 

@@ -1,0 +1,235 @@
+// ssd_selective_plan.h -- how the selective operators cut their work (internal to
+// libssd; plain C++, so that the host layer's tests compile it without a GPU): runs of
+// tokens, the slots that hold them, and the layouts of the scan's workspaces.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "ssd_selective_launch.h"
+
+#ifdef __HIPCC__
+#include <hip/hip_runtime.h>
+#define SSD_BOTH __host__ __device__ __forceinline__
+#else
+#define SSD_BOTH inline
+#endif
+
+namespace ssd {
+
+// Division of n < 2^31 by a number that the host knows (Granlund and Montgomery, "Division by
+// invariant integers using multiplication"): with l = ceil(log2 d) and M = floor(2^32
+// (2^l - d) / d) + 1, n / d = (n + floor(M n / 2^32)) >> l.  A wave's start would spend
+// microseconds in divisions.
+struct Divide {
+  uint32_t d, m, shift;
+  Divide() = default;
+  explicit Divide(int64_t by) : d((uint32_t)by), m(0), shift(0) {
+    while (((uint64_t)1 << shift) < d) ++shift;
+    m = (uint32_t)((((((uint64_t)1 << shift) - d) << 32) / d) + 1);
+  }
+  SSD_BOTH uint32_t of(uint32_t n) const {
+    return (uint32_t)(n + (uint32_t)(((uint64_t)m * n) >> 32)) >> shift;
+  }
+};
+
+// Every sequence is cut into runs of at most `run` tokens, counted by slots:
+// sequence i owns the slots from cu[i] / run + i on.  Since
+// ceil(len / run) <= floor(cu[i+1] / run) - floor(cu[i] / run) + 1, these never meet those
+// of sequence i + 1, and tokens / run + nseq slots hold all sequences of any
+// lengths: the host needs none of them to size a launch (up to nseq slots
+// stay empty).  Without cu all lengths are equal and no slot is.  (Tokens, sequences and
+// slots are fewer than 2^31.)
+struct RunGrid {
+  const int32_t* cu;
+  int tokens, nseq, run, len;   // len: of a sequence, without cu
+  int per_seq;                  // slots of a sequence, without cu
+  Divide by_run, by_per_seq;
+};
+
+inline RunGrid make_run_grid(const int32_t* cu, int64_t tokens, int64_t nseq, int64_t run) {
+  RunGrid g{};
+  g.cu = cu;
+  g.tokens = (int)tokens;
+  g.nseq = (int)nseq;
+  g.run = (int)run;
+  g.len = (int)(tokens / nseq);
+  g.per_seq = g.len > g.run ? (g.len + g.run - 1) / g.run : 1;
+  g.by_run = Divide(g.run);
+  g.by_per_seq = Divide(g.per_seq);
+  return g;
+}
+inline int64_t run_slots(const RunGrid& g) {
+  return g.cu != nullptr ? (int64_t)(g.tokens / g.run) + g.nseq : (int64_t)g.nseq * g.per_seq;
+}
+
+struct Run {
+  int seq, seq_begin, seq_end;   // the sequence and its tokens
+  int begin, end;                // the run's tokens
+  int first;                     // the slot of the sequence's first run
+  int index, count;              // this run and how many the sequence has
+  bool on;                       // whether the slot holds a run (an empty sequence has one)
+};
+
+// An entry of cu, as the nearest token or end.
+SSD_BOTH int seq_bound(const RunGrid& g, int v) { return v < 0 ? 0 : (v > g.tokens ? g.tokens : v); }
+// The slot of the first run of a sequence that begins at `begin`.
+SSD_BOTH int first_slot(const RunGrid& g, int begin, int seq) {
+  return (int)g.by_run.of((uint32_t)begin) + seq;
+}
+SSD_BOTH int run_count(const RunGrid& g, int len) {
+  return len > g.run ? (int)g.by_run.of((uint32_t)(len - 1)) + 1 : 1;
+}
+SSD_BOTH Run place_run(const RunGrid& g, int slot, Run r) {
+  const int len = r.seq_end > r.seq_begin ? r.seq_end - r.seq_begin : 0;
+  r.seq_end = r.seq_begin + len;
+  r.index = slot - r.first;
+  r.count = run_count(g, len);
+  r.on = r.index >= 0 && r.index < r.count;
+  r.begin = r.on ? r.seq_begin + r.index * g.run : 0;
+  r.end = r.on && r.seq_end - r.begin > g.run ? r.begin + g.run : r.seq_end;
+  return r;
+}
+// The run of `slot` where the sequences are equally long, and where they are packed: `seq`, from
+// `begin` to `end`, is the last sequence whose first slot is not behind `slot`.  Where cu
+// descends that is some sequence, and the result some run of tokens in [0, tokens), or none.
+SSD_BOTH Run equal_run(const RunGrid& g, int slot) {
+  Run r;
+  r.seq = (int)g.by_per_seq.of((uint32_t)slot);
+  r.seq_begin = r.seq * g.len;
+  r.seq_end = r.seq_begin + g.len;
+  r.first = r.seq * g.per_seq;
+  return place_run(g, slot, r);
+}
+SSD_BOTH Run packed_run(const RunGrid& g, int slot, int seq, int begin, int end) {
+  Run r;
+  r.seq = seq;
+  r.seq_begin = begin;
+  r.seq_end = end;
+  r.first = first_slot(g, begin, seq);
+  return place_run(g, slot, r);
+}
+
+// ---- the scan
+constexpr int kScanLanes = 64;     // channels of a wave
+// Tokens whose states a wave of the gradients' second walk holds in registers at once; states
+// are marked in memory at this distance by the first walk.
+constexpr int kMark = 8;
+constexpr int kBwdWaves = 4;       // waves of a workgroup of the second walk
+
+inline int64_t channel_blocks(const ScanShape& s) {
+  return s.ngroups * ((s.dim / s.ngroups + kScanLanes - 1) / kScanLanes);
+}
+
+// The tokens of a run.  Waves of one run for each channel block of every sequence may
+// leave most of the chip idle; runs that start from the states of those before them
+// cost a second walk over all but each sequence's last one (forward), or longer joins
+// (backward, where two walks are made in any case).  Measured at 5120 channels of 16 states in
+// bf16: forward, 640 chains (8 x 2048 tokens) cut 507 us, whole 709; 1280 (16 x 1024) 523 and
+// 495; 2560 (32 x 1024) 1017 and 714.  Gradients: 1280 cut 1678, whole 2029; 2560 3380 and 3107.
+inline int64_t scan_run(const ScanShape& s, bool backward) {
+  const int64_t blocks = channel_blocks(s);
+  const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
+  const bool whole = s.nseq * blocks >= (backward ? 2048 : 1024);
+  const int64_t waves = backward ? 4096 : 8192, unit = backward ? kMark : 4;
+  // (a sequence of four times the mean is still whole)
+  int64_t run = whole ? 4 * mean : (s.tokens * blocks + waves - 1) / waves;
+  int64_t least = 24;
+  if (!backward) {
+    // Where there are waves for every SIMD in any case, a run's walk (0.36 us a token, twice) is
+    // weighed against the join (0.07 us a run): the sum is least at a root of tokens / 10.
+    least = 8;
+    while (10 * least * least < s.tokens) least += unit;
+  }
+  if (run < least) run = least;
+  run = (run + unit - 1) / unit * unit;
+  const int64_t most = INT32_MAX / unit * unit;
+  return run > most ? most : run;
+}
+// Slots, however the sequences are given.
+inline int64_t scan_slots(const ScanShape& s, bool backward) {
+  return s.tokens / scan_run(s, backward) + s.nseq;
+}
+// Marks: each run's own from begin / kMark + slot on (as slots from cu).
+inline int64_t scan_marks(const ScanShape& s) { return s.tokens / kMark + scan_slots(s, true) + 1; }
+SSD_BOTH int64_t first_mark(const Run& r, int64_t slot) { return r.begin / kMark + slot; }
+
+// Blocks of a group's channels that the second walk's workgroups take: a lane has four
+// states of two channels.
+inline int64_t wide_blocks(const ScanShape& s) {
+  const int64_t channels = kBwdWaves * (2 * kScanLanes * 4 / s.n);
+  return (s.dim / s.ngroups + channels - 1) / channels;
+}
+
+// Few runs: each goes through those before it itself.  Many: a launch of their own joins them.
+constexpr int kFoldRuns = 4;       // runs that a sequence may have for the first form
+inline bool joins(const RunGrid& g) {
+  return g.cu != nullptr ? g.tokens / g.run > kFoldRuns : g.per_seq > kFoldRuns;
+}
+
+// The forward call's workspace: states [slots, N, dim], then totals [slots, dim].
+inline size_t scan_fwd_bytes(const ScanShape& s) {
+  if (s.tokens <= scan_run(s, false)) return 16;
+  return sizeof(float) * (size_t)scan_slots(s, false) * (size_t)(s.dim * (s.n + 1));
+}
+
+// The gradients', in bytes from its start.
+struct BwdLayout {
+  size_t states, totals, back, marks, mark_totals, dA, bc, all;
+};
+inline BwdLayout bwd_layout(const ScanShape& s) {
+  const size_t slots = (size_t)scan_slots(s, true), marks = (size_t)scan_marks(s);
+  const size_t D = (size_t)s.dim, N = (size_t)s.n;
+  size_t at = 0;
+  const auto take = [&at](size_t floats) {
+    const size_t p = at;
+    at += (floats * sizeof(float) + 15) & ~(size_t)15;
+    return p;
+  };
+  BwdLayout l;
+  l.states = take(slots * N * D);
+  l.totals = take(slots * D);
+  l.back = take(slots * N * D);
+  l.marks = take(marks * N * D);
+  l.mark_totals = take(marks * D);
+  l.dA = take(slots * (N + 2) * D);
+  l.bc = take((size_t)wide_blocks(s) * (size_t)(s.tokens * s.ngroups) * 2 * N);
+  l.all = at;
+  return l;
+}
+
+// Whether the launches' grids hold a shape: a launch has fewer than 2^32 threads.
+inline bool scan_grid_fits(const ScanShape& s, bool backward) {
+  constexpr int64_t kBlocks = (int64_t)1 << 26;     // of 64 threads
+  const int64_t slots = scan_slots(s, backward);
+  if (slots >= kBlocks / channel_blocks(s)) return false;
+  if (!backward) return true;
+  // the second walk's workgroups have 256 threads, and so have the sums' over rows of B and C
+  return slots < kBlocks / kBwdWaves / (s.ngroups * wide_blocks(s)) &&
+         s.tokens <= (kBlocks / 4 - 1) * 256 / (2 * s.n * s.ngroups);
+}
+inline bool scan_step_grid_fits(const ScanShape& s) {
+  return s.tokens < ((int64_t)1 << 32) / (s.dim * (s.n / 4) + 256);
+}
+
+// ---- the convolution
+// Tokens of a run: enough runs for some 4000 waves, and of the gradients (whose runs
+// each leave a row of partial sums) no fewer than 64 tokens where that fills the chip.
+inline int64_t conv_run(const ConvShape& s, bool backward) {
+  const int64_t waves = (s.dim + 64 * 8 - 1) / (64 * 8);
+  const int64_t run = s.tokens * waves / (backward ? 2048 : 4096);
+  return run < 8 ? 8 : (run > 64 ? 64 : run);
+}
+inline int64_t conv_slots(const ConvShape& s, bool backward) {
+  return s.tokens / conv_run(s, backward) + s.nseq;
+}
+// A launch has fewer than 2^32 threads: up to 256 more than channels for each slot.
+inline bool conv_grid_fits(const ConvShape& s, bool backward, bool step) {
+  const int64_t slots = step ? s.tokens : conv_slots(s, backward);
+  return slots < ((int64_t)1 << 32) / (s.dim + 256);
+}
+inline size_t conv_bwd_bytes(const ConvShape& s) {
+  return sizeof(float) * (size_t)conv_slots(s, true) * (size_t)((s.width + 1) * s.dim);
+}
+
+}  // namespace ssd

@@ -226,8 +226,6 @@ __device__ __forceinline__ void load_run(const ScanArgs& a, int64_t slot, int64_
 // ---- the states at the runs' starts
 // Few runs: each goes through those before it itself (no launch).  Many: a launch of their
 // own (scan_join_kernel) replaces what the runs leave by what they start from.
-constexpr int kFoldRuns = 4;      // runs that a sequence may have for the first form
-
 // The first form, for some of a channel's states: `left(s, n)` is what run s leaves of
 // state n (the first run's includes the initial state).
 template <int N, class Left>
@@ -248,10 +246,5 @@ __device__ __forceinline__ void fold_runs(const ScanArgs& a, int64_t first, int6
 // gradients at the runs' starts by those at their ends.
 void launch_scan_join(const ScanArgs& a, int64_t n, float* back, const float* dfinal,
                       hipStream_t st);
-
-// Whether a sequence may have so many runs that their states are joined by a launch.
-inline bool joins(const RunGrid& g) {
-  return g.cu != nullptr ? g.tokens / g.run > kFoldRuns : g.per_seq > kFoldRuns;
-}
 
 }  // namespace ssd

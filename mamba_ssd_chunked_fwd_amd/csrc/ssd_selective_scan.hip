@@ -28,9 +28,9 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const ScanArgs a, float*
     int first = 0, count = 0;
     if (mine < g.nseq) {
       if (g.cu != nullptr) {
-        const int begin = seq_bound(g, (int)mine), end = seq_bound(g, (int)mine + 1);
-        first = (int)g.by_run.of(begin) + (int)mine;
-        count = end > begin ? (int)g.by_run.of(end - begin - 1) + 1 : 0;
+        const int begin = seq_bound(g, g.cu[mine]), end = seq_bound(g, g.cu[mine + 1]);
+        first = first_slot(g, begin, (int)mine);
+        count = end > begin ? run_count(g, end - begin) : 0;
       } else {
         first = (int)mine * g.per_seq;
         count = g.per_seq;
@@ -205,22 +205,6 @@ __global__ __launch_bounds__(kWave, NS == 64 ? 2 : 1) void scan_kernel(const Sca
   }
 }
 
-// The tokens of a run.  Waves of one run for each channel block of every sequence may
-// leave most of the chip idle; runs that start from the states of those before them
-// cost a second walk over all but each sequence's last one.
-int64_t run_length(const ScanShape& s) {
-  const int64_t blocks = s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
-  const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
-  int64_t run = s.nseq * blocks >= 1024 ? 4 * mean : (s.tokens * blocks + 8191) / 8192;
-  // where there are waves for every SIMD in any case, a run's walk (0.36 us a token, twice) is
-  // weighed against the join (0.07 us a run): the sum is least at a tenth of the tokens' root
-  int64_t least = 8;
-  while (10 * least * least < s.tokens) least += kBlock;
-  if (run < least) run = least;
-  run = (run + kBlock - 1) / kBlock * kBlock;
-  return run > INT32_MAX ? INT32_MAX / kBlock * kBlock : run;
-}
-
 struct ScanPlan {
   RunGrid runs;
   bool split;
@@ -229,15 +213,12 @@ struct ScanPlan {
 
 ScanPlan make_plan(const ScanShape& s, const int32_t* cu) {
   ScanPlan p;
-  p.runs = make_run_grid(cu, s.tokens, s.nseq, run_length(s));
+  p.runs = make_run_grid(cu, s.tokens, s.nseq, scan_run(s, false));
   p.slots = run_slots(p.runs);
   p.split = cu != nullptr ? s.tokens > p.runs.run : p.runs.per_seq > 1;
-  p.blocks = s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
+  p.blocks = channel_blocks(s);
   return p;
 }
-
-// More slots than without cu, so that the workspace's size does not ask for it.
-int64_t most_slots(const ScanShape& s) { return s.tokens / run_length(s) + s.nseq; }
 
 template <int N>
 void join_n(const ScanArgs& a, float* back, const float* dfinal, hipStream_t st) {
@@ -273,16 +254,6 @@ void launch_scan_join(const ScanArgs& a, int64_t n, float* back, const float* df
     join_n<32>(a, back, dfinal, st);
   else
     join_n<64>(a, back, dfinal, st);
-}
-
-bool scan_fits(const ScanShape& s) {
-  const int64_t blocks = s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
-  return most_slots(s) < kScanMaxBlocks / blocks;
-}
-
-size_t scan_fwd_workspace(const ScanShape& s) {
-  if (s.tokens <= run_length(s)) return 16;
-  return sizeof(float) * (size_t)(most_slots(s) * s.dim * (s.n + 1));
 }
 
 int launch_scan_fwd(const ScanInputs& in, const float* init, const int32_t* cu, void* y,

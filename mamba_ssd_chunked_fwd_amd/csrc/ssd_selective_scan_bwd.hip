@@ -8,10 +8,7 @@
 namespace ssd {
 namespace {
 
-// Tokens whose states a wave holds in registers at once; states are marked in memory
-// at this distance by the first walk.
-constexpr int kMark = 8;
-constexpr int kWaves = 4;
+constexpr int kWaves = kBwdWaves;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct BwdArgs {
@@ -27,10 +24,6 @@ struct BwdArgs {
   int64_t slots;
   Divide by_wide, by_wide_slot;   // by the second walk's blocks of a group, and of all
 };
-
-__device__ __forceinline__ int64_t first_mark(const Run& r, int64_t slot) {
-  return (int64_t)(r.begin / kMark) + slot;
-}
 
 // The first walk, up the tokens: of each run the state that it leaves, the states inside
 // it, and the gradient that its outputs give the state at its start,
@@ -641,8 +634,8 @@ __global__ __launch_bounds__(256) void scan_sum_bc_kernel(const BwdArgs b, int n
   const ScanArgs& a = b.f;
   int64_t begin = 0, end = a.runs.tokens;
   if (a.runs.cu != nullptr) {      // rows outside every sequence are left as they are
-    begin = seq_bound(a.runs, 0);
-    end = seq_bound(a.runs, a.runs.nseq);
+    begin = seq_bound(a.runs, a.runs.cu[0]);
+    end = seq_bound(a.runs, a.runs.cu[a.runs.nseq]);
   }
   const int64_t row = 2 * n * a.ngroups, all = (int64_t)a.runs.tokens * row;
   const int64_t i = begin * row + (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -676,55 +669,6 @@ __global__ __launch_bounds__(256) void scan_sum_slots_kernel(const BwdArgs b, in
     (k == n ? b.out.dD : b.out.ddt_bias)[d] = sum;
 }
 
-int64_t channel_blocks(const ScanShape& s) {
-  return s.ngroups * ((s.dim / s.ngroups + kWave - 1) / kWave);
-}
-
-constexpr int64_t kLeastRun = 24;
-
-int64_t run_length(const ScanShape& s) {
-  const int64_t blocks = channel_blocks(s);
-  const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
-  int64_t run = s.nseq * blocks >= 2048 ? 4 * mean : (s.tokens * blocks + 4095) / 4096;
-  run = (run + kMark - 1) / kMark * kMark;
-  constexpr int64_t kMost = INT32_MAX / kMark * kMark;
-  return run < kLeastRun ? kLeastRun : (run > kMost ? kMost : run);
-}
-int64_t most_slots(const ScanShape& s) { return s.tokens / run_length(s) + s.nseq; }
-int64_t most_marks(const ScanShape& s) { return s.tokens / kMark + most_slots(s) + 1; }
-
-// Blocks of a group's channels that the second walk's workgroups take.
-int64_t wide_blocks(const ScanShape& s) {
-  const int64_t channels = kWaves * (512 / s.n);
-  return (s.dim / s.ngroups + channels - 1) / channels;
-}
-
-size_t aligned(size_t n) { return (n + 15) & ~(size_t)15; }
-
-struct BwdLayout {
-  size_t states, totals, back, marks, mark_totals, dA, bc, all;
-};
-BwdLayout layout(const ScanShape& s) {
-  const size_t f = sizeof(float), slots = (size_t)most_slots(s), marks = (size_t)most_marks(s);
-  const size_t D = (size_t)s.dim, N = (size_t)s.n;
-  BwdLayout l;
-  size_t at = 0;
-  auto take = [&](size_t n) {
-    const size_t p = at;
-    at += aligned(n * f);
-    return p;
-  };
-  l.states = take(slots * N * D);
-  l.totals = take(slots * D);
-  l.back = take(slots * N * D);
-  l.marks = take(marks * N * D);
-  l.mark_totals = take(marks * D);
-  l.dA = take(slots * (N + 2) * D);
-  l.bc = take((size_t)wide_blocks(s) * (size_t)(s.tokens * s.ngroups) * 2 * N);
-  l.all = at;
-  return l;
-}
-
 template <int N, bool BF16>
 void launch_n(const BwdArgs& b, int64_t blocks, int64_t wide, hipStream_t st) {
   constexpr int NS = N < 16 ? N : 16;
@@ -740,26 +684,16 @@ void launch_n(const BwdArgs& b, int64_t blocks, int64_t wide, hipStream_t st) {
 
 }  // namespace
 
-bool scan_bwd_fits(const ScanShape& s) {
-  const int64_t rows = 2 * s.n * s.ngroups;
-  // (the second walk's workgroups have four waves of at least 8 channels each)
-  return most_slots(s) < kScanMaxBlocks / 4 / (s.ngroups * wide_blocks(s)) &&
-         most_slots(s) < kScanMaxBlocks / channel_blocks(s) &&
-         s.tokens <= (kScanMaxBlocks / 4 - 1) * 256 / rows;
-}
-
-size_t scan_bwd_workspace(const ScanShape& s) { return layout(s).all; }
-
 int launch_scan_bwd(const ScanInputs& in, const float* init, const int32_t* cu, const void* dy,
                     const float* dfinal, const ScanGradients& out, void* ws, bool softplus,
                     bool bf16, const ScanShape& s, void* stream) {
   clear_launch_error();
-  const BwdLayout l = layout(s);
+  const BwdLayout l = bwd_layout(s);
   char* base = (char*)ws;
   BwdArgs b{};
   ScanArgs& a = b.f;
   a = make_scan_args(in, init, s, softplus);
-  a.runs = make_run_grid(cu, s.tokens, s.nseq, run_length(s));
+  a.runs = make_run_grid(cu, s.tokens, s.nseq, scan_run(s, true));
   b.slots = run_slots(a.runs);
   a.joined = joins(a.runs);
   a.states = (float*)(base + l.states);

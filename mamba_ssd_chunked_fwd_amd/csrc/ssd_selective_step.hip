@@ -65,11 +65,6 @@ __global__ __launch_bounds__(256) void selective_step_kernel(const ScanArgs a, D
 
 }  // namespace
 
-// A launch has fewer than 2^32 threads.
-bool scan_step_fits(const ScanShape& s) {
-  return s.tokens < ((int64_t)1 << 32) / (s.dim * (s.n / 4) + 256);
-}
-
 int launch_scan_step(const ScanInputs& in, float* state, void* y, bool softplus, bool bf16,
                      const ScanShape& s, void* stream) {
   clear_launch_error();

@@ -378,17 +378,6 @@ ConvGrid conv_grid(const ConvShape& s, int V) {
   return g;
 }
 
-// Tokens of a run: enough runs for some 4000 waves, and of the gradients (whose runs
-// each leave a row of partial sums) no fewer than 64 tokens where that fills the chip.
-int64_t conv_run(const ConvShape& s, bool backward) {
-  const int64_t waves = (s.dim + kWave * 8 - 1) / (kWave * 8);
-  const int64_t run = s.tokens * waves / (backward ? 2048 : 4096);
-  return run < 8 ? 8 : (run > 64 ? 64 : run);
-}
-int64_t conv_slots(const ConvShape& s, bool backward) {
-  return s.tokens / conv_run(s, backward) + s.nseq;
-}
-
 // Channels of a lane.  Measured at 16384 x 5376 in bf16: forward 8 channels 79 us, 4 72 us
 // (126 registers and 16-byte loads against 60 and 8); gradients 8 171, 4 132, 2 123.
 constexpr int kFwdVec = 4, kBwdVec = 2;
@@ -431,12 +420,6 @@ ConvArgs conv_args(const void* x, const float* weight, const float* bias, const 
 
 }  // namespace
 
-// A launch has fewer than 2^32 threads: up to 256 more than channels for each slot.
-bool short_conv_fits(const ConvShape& s, bool backward, bool step) {
-  const int64_t slots = step ? s.tokens : conv_slots(s, backward);
-  return slots < ((int64_t)1 << 32) / (s.dim + 256);
-}
-
 int launch_short_conv_fwd(const void* x, const float* weight, const float* bias, const void* init,
                           const int32_t* cu, void* y, void* fin, bool silu, bool bf16,
                           const ConvShape& s, void* stream) {
@@ -455,10 +438,6 @@ int launch_short_conv_fwd(const void* x, const float* weight, const float* bias,
         dim3((unsigned)(a.slots * g.blocks)), dim3(g.threads), 0, (hipStream_t)stream, a);
   });
   return (int)hipGetLastError();
-}
-
-size_t short_conv_bwd_workspace(const ConvShape& s) {
-  return sizeof(float) * (size_t)(conv_slots(s, true) * (s.width + 1) * s.dim);
 }
 
 int launch_short_conv_bwd(const void* x, const float* weight, const float* bias, const void* init,
