@@ -7,6 +7,8 @@
 // channels at a time.
 #pragma once
 
+#include <cfloat>
+
 #include "ssd_selective_device.h"
 #include "ssd_selective_launch.h"
 
@@ -89,6 +91,13 @@ __device__ __forceinline__ void store_states(float* p, const float (&v)[N]) {
     *(f32x4*)(p + 4 * k) = (f32x4){v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
 }
 
+// A in powers of two: exp(delta A) = exp2(delta A2).  Kept finite where A is, so that no time (a
+// token past a run's end has none) decays nothing.
+__device__ __forceinline__ float in_powers_of_two(float A) {
+  const float v = A * kLog2e;
+  return v < -FLT_MAX ? -FLT_MAX : (v > FLT_MAX ? FLT_MAX : v);
+}
+
 // N values of B or C of one token, the same for all lanes.
 template <int N, bool BF16>
 struct States {
@@ -112,8 +121,9 @@ struct States {
   }
 };
 
-// B and C (or B alone) of the tokens of a run, one after the other, in pieces of 32 bytes, each piece read while the one before it is worked on: more would not leave
-// enough scalar registers.
+// B and C (or B alone) of the tokens of a run, one after the other, in pieces of 32 bytes,
+// each piece read while the one before it is worked on: more would not leave enough scalar
+// registers.
 template <int NS, bool BF16, bool BOTH>
 struct StateRows {
   static constexpr int kMost = BF16 ? 16 : 8;

@@ -19,7 +19,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const ScanArgs a, float*
   const int n = (int)(blockIdx.x / blocks) * 4 + threadIdx.x / kWave;
   const int64_t d = (int64_t)(blockIdx.x % blocks) * kWave + lane;
   const bool on = d < a.dim;
-  const float A2 = on ? a.in.A[d * N + n] * kLog2e : 0.0f;
+  const float A2 = on ? in_powers_of_two(a.in.A[d * N + n]) : 0.0f;
   const RunGrid& g = a.runs;
   constexpr int kAhead = 16;
   // 64 sequences at a time: those that have more than one run
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(kWave, NS == 64 ? 2 : 1) void scan_kernel(const Sca
   if (!OUT && last) return;
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
-    A2[n] *= kLog2e;
+    A2[n] = in_powers_of_two(A2[n]);
     h[n] = 0.0f;
   }
   if constexpr (OUT) {

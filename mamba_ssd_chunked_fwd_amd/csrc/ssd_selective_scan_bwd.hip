@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   if (!r.on) return;
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
-    A2[n] *= kLog2e;
+    A2[n] = in_powers_of_two(A2[n]);
     h[n] = 0.0f;
     decay[n] = 1.0f;
     back[n] = 0.0f;
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
     asm("" : "+s"(step));      // (its multiples would stay in scalar registers)
     float* p = b.marks + (m * N + n0) * step + d;
 #pragma unroll
-    for (int n = 0; n < N; ++n, p += step) *p = h[n];
+    for (int n = 0; n < NS; ++n, p += step) *p = h[n];
     b.mark_totals[m * step + d] = (float)total;
   };
   auto work = [&](const Block& k, int left) {
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
     const int64_t state = ((int64_t)r.seq * a.dim + d[c]) * N + 4 * q;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      A2[c][n] = A[n] * kLog2e;
+      A2[c][n] = in_powers_of_two(A[n]);
       dA[c][n] = 0.0f;
     }
     // the state at the run's start, and the gradient of the state at its end

@@ -220,6 +220,23 @@ def test_decays_from_none_to_no_memory(ssd):
     assert all(torch.isfinite(t).all() for t in grads if t is not None)
 
 
+def test_decays_next_to_the_largest_finite_number(ssd):
+    """A times log2(e) is not finite, and tokens past a run's end have no time: their decay is
+    still 1."""
+    a = block_inputs(13, dtype=torch.float32)
+    a[2] = a[2].clone()
+    a[2][:, 0], a[2][:, 1] = -3.2e38, -3.4e38
+    dy = torch.randn(a[0].shape, generator=torch.Generator().manual_seed(4)).to(DEV)
+    args = [dbl(t)[0] if t.dim() > 2 else dbl(t) for t in a]
+    want = ref.scan(*args, [13], True, None, dbl(dy)[0])
+    names = ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias")
+    grads = dict(zip(names, ssd.selective_scan_backward(*a, dy)))
+    y, _ = ssd.selective_scan(*a)
+    for m, t in [("y", y), *grads.items()]:
+        got = t.double().cpu().reshape(want[m].shape)
+        assert float((got - want[m]).norm()) <= 1e-5 * float(want[m].norm()), m
+
+
 def test_entries_outside_the_tokens_are_the_nearer_end(ssd):
     a = block_inputs(100)
     cu = torch.tensor([0, 11, 100], dtype=torch.int32, device=DEV)
