@@ -130,8 +130,10 @@ inline int64_t channel_blocks(const ScanShape& s) {
 inline int64_t scan_run(const ScanShape& s, bool backward) {
   const int64_t blocks = channel_blocks(s);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
-  const bool whole = s.nseq * blocks >= (backward ? 2048 : 1024);
-  const int64_t waves = backward ? 4096 : 8192, unit = backward ? kMark : 4;
+  const int64_t chains = s.nseq * blocks, unit = backward ? kMark : 4;
+  const bool whole = chains >= (backward ? 2048 : 1024);
+  // waves that the chip holds at once, less those of the sequences' last, shorter runs
+  const int64_t waves = (backward ? 4096 : 8192) - chains;
   // (a sequence of four times the mean is still whole)
   int64_t run = whole ? 4 * mean : (s.tokens * blocks + waves - 1) / waves;
   int64_t least = 24;
