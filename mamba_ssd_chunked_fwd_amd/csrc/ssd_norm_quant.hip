@@ -8,7 +8,12 @@
 // lane exchanges, longer ones meet in LDS.  A code's border may lie anywhere, and a
 // value that 32 bits put on its other side comes out a whole step (up to 12%) away, so
 // everything between the inputs and the codes is formed in 64 bits, which the
-// vector unit does at the rate of 32.
+// vector unit does at the rate of 32.  The codes are rounded once: to 32 bits "to odd", then by
+// the 8-bit conversion.
+//
+// Measured at 16384 x 5120, bf16 with an fp32 stream, groups of 128, e4m3: 191 us for 925 MB (4.8
+// TB/s; a device copy moves 5.15).  Rows of up to 8192 channels are read a row ahead (two
+// vectors a lane do not leave the registers for it).  Branches on what a row has cost 281 us.
 #include "ssd_host.h"
 #include "ssd_selective_device.h"
 #include "ssd_selective_launch.h"

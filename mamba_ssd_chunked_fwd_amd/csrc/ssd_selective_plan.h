@@ -127,6 +127,8 @@ inline int64_t channel_blocks(const ScanShape& s) {
 // (backward, where two walks are made in any case).  Measured at 5120 channels of 16 states in
 // bf16: forward, 640 chains (8 x 2048 tokens) cut 507 us, whole 709; 1280 (16 x 1024) 523 and
 // 495; 2560 (32 x 1024) 1017 and 714.  Gradients: 1280 cut 1678, whole 2029; 2560 3380 and 3107.
+// Waves of the gradients' two walks (16384 x 2560): 2048 327 + 648 us, 4096 215 + 616, 6144 216 +
+// 617 and longer joins.
 inline int64_t scan_run(const ScanShape& s, bool backward) {
   const int64_t blocks = channel_blocks(s);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
@@ -138,8 +140,9 @@ inline int64_t scan_run(const ScanShape& s, bool backward) {
   int64_t run = whole ? 4 * mean : (s.tokens * blocks + waves - 1) / waves;
   int64_t least = 24;
   if (!backward) {
-    // Where there are waves for every SIMD in any case, a run's walk (0.36 us a token, twice) is
-    // weighed against the join (0.07 us a run): the sum is least at a root of tokens / 10.
+    // Where there are waves for every SIMD in any case, a run's walk (0.36 us a token, twice)
+    // is weighed against the join (0.07 us a run): their sum is least near the root of a tenth
+    // of the tokens (643 tokens of 1536 channels: 28 us with runs of 12, 43 with runs of 32).
     least = 8;
     while (10 * least * least < s.tokens) least += unit;
   }

@@ -1,4 +1,38 @@
-// Gradients of the selective scan (ssd_selective_scan.hip).
+// Gradients of the selective scan (ssd_selective_scan.hip).  With e_t = exp(delta_t A), du = dy
+// silu(z) and the state's gradient R_t = C_t du_t + e_{t+1} R_{t+1}, every gradient is a sum over
+// states, channels or tokens of products of R_t, h_t and h_{t-1} (include/ssd_selective.h).
+//
+// States are not kept from the forward call (64 bytes for each channel and token of 16 states,
+// against 6 of inputs in bf16), and h_{t-1} = (h_t - delta x B) / e_t loses what has decayed.
+// So:
+//   1. scan_local_kernel goes up every run from zeros and leaves the run's last state, the states
+//      at every eighth token (marks), and the gradient that the run's own outputs give the state
+//      at its start;
+//   2. scan_join_kernel makes the states at the runs' starts and the gradients at their ends from
+//      these (few runs: the second walk does it itself);
+//   3. scan_bwd_kernel goes down every run, eight tokens at a time: up from the mark with the
+//      states in registers, then down through them;
+//   4. two kernels add what the second walk leaves of dB and dC (for each block of channels) and
+//      of dA, dD and ddt_bias (for each run), in a fixed order: no atomics.
+//
+// MI355X design.  All of it is bound by vector instructions, so the second walk is laid out for
+// few of them: sums over N states of a channel (dx, ddt, dz) want its states in one lane, sums
+// over a group's channels (dB, dC) want channels in one lane.  Four states of two channels are
+// the middle: a token costs a lane 23 instructions for each of its 8 (state, channel) pairs, of
+// which 15 are the formula's, and per token and channel six DPP adds sum over four lanes; dB and
+// dC go through LDS, four tokens at a time, where the lanes of a wave add 8 vectors each.  (A
+// channel a lane with its sums over lanes by DPP alone: 2634 us for what takes 566 below.)  Nine
+// states of 2 x 4 values take 72 of the 256 registers of two waves a SIMD; decays of four of the
+// eight tokens wait in LDS, the others are formed again (one exponential costs two instructions).
+// Eight states a channel have two lanes a channel, more tokens of their own, and run at one wave
+// a SIMD (measured 737 us against 1125 at two, which spill).  Waves of a workgroup share B and C
+// and their sums of dB and dC: four of them 622 us and 13 for the sums over blocks, two 606 and
+// 23, eight 680 and 8.
+//
+// Measured at 16384 tokens of 2560 channels of 16 states in bf16 (three sequences): first walk
+// 199 us (vector unit busy 87%), joining 17, second walk 566 (74%: two waves a SIMD do not cover
+// LDS reads and barriers; B and C read a token ahead spill, 670), sums 13 + 6.  335 MB of marks
+// are written and read; at 5.15 TB/s all bytes of both walks take 330 us.
 #include "ssd_selective_scan.h"
 
 #include "ssd_host.h"
@@ -524,33 +558,6 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
       values[wave][j % kBatch][1][lane] = vC;
       fence();
     };
-    // The sums of a batch's dB and dC over the wave's pairs: 8 L of them (token, half, lane
-    // of the pair), of kPairs vectors each, are shared by the 64 lanes, eight vectors a lane.
-    auto batch = [&](int j0) {
-      constexpr int kTasks = 2 * kBatch * L;
-      constexpr int kParts = kTasks < kWave ? kWave / kTasks : 1;   // lanes of a sum
-      constexpr int kRounds = kTasks > kWave ? kTasks / kWave : 1;
-      constexpr int kEach = La::kPairs / kParts;
-      wave_sync();
-#pragma unroll
-      for (int round = 0; round < kRounds; ++round) {
-        const int part = lane % kParts, task = lane / kParts + round * kWave;
-        const int k = task % L, half = task / L % 2, j = task / (2 * L);
-        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < kEach; ++s) {
-          const int p = part * kEach + (s + j) % kEach;     // (spread over the banks)
-          sum += values[wave][j][half][p * L + k];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (kParts >= 2) sum[e] += moved<kXor1>(sum[e]);
-          if (kParts >= 4) sum[e] += moved<kXor2>(sum[e]);
-        }
-        if (part == 0) sums[turn][wave][j0 + j][half][k] = sum;
-      }
-      wave_sync();
-    };
     // the lane's own tokens
     auto finish = [&](int i) {
       const int j = i * TURNS + q;
@@ -574,6 +581,37 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
       if (gated)
         Pair<BF16>::store(row_rsrc((char*)b.out.dz + row), own_at[i].y, vz, on, paired);
     };
+    // The sums of a batch's dB and dC over the wave's pairs: 8 L of them (token, half, lane
+    // of the pair), of kPairs vectors each, are shared by the 64 lanes, eight vectors a lane.
+    // `meanwhile` fills the wait for them.
+    auto batch = [&](int j0, auto meanwhile) {
+      constexpr int kTasks = 2 * kBatch * L;
+      constexpr int kParts = kTasks < kWave ? kWave / kTasks : 1;   // lanes of a sum
+      constexpr int kRounds = kTasks > kWave ? kTasks / kWave : 1;
+      constexpr int kEach = La::kPairs / kParts;
+      wave_sync();
+#pragma unroll
+      for (int round = 0; round < kRounds; ++round) {
+        const int part = lane % kParts, task = lane / kParts + round * kWave;
+        const int k = task % L, half = task / L % 2, j = task / (2 * L);
+        f32x4 v[kEach];
+#pragma unroll
+        for (int s = 0; s < kEach; ++s)
+          // (spread over the banks)
+          v[s] = values[wave][j][half][(part * kEach + (s + j) % kEach) * L + k];
+        if (round == 0) meanwhile();
+        f32x4 sum = v[0];
+#pragma unroll
+        for (int s = 1; s < kEach; ++s) sum += v[s];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (kParts >= 2) sum[e] += moved<kXor1>(sum[e]);
+          if (kParts >= 4) sum[e] += moved<kXor2>(sum[e]);
+        }
+        if (part == 0) sums[turn][wave][j0 + j][half][k] = sum;
+      }
+      wave_sync();
+    };
     up(std::integral_constant<int, 0>{});
     up(std::integral_constant<int, 1>{});
     up(std::integral_constant<int, 2>{});
@@ -586,20 +624,22 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
     down(std::integral_constant<int, 6>{});
     down(std::integral_constant<int, 5>{});
     down(std::integral_constant<int, 4>{});
-    batch(4);
     // (tokens are finished, and the next block's rows asked for, where registers are free)
+    batch(4, [&] {
 #pragma unroll
-    for (int i = OWN - 1; i >= 0; --i)
-      if (i * TURNS >= kBatch) finish(i);
+      for (int i = OWN - 1; i >= 0; --i)
+        if (i * TURNS >= kBatch) finish(i);
+    });
     if (m > 0) load(m - 1);
     down(std::integral_constant<int, 3>{});
     down(std::integral_constant<int, 2>{});
     down(std::integral_constant<int, 1>{});
     down(std::integral_constant<int, 0>{});
-    batch(0);
+    batch(0, [&] {
 #pragma unroll
-    for (int i = OWN - 1; i >= 0; --i)
-      if (i * TURNS < kBatch) finish(i);
+      for (int i = OWN - 1; i >= 0; --i)
+        if (i * TURNS < kBatch) finish(i);
+    });
     if (m > 0) stage(turn ^ 1);
     __syncthreads();
     // dB and dC of this block of channels

@@ -1,11 +1,15 @@
-// The recurrent form of the selective scan: one token for every sequence b, the state
-// updated in place.  Per channel d and state n,
+// The recurrent form of the selective scan: one token for every sequence b, the state updated in
+// place.  Per channel d and state n,
 //   h = exp(delta A) h + delta x B,   y = (sum_n C h + D x) silu(z)
 //
-// MI355X design.  The state is read and written once (8 N bytes per channel) and little
-// else: an HBM stream.  A lane holds a 16-byte unit, four states of one channel; the N/4
-// lanes of a channel lie side by side, form the channel's time step each for itself
-// and meet in u by lane exchanges.
+// MI355X design.  The state is read and written once (8 N bytes per channel) and little else: an
+// HBM stream.  A lane holds a 16-byte unit, four states of one channel; the N/4 lanes of a
+// channel lie side by side, form the channel's time step each for itself and meet in u by lane
+// exchanges.  All of it is fp32.
+//
+// Measured: 200 sequences of 5120 channels of 16 states (131 MB of states, 139 in all) 25.4 us =
+// 5.5 TB/s, where part of the state still lies in the last-level cache (a device copy moves
+// 5.15); one sequence of 2560 channels 2.9 us, of which a launch is the most.
 #include "ssd_host.h"
 #include "ssd_selective_scan.h"
 
@@ -79,10 +83,10 @@ int launch_scan_step(const ScanInputs& in, float* state, void* y, bool softplus,
   case N:                                                                                        \
     if (bf16)                                                                                    \
       hipLaunchKernelGGL((selective_step_kernel<N, true>), grid, dim3(256), 0, st, a, by_blocks, \
-                         by_group);   \
+                         by_group);                                                              \
     else                                                                                         \
-      hipLaunchKernelGGL((selective_step_kernel<N, false>), grid, dim3(256), 0, st, a, by_blocks, \
-                         by_group);  \
+      hipLaunchKernelGGL((selective_step_kernel<N, false>), grid, dim3(256), 0, st, a,           \
+                         by_blocks, by_group);                                                   \
     break
   switch (s.n) {
     SSD_STEP(8);
