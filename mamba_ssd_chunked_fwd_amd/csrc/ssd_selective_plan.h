@@ -134,8 +134,10 @@ inline int64_t scan_run(const ScanShape& s, bool backward) {
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
   const int64_t chains = s.nseq * blocks, unit = backward ? kMark : 4;
   const bool whole = chains >= (backward ? 2048 : 1024);
-  // waves that the chip holds at once, less those of the sequences' last, shorter runs
-  const int64_t waves = (backward ? 4096 : 8192) - chains;
+  // (8192 waves are what the chip holds at once.  The gradients' second walk takes a few rounds
+  // of longer workgroups, into which the sequences' last, shorter runs have to fit: 648 us
+  // without room for them, 622 with it; forward it makes no difference)
+  const int64_t waves = backward ? 4096 - chains : 8192;
   // (a sequence of four times the mean is still whole)
   int64_t run = whole ? 4 * mean : (s.tokens * blocks + waves - 1) / waves;
   int64_t least = 24;
