@@ -594,7 +594,7 @@ def _arg(t, name: str, shape, dtypes, device, optional: bool = False):
     """The address of a tensor that passes ``_check`` (None of an optional one).
     These calls take some microseconds: what is checked is looked at once here,
     and ``_check`` finds the words where something is wrong."""
-    if type(t) is torch.Tensor and t.dtype in dtypes and t.device == device and \
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and \
             (shape is None or t.shape == shape) and t.is_cuda and t.is_contiguous():
         p = t.data_ptr()
         if p % 16 == 0:
@@ -853,7 +853,7 @@ def _rows_arg(t, name: str, shape, dtypes, device, size: int):
     """The address and the row stride (in elements) of a tensor whose rows (its last
     dimensions, ``shape`` being all of them) may be columns of a wider tensor.  It
     starts on a multiple of ``size`` bytes, and so does every row."""
-    if type(t) is torch.Tensor and t.dtype in dtypes and t.device == device and \
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and \
             t.shape == shape and t.is_cuda:
         p = t.data_ptr()
         stride = 0 if t.is_contiguous() else _row_stride(name, t.shape, t.stride())

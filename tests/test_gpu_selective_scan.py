@@ -262,3 +262,45 @@ def test_rows_more_than_2_31_elements_apart(ssd):
     dy = torch.randn_like(a[0])
     for s, t in zip(ssd.selective_scan_backward(*a, dy), ssd.selective_scan_backward(*b, dy)):
         assert (s is None and t is None) or same_bits(s, t)
+
+
+def test_more_than_2_31_elements(ssd):
+    """Two sequences, the second behind more than 2^31 elements of every row-shaped tensor:
+    what it gives alone, but for roundings (the calls cut it into other runs)."""
+    D, last, dt = 5120, 300, torch.bfloat16
+    T = (1 << 31) // D + 2 * last
+    g = torch.Generator(device=DEV).manual_seed(8)
+
+    def rows(*shape):
+        return torch.randn(1, T, *shape, generator=g, device=DEV, dtype=dt)
+
+    x, de, z, dy, B, C = rows(D), rows(D), rows(D), rows(D), rows(1, 8), rows(1, 8)
+    A = -torch.arange(1, 9, device=DEV).float().repeat(D, 1)
+    bias = torch.full((D,), -3.0, device=DEV)
+    ins = (x, de, A, B, C, bias, z, bias)
+    cu = torch.tensor([0, T - last, T], dtype=torch.int32, device=DEV)
+    tail = [t[:, -last:] if t.dim() > 2 else t for t in ins]
+    y, final = ssd.selective_scan(*ins, None, cu)
+    want, state = ssd.selective_scan(*tail)
+    assert _near(y[:, -last:], want) < 2 ** -8 and _near(final[1:], state) < 2 ** -16
+    del y
+    grads = ssd.selective_scan_backward(*ins, dy, None, None, cu)
+    wants = ssd.selective_scan_backward(*tail, dy[:, -last:].contiguous())
+    for i in (0, 1, 3, 4, 6):
+        assert _near(grads[i][:, -last:], wants[i]) < 2 ** -8, i
+        assert torch.isfinite(grads[i][:, :8]).all()
+
+
+def _near(got, want):
+    got, want = got.double(), want.double()
+    return float((got - want).norm() / want.norm())
+
+
+def test_parameters_are_tensors_too(ssd):
+    a = block_inputs(20)
+    b = [torch.nn.Parameter(t) if t.dim() < 3 else t for t in a]
+    with torch.no_grad():
+        for s, t in zip(ssd.selective_scan(*a), ssd.selective_scan(*b)):
+            assert same_bits(s, t)
+    with pytest.raises(ValueError, match="A requires a gradient"):
+        ssd.selective_scan(*b)
