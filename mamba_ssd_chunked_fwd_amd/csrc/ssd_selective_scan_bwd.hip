@@ -21,8 +21,8 @@
 // the middle: a token costs a lane 23 instructions for each of its 8 (state, channel) pairs, of
 // which 15 are the formula's, and per token and channel six DPP adds sum over four lanes; dB and
 // dC go through LDS, four tokens at a time, where the lanes of a wave add 8 vectors each.  (A
-// channel a lane with its sums over lanes by DPP alone: 2634 us for what takes 566 below.)  Nine
-// states of 2 x 4 values take 72 of the 256 registers of two waves a SIMD; decays of four of the
+// channel a lane with its sums over lanes by DPP alone: 2634 us for what takes 562 below.)  Nine
+// states of 2 x 4 values take 72 of the 256 registers of two waves a SIMD; decays of six of the
 // eight tokens wait in LDS, the others are formed again (one exponential costs two instructions).
 // Eight states a channel have two lanes a channel, more tokens of their own, and run at one wave
 // a SIMD (measured 737 us against 1125 at two, which spill).  Waves of a workgroup share B and C
@@ -30,7 +30,7 @@
 // 23, eight 680 and 8.
 //
 // Measured at 16384 tokens of 2560 channels of 16 states in bf16 (three sequences): first walk
-// 199 us (vector unit busy 87%), joining 17, second walk 566 (74%: two waves a SIMD do not cover
+// 202 us (vector unit busy 87%), joining 18, second walk 562 (74%: two waves a SIMD do not cover
 // LDS reads and barriers; B and C read a token ahead spill, 670), sums 13 + 6.  335 MB of marks
 // are written and read; at 5.15 TB/s all bytes of both walks take 330 us.
 #include "ssd_selective_scan.h"
@@ -276,6 +276,10 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
   constexpr int el = BF16 ? 2 : 4;
   __shared__ f32x4 bc_in[2][kMark][2][L];                 // B and C of a block
   __shared__ f32x4 values[kWaves][kBatch][2][kWave];      // dB and dC of each lane
+  // Decays that stay besides those that lie in `values`: of two more tokens 795 -> 783 us for
+  // 16 states and 1565 -> 1556 for 32; 64 leave no room for them.
+  constexpr int kMore = N == 64 ? 0 : 2;
+  __shared__ f32x4 more[kWaves][kMore ? kMore : 1][2][kWave];
   __shared__ f32x4 sums[2][kWaves][kMark][2][L];          // and of each wave
   __shared__ f32x4 start[kWaves][2][kWave];               // the state at the run's start
 
@@ -487,8 +491,8 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
     };
-    // The decays of the last tokens wait in LDS, where their dB and dC will lie; those of the
-    // first are formed again.
+    // The decays of the last tokens wait in LDS, of four where their dB and dC will lie; those
+    // of the first are formed again.
     auto up = [&](auto jj) {
       constexpr int j = decltype(jj)::value;
       const f32x4 B = bc_in[turn][j][0][q];
@@ -504,7 +508,10 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
           asm volatile("" : "+v"(v));      // (formed here, not where it is used)
           h[j + 1][c][n] = v;
         }
-        if (j >= kMark - kBatch) values[wave][j % kBatch][c][lane] = decay;
+        if constexpr (j >= kMark - kBatch)
+          values[wave][j % kBatch][c][lane] = decay;
+        else if constexpr (j >= kMark - kBatch - kMore)
+          more[wave][j - (kMark - kBatch - kMore)][c][lane] = decay;
       }
       fence();
     };
@@ -519,8 +526,10 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
       f32x4 vB, vC, decay[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (j >= kMark - kBatch) {
+        if constexpr (j >= kMark - kBatch) {
           decay[c] = values[wave][j % kBatch][c][lane];
+        } else if constexpr (j >= kMark - kBatch - kMore) {
+          decay[c] = more[wave][j - (kMark - kBatch - kMore)][c][lane];
         } else {
           float dl = La::template bcast<j % TURNS>(delta[i][c]);
           asm volatile("" : "+v"(dl));     // (its products are formed again, not kept)
