@@ -220,11 +220,16 @@ inline bool scan_step_grid_fits(const ScanShape& s) {
 }
 
 // ---- the convolution
-// Tokens of a run: enough runs for some 4000 waves, and of the gradients (whose runs
-// each leave a row of partial sums) no fewer than 64 tokens where that fills the chip.
+// Tokens of a run: enough runs to fill the chip, and no more than 64 tokens, from where on
+// rows read twice no longer count.  The gradients' runs, which go past their ends and leave a row
+// of partial sums each, are longer.  Measured in bf16: forward 16384 x 5376 78 us with runs of 32
+// to 64, 85 of 16, 84 of 96; gradients 124 with 32 to 64, 144 of 16, 128 of 96; 8192 x 2560
+// forward 18 to 19 with 12 to 24, gradients 33 with 24 to 32 and 37 with 20; 2048 x 2560 gradients
+// 20 with 8 to 16, 26 of 64.
 inline int64_t conv_run(const ConvShape& s, bool backward) {
   const int64_t waves = (s.dim + 64 * 8 - 1) / (64 * 8);
-  const int64_t run = s.tokens * waves / (backward ? 2048 : 4096);
+  int64_t run = s.tokens * waves / (backward ? 1400 : 4096);
+  if (backward) run = (run + 4) / 8 * 8;
   return run < 8 ? 8 : (run > 64 ? 64 : run);
 }
 inline int64_t conv_slots(const ConvShape& s, bool backward) {
