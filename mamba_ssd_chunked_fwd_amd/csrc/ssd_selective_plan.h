@@ -128,7 +128,7 @@ inline int64_t channel_blocks(const ScanShape& s) {
 // bf16: forward, 640 chains (8 x 2048 tokens) cut 507 us, whole 709; 1280 (16 x 1024) 523 and
 // 495; 2560 (32 x 1024) 1017 and 714.  Gradients: 1280 cut 1678, whole 2029; 2560 3380 and 3107.
 // Waves of the gradients' two walks (16384 x 2560): 2048 327 + 648 us, 4096 215 + 616, 6144 216 +
-// 617 and longer joins.
+// 617.
 inline int64_t scan_run(const ScanShape& s, bool backward) {
   const int64_t blocks = channel_blocks(s);
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
@@ -140,9 +140,11 @@ inline int64_t scan_run(const ScanShape& s, bool backward) {
   const int64_t waves = backward ? 4096 - chains : 8192;
   // (a sequence of four times the mean is still whole)
   int64_t run = whole ? 4 * mean : (s.tokens * blocks + waves - 1) / waves;
-  // (and more rounds of shorter ones are no slower: 16384 x 5120 in 1 to 5 sequences 1427 to 1562
-  // us with runs of 344, 1415 to 1440 with 144; 16384 x 2560 763 to 797 with 144 to 168)
-  if (backward && !whole && run > 144) run = 144;
+  // More rounds of shorter runs even out the shorter ones: gradients at 16384 x 5120 in 1 to 5
+  // sequences 1427 to 1562 us with runs of 344, 1415 to 1440 with 144; 16384 x 2560 763 to 797
+  // with 144 to 168.  Forward only where there are several sequences: 3 of 32768 tokens 978 with
+  // 320, 955 with 144, 16384 519 and 497; one of 32768 933 and 951.
+  if (!whole && run > 144 && (backward || s.nseq > 1)) run = 144;
   int64_t least = 24;
   if (!backward) {
     // Where there are waves for every SIMD in any case, a run's walk (0.36 us a token, twice)

@@ -21,7 +21,7 @@
 // the middle: a token costs a lane 23 instructions for each of its 8 (state, channel) pairs, of
 // which 15 are the formula's, and per token and channel six DPP adds sum over four lanes; dB and
 // dC go through LDS, four tokens at a time, where the lanes of a wave add 8 vectors each.  (A
-// channel a lane with its sums over lanes by DPP alone: 2634 us for what takes 562 below.)  Nine
+// channel a lane with its sums over lanes by DPP alone: 2634 us for what takes 538 below.)  Nine
 // states of 2 x 4 values take 72 of the 256 registers of two waves a SIMD; decays of six of the
 // eight tokens wait in LDS, the others are formed again (one exponential costs two instructions).
 // Eight states a channel have two lanes a channel, more tokens of their own, and run at one wave
@@ -30,8 +30,8 @@
 // 23, eight 680 and 8.
 //
 // Measured at 16384 tokens of 2560 channels of 16 states in bf16 (three sequences): first walk
-// 202 us (vector unit busy 87%), joining 18, second walk 562 (74%: two waves a SIMD do not cover
-// LDS reads and barriers; B and C read a token ahead spill, 670), sums 13 + 6.  335 MB of marks
+// 226 us (vector unit busy 87%), joining 19, second walk 538 (74%: two waves a SIMD do not cover
+// LDS reads and barriers; B and C read a token ahead spill, 670), sums 13 + 8.  335 MB of marks
 // are written and read; at 5.15 TB/s all bytes of both walks take 330 us.
 #include "ssd_selective_scan.h"
 
