@@ -32,7 +32,7 @@
 // Measured at 16384 tokens of 2560 channels of 16 states in bf16 (three sequences): first walk
 // 226 us (vector unit busy 87%), joining 19, second walk 538 (74%: two waves a SIMD do not cover
 // LDS reads and barriers; B and C read a token ahead spill, 670), sums 13 + 8.  335 MB of marks
-// are written and read; at 5.15 TB/s all bytes of both walks take 330 us.
+// are written and read; at 5.15 TB/s all bytes of both walks take 350 us.
 #include "ssd_selective_scan.h"
 
 #include "ssd_host.h"
