@@ -176,10 +176,11 @@ ssd_status ssd_selective_scan_step(const void *x, const void *dt, const float *A
  *     scales = max |y| / top        codes = the 8-bit value nearest to y top / max |y|
  * (ties to even), so that codes o scales stands for y.  codes [rows, dim] bytes;
  * scales [rows, dim/group] fp32; the rest as in ssd_add_norm_fwd.  All arithmetic is
- * in 64 bits, so a code is the nearest one but where the 64-bit value lies within some 1e-15
- * of a border.  A group of zeros (or of values below 1e-30) has codes of 0.  A
- * row that holds a value that is not finite has scales of NaN where its group does, as
- * ssd_add_norm_fwd's y would.  residual_out may be the same buffer as residual.
+ * in 64 bits, so a code is the nearest one but where the value lies within some 1e-15 of a
+ * border (on one, where the 64-bit products are exact, it is the even one).  A group of
+ * zeros (or of values below 1e-30) has codes of 0.  A row that holds a value that is not
+ * finite has scales of NaN where its group does, as ssd_add_norm_fwd's y would.
+ * residual_out may be the same buffer as residual.
  * Supported: dim up to 16384; group = dim, or 16, 32, 64, 128 or 256.
  */
 typedef enum { SSD_CODE_E4M3 = 0, SSD_CODE_INT8 = 1 } ssd_code;

@@ -2,6 +2,9 @@
 are equal (everything before them is formed in 64 bits; a value within 1e-10 of a border,
 where two 64-bit orders of summation may differ, may take either neighbour), scales are
 good to one rounding (2^-24), the stream to one rounding of its type."""
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -107,3 +110,26 @@ def test_leading_dimensions_and_wrong_arguments(ssd):
         ssd.add_norm_quant(x, group=8)
     with pytest.raises(ValueError):
         ssd.ssd_add_norm_quant_fwd(x, None, None, None, codes, scales[0], None)
+
+
+@pytest.mark.parametrize("code,top", [("e4m3", 448), ("int8", 127)])
+@pytest.mark.parametrize("group", [16, 80])
+def test_values_on_a_border_go_to_the_even_code(ssd, code, top, group):
+    """Rows of small whole numbers, whose quotients by the largest lie on borders again and
+    again: what exact fractions give."""
+    g = torch.Generator().manual_seed(group)
+    x = torch.randint(-24, 25, (300, 80), generator=g)
+    codes, scales, _ = ssd.add_norm_quant(x.to(torch.bfloat16).to(DEV), dtype=CODES[code],
+                                          group=group)
+    got, ties = dbl(codes).tolist(), 0
+    for row, values in enumerate(x.tolist()):
+        for at in range(0, 80, group):
+            most = max(abs(v) for v in values[at:at + group])
+            for i in range(at, at + group):
+                v = Fraction(top * values[i], most)
+                unit = Fraction(1)
+                if code == "e4m3" and v:
+                    unit = Fraction(2) ** (math.floor(math.log2(abs(v))) - 3)
+                ties += (v / unit) % 1 == Fraction(1, 2)
+                assert got[row][i] == float(round(v / unit) * unit), (row, i, v)
+    assert ties > 100

@@ -49,6 +49,9 @@ NAMED = [
     named(207, dim=320, N=64, lens=[40]),
     # (a chain long enough to have runs of more than 32 tokens)
     named(208, dim=8256, N=8, dt="bf16", lens=[60, 20, 0, 4]),
+    # (so many chains that the gradients' sequences are whole too, but for one of four times the mean)
+    named(209, dim=8256, N=8, dt="bf16", lens=[40, 0, 9, 130] + [17] * 13, before=1, after=2),
+    named(210, dim=4160, N=16, lens=[21] * 40, packed=False),
 ]
 
 
