@@ -999,7 +999,8 @@ def ssd_short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[to
 
 
 def _scan_args(x, dt, A, B, C, D, z, dt_bias, step: bool):
-    """The dims of a selective scan but nseq, and the addresses of its inputs."""
+    """The dims of a selective scan (of a prompt's, all but nseq), and the addresses of its
+    inputs."""
     lead = 1 if step else 2
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
         raise ValueError(f"x must be a tensor [batch, {'' if step else 'seqlen, '}dim]")
@@ -1007,17 +1008,19 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, step: bool):
         raise ValueError("A must be a tensor [dim, dstate]")
     if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
         raise ValueError(f"B must be a tensor [batch, {'' if step else 'seqlen, '}groups, dstate]")
-    dim, N, G, dev, own = x.shape[-1], A.shape[1], B.shape[-2], x.device, (x.dtype,)
-    el, bc = x.element_size(), x.shape[:-1] + (G, N)
-    px, xs = _rows_arg(x, "x", x.shape, _FLOATS, dev, el)
-    pdt, dts = _rows_arg(dt, "dt", x.shape, own, dev, el)
+    shape, dev, own, el = x.shape, x.device, (x.dtype,), x.element_size()
+    dim, N, G = shape[-1], A.shape[1], B.shape[-2]
+    bc = (*shape[:-1], G, N)
+    px, xs = _rows_arg(x, "x", shape, _FLOATS, dev, el)
+    pdt, dts = _rows_arg(dt, "dt", shape, own, dev, el)
     pB, bs = _rows_arg(B, "B", bc, own, dev, 4)
     pC, cs = _rows_arg(C, "C", bc, own, dev, 4)
-    pz, zs = (None, 0) if z is None else _rows_arg(z, "z", x.shape, own, dev, el)
-    return SelectiveScanDims(x.numel() // dim if dim else 0, 0, dim, N, G, xs, dts, zs, bs, cs), [
+    pz, zs = (None, 0) if z is None else _rows_arg(z, "z", shape, own, dev, el)
+    rows = shape[0] if step else shape[0] * shape[1]
+    return SelectiveScanDims(rows, rows, dim, N, G, xs, dts, zs, bs, cs), [
         px, pdt, _arg(A, "A", (dim, N), _F32, dev), pB, pC,
-        _arg(D, "D", (dim,), _F32, dev, True), pz,
-        _arg(dt_bias, "dt_bias", (dim,), _F32, dev, True)]
+        None if D is None else _arg(D, "D", (dim,), _F32, dev), pz,
+        None if dt_bias is None else _arg(dt_bias, "dt_bias", (dim,), _F32, dev)]
 
 
 def _scan_prompt_args(x, dt, A, B, C, D, z, dt_bias, init_state, cu_seqlens):
@@ -1102,7 +1105,6 @@ def ssd_selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
     updated in place and ``y`` [b, dim] written.  x, dt, z [b, dim], B, C [b, G, N]."""
     d, ins = _scan_args(x, dt, A, B, C, D, z, dt_bias, True)
     dev = x.device
-    d.nseq = d.tokens
     _call("ssd_selective_scan_step", dev, *ins,
           _arg(state, "state", (d.tokens, d.dim, d.dstate), _F32, dev),
           _arg(y, "y", x.shape, (x.dtype,), dev), int(softplus), _dtype_code(x.dtype), d)
