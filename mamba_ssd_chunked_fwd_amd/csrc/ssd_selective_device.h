@@ -8,22 +8,39 @@
 
 namespace ssd {
 
-// The run of `slot`: a 64-way search by the lanes of each wave.
-__device__ __forceinline__ Run find_run(const RunGrid& g, int slot) {
-  if (g.cu == nullptr) return equal_run(g, slot);
+// The last sequence of which `reached(begin, sequence)` holds (0 if there is none), where it holds
+// of all before one: a 64-way search by the lanes of each wave.
+template <class Reached>
+__device__ __forceinline__ int last_sequence(const RunGrid& g, Reached reached) {
   int lo = 0, hi = g.nseq;
   while (hi - lo > 1) {
     const int step = (hi - lo + kWave - 1) / kWave;
     const int64_t at = lo + (int64_t)step * (threadIdx.x % kWave);
     const int p = at < hi ? (int)at : hi - 1;
-    const bool reached = at < hi && first_slot(g, seq_bound(g, g.cu[p]), p) <= slot;
-    int n = __popcll(__ballot(reached));
+    int n = __popcll(__ballot(at < hi && reached(seq_bound(g, g.cu[p]), p)));
     n = __builtin_amdgcn_readfirstlane(n < 1 ? 1 : n);
     lo += step * (n - 1);
     if (lo > g.nseq - 1) lo = g.nseq - 1;
     hi = lo + step < hi ? lo + step : hi;
   }
-  return packed_run(g, slot, lo, seq_bound(g, g.cu[lo]), seq_bound(g, g.cu[lo + 1]));
+  return lo;
+}
+// The run of `slot`.
+__device__ __forceinline__ Run find_run(const RunGrid& g, int slot) {
+  if (g.cu == nullptr) return equal_run(g, slot);
+  const int seq = last_sequence(
+      g, [&](int begin, int i) { return first_slot(g, begin, i) <= slot; });
+  return packed_run(g, slot, seq, seq_bound(g, g.cu[seq]), seq_bound(g, g.cu[seq + 1]));
+}
+// The run that a scan's workgroups take at place `at`.
+__device__ __forceinline__ Run find_ordered_run(const RunGrid& g, int at) {
+  if (g.cu == nullptr || !firsts_lead(g)) return find_run(g, at);
+  int seq = at;
+  if (at >= g.nseq)
+    seq = last_sequence(
+        g, [&](int begin, int) { return (int)g.by_run.of((uint32_t)begin) <= at - g.nseq; });
+  const int begin = seq_bound(g, g.cu[seq]);
+  return packed_run(g, slot_at(g, at, seq, begin), seq, begin, seq_bound(g, g.cu[seq + 1]));
 }
 
 __device__ __forceinline__ float rcp_hw(float v) { return __builtin_amdgcn_rcpf(v); }

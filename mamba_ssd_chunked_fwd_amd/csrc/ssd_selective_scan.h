@@ -61,17 +61,17 @@ inline ScanArgs make_scan_args(const ScanInputs& in, const float* init, const Sc
   return a;
 }
 
-// The workgroup's 64 channels and its slot.
+// The workgroup's 64 channels and its place in the order of the slots.
 struct ScanPlace {
-  int slot, group, lanes;
+  int at, group, lanes;
   int64_t channel;
   __device__ __forceinline__ explicit ScanPlace(const ScanArgs& a) {
-    slot = (int)a.by_slot.of(blockIdx.x);
-    const uint32_t rest = blockIdx.x - (uint32_t)slot * a.by_slot.d;
+    at = (int)a.by_slot.of(blockIdx.x);
+    const uint32_t rest = blockIdx.x - (uint32_t)at * a.by_slot.d;
     group = (int)a.by_blocks.of(rest);
-    const int at = (int)(rest - (uint32_t)group * a.by_blocks.d) * kWave;
-    channel = (int64_t)group * a.group_dim + at;
-    lanes = a.group_dim - at < kWave ? a.group_dim - at : kWave;
+    const int first = (int)(rest - (uint32_t)group * a.by_blocks.d) * kWave;
+    channel = (int64_t)group * a.group_dim + first;
+    lanes = a.group_dim - first < kWave ? a.group_dim - first : kWave;
   }
 };
 

@@ -12,9 +12,9 @@
 //   - walks have no branch on what a call has (softplus, gate): both values are formed and one
 //     picked.  With branches, the compiler moved work across them and spilled (1471 -> 1190 us);
 //   - rows are read a block of four tokens ahead, B and C a piece of 32 bytes ahead;
-//   - sequences that do not fill the chip are cut into runs (scan_run).  A first walk leaves the
-//     state of every run but the last from zeros; the states at the runs' starts are then h =
-//     exp(A sum delta) h + left, joined by a launch of its own or, for few runs, by each run; the
+//   - sequences that do not fill the chip are cut into runs (scan_cut, scan_whole).  A first walk
+//     leaves the state of every run but the last from zeros; the states at the runs' starts are
+//     then h = exp(A sum delta) h + left, joined by a launch of its own or, for few runs, by each run; the
 //     second walk has the outputs.  The first walk may take a channel's states in slices, since
 //     nothing is summed over them (64 states: scan 439 -> 348 us).
 // Time sums are held in 64 bits, since every token rounds them again; all else is fp32.
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kWave, NS == 64 ? 2 : 1) void scan_kernel(const Sca
   load_states<NS>(a.in.A + d * N + n0, A2);
   const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
   const float skip = OUT && a.in.D ? a.in.D[d] : 0.0f;
-  const Run r = find_run(a.runs, pl.slot);
+  const Run r = find_ordered_run(a.runs, pl.at);
   if (!r.on) return;
   const bool last = r.index == r.count - 1;
   if (!OUT && last) return;
@@ -136,9 +136,9 @@ __global__ __launch_bounds__(kWave, NS == 64 ? 2 : 1) void scan_kernel(const Sca
   }
   if constexpr (OUT) {
     if (a.joined && r.count > 1) {
-      load_run<N>(a, pl.slot, d, h);
+      load_run<N>(a, r.slot, d, h);
     } else if (r.index > 0) {
-      fold_runs<N>(a, r.first, pl.slot, d, A2, h, [&](int64_t s, int n) {
+      fold_runs<N>(a, r.first, r.slot, d, A2, h, [&](int64_t s, int n) {
         return a.states[(s * N + n) * a.dim + d];
       });
     } else if (a.init != nullptr) {
@@ -222,8 +222,8 @@ __global__ __launch_bounds__(kWave, NS == 64 ? 2 : 1) void scan_kernel(const Sca
   if constexpr (OUT) {
     if (last && a.fin != nullptr) store_states<N>(a.fin + ((int64_t)r.seq * a.dim + d) * N, h);
   } else {
-    store_run<N>(a.states, a, pl.slot, d, n0, h);
-    a.totals[(int64_t)pl.slot * a.dim + d] = (float)total;
+    store_run<N>(a.states, a, r.slot, d, n0, h);
+    a.totals[(int64_t)r.slot * a.dim + d] = (float)total;
   }
 }
 
@@ -235,9 +235,9 @@ struct ScanPlan {
 
 ScanPlan make_plan(const ScanShape& s, const int32_t* cu) {
   ScanPlan p;
-  p.runs = make_run_grid(cu, s.tokens, s.nseq, scan_run(s, false));
+  p.runs = scan_grid(cu, s, false);
   p.slots = run_slots(p.runs);
-  p.split = cu != nullptr ? s.tokens > p.runs.run : p.runs.per_seq > 1;
+  p.split = cu != nullptr ? s.tokens > p.runs.whole : p.runs.per_seq > 1;
   p.blocks = channel_blocks(s);
   return p;
 }

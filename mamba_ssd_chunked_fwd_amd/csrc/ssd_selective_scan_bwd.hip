@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   float A2[NS], h[NS], decay[NS], back[NS];
   load_states<NS>(a.in.A + d * N + n0, A2);
   const float bias = a.in.dt_bias ? a.in.dt_bias[d] : 0.0f;
-  const Run r = find_run(a.runs, pl.slot);
+  const Run r = find_ordered_run(a.runs, pl.at);
   if (!r.on) return;
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
   Rows<BF16> rows(a, pl, r.begin, own, N, n0);
   const int64_t dy_step = a.dim * (BF16 ? 2 : 4);
   const char* dy = (const char*)b.dy + pl.channel * (BF16 ? 2 : 4) + r.begin * dy_step;
-  const int64_t mark0 = first_mark(r, pl.slot);
+  const int64_t mark0 = first_mark(r, r.slot);
   const int tokens = (int)(r.end - r.begin);
   typedef StateRows<NS, BF16, true> Bc;
   Bc bc(rows.B, rows.C, rows.b_step, rows.c_step, tokens);
@@ -164,9 +164,9 @@ __global__ __launch_bounds__(kWave) void scan_local_kernel(const BwdArgs b) {
     work(even, tokens - t);
     if (t + kBlock < tokens) load(even, tokens - t - kBlock);
   }
-  store_run<N>(a.states, a, pl.slot, d, n0, h);
-  store_run<N>(b.back, a, pl.slot, d, n0, back);
-  a.totals[(int64_t)pl.slot * a.dim + d] = (float)total;
+  store_run<N>(a.states, a, r.slot, d, n0, h);
+  store_run<N>(b.back, a, r.slot, d, n0, back);
+  a.totals[(int64_t)r.slot * a.dim + d] = (float)total;
 }
 
 // ---- the second walk, down the tokens
@@ -303,8 +303,8 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
   const ScanArgs& a = b.f;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave, q = lane % L;
-  const int64_t slot = b.by_wide_slot.of(blockIdx.x);
-  const uint32_t rest = blockIdx.x - (uint32_t)slot * b.by_wide_slot.d;
+  const int place_at = (int)b.by_wide_slot.of(blockIdx.x);
+  const uint32_t rest = blockIdx.x - (uint32_t)place_at * b.by_wide_slot.d;
   const int group = (int)b.by_wide.of(rest);
   const int block = (int)(rest - (uint32_t)group * b.by_wide.d);
   // the lane's channels; past the group's end they stand for nothing (zeros), and read the
@@ -315,7 +315,8 @@ __global__ __launch_bounds__(kWave * kWaves, N == 8 ? 1 : 2) void scan_bwd_kerne
   const int64_t d[2] = {base + (on[0] ? at : a.group_dim - (PAIRED ? 2 : 1)),
                         base + (on[1] ? at + 1 : a.group_dim - 1)};
 
-  const Run r = find_run(a.runs, (int)slot);
+  const Run r = find_ordered_run(a.runs, place_at);
+  const int64_t slot = r.slot;
   float* dA_row = b.dA_part + slot * (N + 2) * a.dim;
   if (!r.on || r.begin >= r.end) {
 #pragma unroll
@@ -761,7 +762,7 @@ int launch_scan_bwd(const ScanInputs& in, const float* init, const int32_t* cu, 
   BwdArgs b{};
   ScanArgs& a = b.f;
   a = make_scan_args(in, init, s, softplus);
-  a.runs = make_run_grid(cu, s.tokens, s.nseq, scan_run(s, true));
+  a.runs = scan_grid(cu, s, true);
   b.slots = run_slots(a.runs);
   a.joined = joins(a.runs);
   a.states = (float*)(base + l.states);
