@@ -104,6 +104,11 @@ ssd_status ssd_short_conv_step(const void *x, const float *weight, const float *
  * zeros; z NULL: no gate; final_state NULL: not stored.  final_state may be the same
  * buffer as init_state.  A is finite.  All arithmetic is fp32, y rounded once.
  *
+ * Decays are meant to be at most 1 (delta A <= 0).  Larger ones give what the recurrence gives
+ * while the product of any stretch of a sequence's decays stays below 2^127; where one passes
+ * it, results (and gradients) may be NaN even if every state stays finite, as one of 0 does: the
+ * products of whole runs of tokens are formed by themselves.
+ *
  * Supported: N in {8, 16, 32, 64}, dim up to 2^20, nseq below 2^22 and, with the blocks of
  * 64 channels that the groups have, nseq * blocks below some 2^26 (a launch has fewer than
  * 2^32 threads); anything else valid returns SSD_ERR_UNSUPPORTED.

@@ -1071,7 +1071,9 @@ def ssd_selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B
     exp(delta_t A) h_{t-1} + delta_t x_t B_t and y_t = (C_t . h_t + D x_t) silu(z_t).
     x, dt, z, y [b, L, dim], B and C [b, L, G, N] (fp32 or bf16; rows of the inputs may be
     columns of wider tensors), A [dim, N], D and dt_bias [dim] fp32, states
-    [sequences, dim, N] fp32; D, z, dt_bias and the states may be None.  With
+    [sequences, dim, N] fp32; D, z, dt_bias and the states may be None.  Decays are meant
+    to be at most 1 (delta A <= 0): where a product of larger ones over some tokens passes
+    2^127 results may be NaN.  With
     cu_seqlens [sequences + 1] int32 the sequences are packed in a batch of 1; else each
     batch row is one.  ``workspace`` has selective_scan_workspace_bytes(dims, dtype)
     bytes."""
