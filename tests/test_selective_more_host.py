@@ -1,10 +1,11 @@
 """Host-side checks of the selective scan (no GPU needed): the comparison of the parameters'
-gradients sees sums of fewer bits."""
+gradients sees sums of fewer bits, and the launch that joins runs has no registers in memory."""
 import pytest
 import torch
 
 import selective_ref as ref
 from test_gpu_selective_sums import SUMS
+from test_kernel_scratch_host import scratch  # noqa: F401
 
 
 def test_sums_in_fewer_bits_are_seen():
@@ -19,3 +20,9 @@ def test_sums_in_fewer_bits_are_seen():
     with pytest.raises(AssertionError):
         ref.check({"dA": low.float()}, {"dA": want}, {"dA": want}, SUMS)
     ref.check({"dA": want.float()}, {"dA": want}, {"dA": want}, SUMS)
+
+
+def test_scratch_of_the_join(scratch):  # noqa: F811
+    sizes = {n: s for n, s in scratch.items() if "scan_join_kernel" in n}
+    assert len(sizes) == 4                 # 8, 16, 32 and 64 states
+    assert max(sizes.values()) == 0, sizes
