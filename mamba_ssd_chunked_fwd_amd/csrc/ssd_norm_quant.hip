@@ -294,8 +294,9 @@ int launch_add_norm_quant(const void* x, const void* res, const float* scale, co
   const int vectors = (int)((dim + kVec - 1) / kVec);
   const int nv = vectors > kMaxWaves * kWave ? 2 : 1;
   const int waves = (vectors + nv * kWave - 1) / (nv * kWave);
-  // as many whole workgroups for each of the 256 CUs as its registers hold (20 waves)
-  const int64_t most = 256 * (waves > 20 ? 1 : 20 / waves);
+  // as many whole workgroups (of 1 to 16 waves) for each of the 256 CUs as its registers hold:
+  // 20 waves
+  const int64_t most = 256 * (20 / waves);
   const int blocks = (int)(rows < most ? rows : most);
   const bool grouped = group == 16 || group == 32 || group == 64 || group == 128 || group == 256;
   const bool whole = dim % kVec == 0;
