@@ -318,11 +318,9 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(const ConvArgs a) {
     if constexpr (V == 1) {
       row[k * a.dim] = k < W ? dw[k < W ? k : 0][0] : db[0];
     } else {
+      static_assert(V == 2, "channels of a lane");
       const float* v = k < W ? dw[k < W ? k : 0] : db;
-      if constexpr (V == 2)
-        *(f32x2*)(row + k * a.dim) = (f32x2){v[0], v[1]};
-      else
-        *(f32x4*)(row + k * a.dim) = (f32x4){v[0], v[1], v[2], v[3]};
+      *(f32x2*)(row + k * a.dim) = (f32x2){v[0], v[1]};
     }
   }
 }
