@@ -155,9 +155,9 @@ inline int64_t scan_cut(const ScanShape& s, bool backward) {
   int64_t run = (s.tokens * blocks + waves - 1) / waves;
   // More rounds of shorter runs even out the shorter ones: gradients at 16384 x 5120 in 1 to 5
   // sequences 1427 to 1562 us with runs of 344, 1415 to 1440 with 144; 16384 x 2560 763 to 797
-  // with 144 to 168.  Forward only where there are several sequences: 3 of 32768 tokens 978 with
-  // 320, 955 with 144, 16384 519 and 497; one of 32768 933 and 951.
-  if (run > 144 && (backward || s.nseq > 1)) run = 144;
+  // with 144 to 168.  Forward 32768 tokens in 3 sequences 978 with 320, 955 with 144, in one 976
+  // and 965; one of 65536 x 2560 1013 and 977, of 16384 x 5120 506 with 160 and 520.
+  if (run > 144) run = 144;
   // (very many sequences: gradients of 3000 x 2560 in 400, one of them of 2600 tokens, 343 us with
   // runs of 32, 362 with 64)
   const int64_t mean = (s.tokens + s.nseq - 1) / s.nseq;
