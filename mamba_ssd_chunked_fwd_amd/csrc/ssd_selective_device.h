@@ -50,9 +50,9 @@ __device__ __forceinline__ float sigmoid_f(float v) {
   return rcp_hw(1.0f + exp2_hw(-kLog2e * v));
 }
 
-// ln(1 + exp(v)) = max(v, 0) + ln(1 + e) with e = exp(-|v|), and
-// ln(1 + e) = 2 artanh(s) with s = e / (2 + e) <= 1/3: good to a few roundings of the
-// result for every v, also where it is small (1 + e would lose e's digits).  The
+// ln(1 + exp(v)) = max(v, 0) + ln(1 + e) with e = exp(-|v|), and ln(1 + e) = 2 artanh(s) with s =
+// e / (2 + e) <= 1/3: good to a few roundings of the result and of the exponent, |v| 2^-24 of it,
+// which count where v is far below zero (1 + e would lose all of e's digits there).  The
 // polynomial is artanh(s) / s in s^2, fitted to 4e-9 of it by weighted least squares.
 __device__ __forceinline__ float softplus_f(float v) {
   const float e = exp2_hw(-kLog2e * __builtin_fabsf(v));

@@ -116,10 +116,10 @@ SSD_BOTH Run packed_run(const RunGrid& g, int slot, int seq, int begin, int end)
 
 // Where some sequences stay whole and others are cut, a scan's workgroups take the first slots of
 // all sequences first, then the others: the whole ones are long workgroups among many whose slot
-// holds no run, and in the slots' order gathered on some of the SIMDs (16 sequences of 2048
-// tokens of 5120 channels 1726 us, in this order 985).  Place `at` < nseq is the first slot of sequence `at`;
-// place nseq + e is slot e + (the number of sequences that begin before the end of the tokens'
-// e'th `run`), of which `seq` is the last (0 if there is none).
+// holds no run, and in the slots' order gathered on some of the SIMDs (16 sequences of 2048 tokens
+// of 5120 channels 1726 us, in this order 985).  Place `at` < nseq is the first slot of sequence
+// `at`; place nseq + e is slot e + (the number of sequences that begin before the end of the
+// tokens' e'th `run`), of which `seq` is the last (0 if there is none).
 SSD_BOTH bool firsts_lead(const RunGrid& g) { return g.whole > g.run; }
 SSD_BOTH int slot_at(const RunGrid& g, int at, int seq, int begin) {
   if (at < g.nseq) return first_slot(g, begin, seq);
@@ -139,10 +139,11 @@ inline int64_t channel_blocks(const ScanShape& s) {
 }
 
 // A channel block of a sequence is a chain that one wave walks, and fewer than 1024 chains leave
-// SIMDs idle.  Runs that start from the states of those before them fill the chip, but cost a second walk
-// over all but each sequence's last one (forward), or longer joins (backward, where two walks are
-// made in any case).  The lengths of packed sequences are not known here: one of them may hold
-// almost all tokens, and any number be empty.  So a sequence is cut or not by its own length.
+// SIMDs idle.  Runs that start from the states of those before them fill the chip, but cost a
+// second walk over all but each sequence's last one (forward), or longer joins (backward, where
+// two walks are made in any case).  The lengths of packed sequences are not known here: one of
+// them may hold almost all tokens, and any number be empty.  So a sequence is cut or not by its
+// own length.
 
 // The tokens of a run of a sequence that is cut.
 inline int64_t scan_cut(const ScanShape& s, bool backward) {
@@ -177,11 +178,11 @@ inline int64_t scan_cut(const ScanShape& s, bool backward) {
 // The longest sequence that is walked whole: one whose chain ends about when all tokens do, as
 // equal sequences' do from 1280 chains on (gradients 2560).  Measured at 32768 tokens of 5120
 // channels of 16 states in bf16, in 13, 16, 20, 26 and 52 equal sequences: whole 1209, 982, 802,
-// 851 and 668 us, cut 960, 963, 957, 941 and 969; gradients in 26, 32, 52 and 64: whole 3650, 2984,
-// 3092 and 2769, cut 2920, 2969, 3001 and 3003; at 16384 x 2560 in 52 and 64 956 and 775 whole,
-// 916 and 902 cut.  One sequence with 90% of the tokens beside 12 to 127 others is cut: 900 to
-// 980 us and 2800 to 2970.  (Runs of four times the mean length, whatever that is, took it up to
-// 5880 and 6070.)
+// 851 and 668 us, cut 960, 963, 957, 941 and 969; gradients in 26, 32, 52 and 64: whole 3650,
+// 2984, 3092 and 2769, cut 2920, 2969, 3001 and 3003; at 16384 x 2560 in 52 and 64 956 and 775
+// whole, 916 and 902 cut.  One sequence with 90% of the tokens beside 12 to 127 others is cut: 900
+// to 980 us and 2800 to 2970.  (Runs of four times the mean length, whatever that is, took it up
+// to 5880 and 6070.)
 inline int64_t scan_whole(const ScanShape& s, bool backward) {
   const int64_t blocks = channel_blocks(s), unit = backward ? kMark : 4;
   const int64_t cut = scan_cut(s, backward), mean = (s.tokens + s.nseq - 1) / s.nseq;
@@ -287,15 +288,17 @@ inline bool scan_step_grid_fits(const ScanShape& s) {
 }
 
 // ---- the convolution
-// Tokens of a run: enough runs to fill the chip, and no more than 64 tokens, from where on
-// rows read twice no longer count.  The gradients' runs, which go past their ends and leave a row
-// of partial sums each, are longer.  Measured in bf16: forward 16384 x 5376 78 us with runs of 32
-// to 64, 85 of 16, 84 of 96; gradients 124 with 32 to 64, 144 of 16, 128 of 96; 8192 x 2560
-// forward 18 to 19 with 12 to 24, gradients 33 with 24 to 32 and 37 with 20; 2048 x 2560 gradients
-// 20 with 8 to 16, 26 of 64.
+// Tokens of a run: enough runs to fill the chip, and no more than 64 tokens, from where on rows
+// read twice no longer count.  The gradients' runs, which go past their ends and leave a row of
+// partial sums each, are longer.  `units` of 512 channels are two waves each forward and four in
+// the gradients (eight where rows do not start on whole vectors).  Measured in bf16, calls one
+// behind the other: forward 16384 x 5376 80 us with runs of 44, 81 of 32, 83 of 64, 87 of 16; 8192
+// x 2560 18.7 of 10, 17.5 of 16 to 32, 20.5 of 64.  Gradients 16384 x 5376 128 with 64, 129 of 32,
+// 131 of 96, 152 of 16; 8192 x 2560 33 with 32, 38 of 16, 37 of 64; 2048 x 2560 21 with 8 to 32,
+// 27 of 64.
 inline int64_t conv_run(const ConvShape& s, bool backward) {
-  const int64_t waves = (s.dim + 64 * 8 - 1) / (64 * 8);
-  int64_t run = s.tokens * waves / (backward ? 1400 : 4096);
+  const int64_t units = (s.dim + 511) / 512;
+  int64_t run = s.tokens * units / (backward ? 1400 : 4096);
   if (backward) run = (run + 4) / 8 * 8;
   return run < 8 ? 8 : (run > 64 ? 64 : run);
 }

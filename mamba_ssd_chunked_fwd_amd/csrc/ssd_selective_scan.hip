@@ -14,14 +14,16 @@
 //   - rows are read a block of four tokens ahead, B and C a piece of 32 bytes ahead;
 //   - sequences that do not fill the chip are cut into runs (scan_cut, scan_whole).  A first walk
 //     leaves the state of every run but the last from zeros; the states at the runs' starts are
-//     then h = exp(A sum delta) h + left, joined by a launch of its own or, for few runs, by each run; the
-//     second walk has the outputs.  The first walk may take a channel's states in slices, since
-//     nothing is summed over them (64 states: scan 439 -> 348 us).
+//     then h = exp(A sum delta) h + left, joined by a launch of its own or, for few runs, by each
+//     run; the second walk has the outputs.  The first walk may take a channel's states in
+//     slices, since nothing is summed over them (64 states: scan 439 -> 348 us).
 // Time sums are held in 64 bits, since every token rounds them again; all else is fp32.
 //
-// Measured at 32768 tokens of 5120 channels of 16 states in bf16: first walk 406 us, joining 19,
-// second walk 549 (vector unit busy all the time in both); one sequence cannot do with a single
-// walk: 80 waves for 1024 SIMDs.  Short calls: 643 tokens of 1536 channels 10 + 8 + 10.
+// Measured at one sequence of 32768 tokens of 5120 channels of 16 states in bf16 (means of the
+// profiler): first walk 407 us, joining 39, second walk 547 (vector unit busy all the time in both
+// walks); it cannot do with a single walk: 80 waves for 1024 SIMDs.  Short calls: 643 tokens of
+// 1536 channels 10 + 8 + 10.  64 states take two waves a SIMD, whose 256 registers lack 18 to
+// 27 for the outputs (76 bytes of scratch a lane); 32 and fewer fit.
 #include "ssd_selective_scan.h"
 
 #include "ssd_host.h"

@@ -17,22 +17,25 @@
 //
 // MI355X design.  All of it is bound by vector instructions, so the second walk is laid out for
 // few of them: sums over N states of a channel (dx, ddt, dz) want its states in one lane, sums
-// over a group's channels (dB, dC) want channels in one lane.  Four states of two channels are
-// the middle: a token costs a lane 23 instructions for each of its 8 (state, channel) pairs, of
-// which 15 are the formula's, and per token and channel six DPP adds sum over four lanes; dB and
-// dC go through LDS, four tokens at a time, where the lanes of a wave add 8 vectors each.  (A
-// channel a lane with its sums over lanes by DPP alone: 2634 us for what takes 538 below.)  Nine
-// states of 2 x 4 values take 72 of the 256 registers of two waves a SIMD; decays of six of the
-// eight tokens wait in LDS, the others are formed again (one exponential costs two instructions).
-// Eight states a channel have two lanes a channel, more tokens of their own, and run at one wave
-// a SIMD (measured 737 us against 1125 at two, which spill).  Waves of a workgroup share B and C
-// and their sums of dB and dC: four of them 622 us and 13 for the sums over blocks, two 606 and
-// 23, eight 680 and 8.
+// over a group's channels (dB, dC) want channels in one lane.  Four states of two channels are the
+// middle: a token costs a lane 24 instructions (an exponential counts for two) for each of its 8
+// (state, channel) pairs, of which 14 are the formula's: five for h, nine for R, its product with
+// the decay and what is summed.  Per token and channel six DPP adds sum over four lanes; dB and dC
+// go through LDS, four tokens at a time, where the lanes of a wave add 8 vectors each.  (A channel
+// a lane with its sums over lanes by DPP alone: 2634 us for what takes 533 below.)  Nine states of
+// 2 x 4 values take 72 of the 256 registers of two waves a SIMD; decays of six of the eight tokens
+// wait in LDS, the others are formed again (one exponential costs two instructions). Eight states
+// a channel have two lanes a channel, more tokens of their own, and run at one wave a SIMD
+// (measured 737 us against 1125 at two, which spill).  Waves of a workgroup share B and C and
+// their sums of dB and dC: four of them 622 us and 13 for the sums over blocks, two 606 and 23,
+// eight 680 and 8.
 //
-// Measured at 16384 tokens of 2560 channels of 16 states in bf16 (three sequences): first walk
-// 226 us (vector unit busy 87%), joining 19, second walk 538 (74%: two waves a SIMD do not cover
-// LDS reads and barriers; B and C read a token ahead spill, 670), sums 13 + 8.  335 MB of marks
-// are written and read; at 5.15 TB/s all bytes of both walks take 350 us.
+// Measured at 16384 tokens of 2560 channels of 16 states in bf16 (three sequences; means of the
+// profiler): first walk 222 us (vector unit busy 79%), joining 19, second walk 533 (78%: two waves
+// a SIMD do not cover LDS reads and barriers; B and C read a token ahead spill, 670), sums 13 + 8.
+// 335 MB of marks are written and read; at 5.15 TB/s all bytes of both walks take 350 us.  The
+// second walk's 256 registers lack four for 16 and 64 states (20 bytes of scratch a lane), and six
+// to 17 where channels are not read in pairs (28 to 72 bytes).
 #include "ssd_selective_scan.h"
 
 #include "ssd_host.h"
@@ -196,7 +199,8 @@ struct Lanes {
     if (L >= 16) v += moved<kRowRor8>(v);
     return v;
   }
-  // Of several values at once (one after the other 781 us, where this takes 777).
+  // Of several values at once (the call at 16384 x 2560 x 16: one after the other 806 to 808 us
+  // in five rounds, this 802 to 804).
   template <int K>
   static __device__ __forceinline__ void sum(float (&v)[K]) {
 #pragma unroll

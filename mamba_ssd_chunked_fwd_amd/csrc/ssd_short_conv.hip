@@ -7,15 +7,16 @@
 // A lane owns neighbouring channels and goes along a run of tokens with the last W - 1 rows in
 // registers, so every row is read once (and W - 1 again at a run's start); the taps stay in
 // registers.  Rows of a block of four tokens are on the way while another is worked on.  Runs
-// (conv_run) are as long as some 4000 waves allow: runs of 64 read 5% again, and the gradients'
-// leave as few rows of partial sums of dweight and dbias as that (added by a kernel of their own
-// in a fixed order).  The gradients finish a row of dx W - 1 tokens later, so their runs go W - 1
-// tokens past their end and form those tokens' pre-activations again.  Sums are fp32, each output
-// rounded once.
+// (conv_run) are as long as some 8000 waves allow, the gradients' as some 5600: runs of 64 read 5%
+// again, and the gradients' leave as few rows of partial sums of dweight and dbias as that (added
+// by a kernel of their own in a fixed order).  The gradients finish a row of dx W - 1 tokens
+// later, so their runs go W - 1 tokens past their end and form those tokens' pre-activations
+// again.  Sums are fp32, each output rounded once.
 //
-// Measured at 16384 x 5376 in bf16, 4 taps: forward 77 us (352 MB: 4.6 TB/s), gradients 127 (529
-// MB: 4.2), sums 7; a device copy moves 5.15 TB/s.  One token of 200 sequences of 5376 channels
-// 6.5 us.
+// Measured at 16384 x 5376 in bf16, 4 taps, calls one behind the other: forward 80 us (353 MB: 4.4
+// TB/s), gradients with their sums 128 (529 MB: 4.1), in fp32 153 (705 MB: 4.6) and 234 (1057 MB:
+// 4.5); a device copy moves 5.15 TB/s.  (Under the profiler, apart: 78, 132 and 8.)  One token of
+// 200 sequences of 5376 channels 6.5 us.
 #include "ssd_host.h"
 #include "ssd_selective_device.h"
 #include "ssd_selective_launch.h"
@@ -395,8 +396,9 @@ ConvGrid conv_grid(const ConvShape& s, int V) {
   return g;
 }
 
-// Channels of a lane.  Measured at 16384 x 5376 in bf16: forward 8 channels 79 us, 4 72 us
-// (126 registers and 16-byte loads against 60 and 8); gradients 8 171, 4 132, 2 123.
+// Channels of a lane.  Kernels of an earlier form against each other, 16384 x 5376 in bf16:
+// forward 8 channels 79 us, 4 72 us (126 registers and 16-byte loads against 60 and 8); gradients
+// 8 171, 4 132, 2 123.
 constexpr int kFwdVec = 4, kBwdVec = 2;
 
 // f(std::integral_constant W, bool BF16, int V, bool SILU) as types.
